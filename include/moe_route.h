@@ -63,6 +63,8 @@ extern "C" {
 #define MOE_MAX_EXPERTS 64
 #define MOE_MAX_TOPK 8
 #define MOE_MAX_LORE_RANK 64
+#define MOE_DISTILL_MAX_CLASSES (1 << 18) /* moe_distill_topk: V at most this          */
+#define MOE_DISTILL_MAX_TOP 1024         /* moe_distill_topk: K at most this          */
 #define MOE_FLOE_MAX_DIM 16384 /* MOE_MODE_FLOE: inter and hidden at most this */
 /* Scratch bytes per GPU of moe_layer_forward_noalloc (128 MiB). */
 #define MOE_NOALLOC_SCRATCH_BYTES ((size_t)128 << 20)
@@ -394,6 +396,116 @@ moe_status_t moe_layer_forward_noalloc(const moe_dims_t* dims, int32_t T, const 
                                        const moe_weights_t* w, const uint64_t* resident,
                                        int64_t resident_stride, moe_mode_t mode, void* out,
                                        void* stream);
+
+/* ---- Training: tokens sorted by expert and back, the router's gradient, and
+ * distillation of a router from another's top choices
+ *
+ * With these a layer can be trained around a caller's own expert products:
+ * moe_route and moe_permute give the weights and the sorted positions,
+ * moe_dispatch the sorted rows, moe_undispatch brings the experts' rows back;
+ * moe_undispatch_backward and moe_undispatch give the gradients of the rows,
+ * the weights and the hidden states, moe_route_backward takes the weights'
+ * gradient on to the router.  moe_distill_topk trains a prefetch router
+ * toward the router's choices [APEX page, Sec. 4.1] (or any student toward a
+ * teacher's top logits).
+ *
+ * No output may overlap another buffer of the call, except where an input is
+ * named as the output itself (the same address): MOE_EINVAL.  Sums run in
+ * fp32 (moe_distill_topk: the teacher's entries in 64 bits) in a fixed order,
+ * so results are bitwise reproducible.  Shape limits are those of the head of
+ * this file, but the intermediate sizes do not count: T * k * hidden < 2^31
+ * and T <= 2^22.  Results depend on no state between calls; two captured
+ * graphs need a workspace each when they can run at the same time.  T = 0
+ * enqueues nothing (but see moe_route_backward), and no buffer is looked at. */
+
+/* Rows sorted by expert: x_perm[inv[t*k+j]] = x[t] for every slot with inv in
+ * 0..T*k-1 (moe_permute; other slots are skipped).  x [T][H], x_perm [T*k][H]
+ * dtype.  Rows that no slot names are left as they were.  The gradient is
+ * moe_undispatch with topk_w_opt = NULL. */
+moe_status_t moe_dispatch(const moe_dims_t* dims, int32_t T, const void* x, const int32_t* inv,
+                          void* x_perm, void* stream);
+
+/* The way back: out[t] = add[t] + sum_j w_tj y_perm[inv[t*k+j]] over the slots
+ * with inv in 0..T*k-1, summed in fp32 in slot order and rounded once.
+ *   y_perm [T*k][H] of row_dtype: dims.dtype, or MOE_F32 for a bf16 layer
+ *     (moe_expert_ffn's rows); rows that no slot names are not read.
+ *   topk_w_opt [T*k] fp32; NULL: every weight is 1 (the gradient of
+ *     moe_dispatch).  add_opt [T][H] dtype: NULL, a buffer, or out itself.
+ *   A token without any such slot gets add[t], or 0. */
+moe_status_t moe_undispatch(const moe_dims_t* dims, int32_t T, const void* y_perm,
+                            moe_dtype_t row_dtype, const int32_t* inv, const float* topk_w_opt,
+                            const void* add_opt, void* out, void* stream);
+
+/* Gradient of moe_undispatch with weights, dout [T][H] dtype:
+ *   dy_perm[inv[t*k+j]] = w_tj dout[t] (row_dtype; rows that no slot names are
+ *     left as they were); needs topk_w.
+ *   dtopk_w[t*k+j] = <dout[t], y_perm[inv[t*k+j]]> in fp32, 0 for a slot
+ *     without a row; needs y_perm.
+ * Either output may be NULL, not both (MOE_EINVAL).  The gradient of add is
+ * dout. */
+moe_status_t moe_undispatch_backward(const moe_dims_t* dims, int32_t T, const void* dout,
+                                     const void* y_perm_opt, moe_dtype_t row_dtype,
+                                     const int32_t* inv, const float* topk_w_opt,
+                                     void* dy_perm_opt, float* dtopk_w_opt, void* stream);
+
+/* Bytes of workspace moe_route_backward needs for dw_router (host output). */
+moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* bytes /* host */);
+
+/* Gradient of the router l = x W_r^T and of moe_route's weights:
+ *   dlogits [T][E] fp32 = (d topk_w / d logits)^T dtopk_w + dlogits_add, for
+ *     topk_w = p_e (softmax over all E), or p_e / sum over the slots' experts
+ *     when dims.renormalize; the choice of experts is held fixed.
+ *   dx [T][H] dtype = dx_add + dlogits W_r, rounded once.
+ *   dw_router [E][H] fp32 = dlogits^T x, added to what it holds when
+ *     accumulate_dw is 1 (0: overwritten; any other value is MOE_EINVAL).
+ * topk_ids [T][k] and logits [T][E] are moe_route's; ids outside 0..E-1 are
+ * skipped, an expert named twice counts twice.  dtopk_w_opt NULL: only
+ * dlogits_add counts (a given gradient of the logits, such as
+ * moe_distill_topk's; topk_ids and logits may then be NULL).  One of the two
+ * must be given.  dlogits_add_opt may be dlogits itself, dx_add_opt dx itself.
+ * dx_opt needs w_router, dw_router_opt needs x and ws
+ * (moe_route_backward_size); either may be NULL.  T = 0 clears dw_router
+ * unless it accumulates, and enqueues nothing else. */
+moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x_opt,
+                                const void* w_router_opt, const int32_t* topk_ids_opt,
+                                const float* logits_opt, const float* dtopk_w_opt,
+                                const float* dlogits_add_opt, float* dlogits,
+                                const void* dx_add_opt, void* dx_opt, float* dw_router_opt,
+                                int32_t accumulate_dw, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace moe_distill_topk needs (host output; may be 0). */
+moe_status_t moe_distill_topk_size(int32_t T, int32_t V, size_t* bytes /* host */);
+
+/* Distillation from a teacher's top logits, forward and backward.  Per row t,
+ * z = student[t] / temperature over the V classes, q = softmax(z), the
+ * teacher's K entries (id_k, u_k):
+ *   teacher_lse_opt NULL: p = softmax over the K entries of u / temperature,
+ *     KL = sum_k p_k (log p_k - log q_{id_k});
+ *   teacher_lse_opt [T] fp32, the log-sum-exp of all of the teacher's logits
+ *     over temperature: p_k = exp(u_k / temperature - lse), and the mass left,
+ *     p_T = max(0, 1 - sum p), stands against the classes that the K do not
+ *     name as one class, q_T = the sum of their q:
+ *     KL += p_T (log p_T - log q_T) (left out when the K name all classes).
+ *   loss [T] fp32 = scale * token_w[t] * KL (token_w_opt NULL: 1).
+ *   dstudent_opt [T][ld] of the student's dtype = d loss[t] / d student[t],
+ *     rounded once; NULL: the loss alone; the student's buffer itself is
+ *     allowed.  Columns V..ld-1 are neither read nor written.
+ * student [T][ld] dtype, ld >= V (rows need not be aligned); teacher_ids and
+ * teacher_logits [T][K].  Entries with an id outside 0..V-1 are skipped; a
+ * class named twice has both entries' mass.  A row with token_w = 0 is not
+ * read: loss and gradient 0; so are those of a row without an entry (no lse:
+ * one whose entries all have logit -inf, too).  A student logit of -inf has q = 0: its
+ * gradient is -p, and the loss is +inf where p > 0; a row of them only, and a
+ * NaN, gives NaN.
+ * Limits: V <= MOE_DISTILL_MAX_CLASSES, K <= MOE_DISTILL_MAX_TOP, ld <= 2^31,
+ * T <= 2^22, 2^-20 <= temperature <= 2^20 (MOE_EUNSUPPORTED); a temperature
+ * that is not positive and finite, or a scale that is not finite: MOE_EINVAL. */
+moe_status_t moe_distill_topk(int32_t T, int32_t V, int64_t ld, int32_t K, const void* student,
+                              moe_dtype_t dtype, const int32_t* teacher_ids,
+                              const float* teacher_logits, const float* teacher_lse_opt,
+                              const float* token_w_opt, float temperature, float scale,
+                              float* loss, void* dstudent_opt, void* ws, size_t ws_bytes,
+                              void* stream);
 
 /* ---- Exact execution of missed experts on the host or after a fetch ------
  * [SPICE page, "CPU-GPU collaboration: handling prefetch misses", cost rule

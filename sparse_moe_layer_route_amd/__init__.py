@@ -10,4 +10,6 @@ from .binding import (  # noqa: F401
     MoeOffloadCost, MoeOffloadStats, OFFLOAD_NONE, OFFLOAD_FETCH, OFFLOAD_HOST, offload_cost,
     moe_offload_plan, moe_offload_workspace_size, moe_host_ffn_workspace_size,
     moe_host_expert_ffn, moe_layer_forward_offload,
+    moe_dispatch, moe_undispatch, moe_undispatch_backward, moe_route_backward_size,
+    moe_route_backward, moe_distill_topk_size, moe_distill_topk,
 )

@@ -108,6 +108,14 @@ def _load():
         "moe_combine": ([D, I32, P, P, P, P, P, P, P, P, P], ctypes.c_int),
         "moe_layer_forward": ([D, I32, P, Wp, P, I64, ctypes.c_int, P, Dbg, P, SZ, P], ctypes.c_int),
         "moe_layer_forward_noalloc": ([D, I32, P, Wp, P, I64, ctypes.c_int, P, P], ctypes.c_int),
+        "moe_dispatch": ([D, I32, P, P, P, P], ctypes.c_int),
+        "moe_undispatch": ([D, I32, P, ctypes.c_int, P, P, P, P, P], ctypes.c_int),
+        "moe_undispatch_backward": ([D, I32, P, P, ctypes.c_int, P, P, P, P, P], ctypes.c_int),
+        "moe_route_backward_size": ([D, I32, ctypes.POINTER(SZ)], ctypes.c_int),
+        "moe_route_backward": ([D, I32, P, P, P, P, P, P, P, P, P, P, I32, P, SZ, P], ctypes.c_int),
+        "moe_distill_topk_size": ([I32, I32, ctypes.POINTER(SZ)], ctypes.c_int),
+        "moe_distill_topk": ([I32, I32, I64, I32, P, ctypes.c_int, P, P, P, P, ctypes.c_float,
+                              ctypes.c_float, P, P, P, SZ, P], ctypes.c_int),
         "moe_offload_plan": ([D, P, P, ctypes.POINTER(MoeOffloadCost), P], ctypes.c_int),
         "moe_offload_workspace_size": ([D, I32, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
                                        ctypes.c_int),
@@ -129,7 +137,9 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_workspace_size", "moe_r
             "moe_prefetch_mask", "moe_prefetch_adaptive", "moe_pack_size", "moe_pack_weights",
             "moe_permute", "moe_floe_predict", "moe_floe_pack", "moe_lore_targets",
             "moe_lore_fit_size", "moe_lore_fit", "moe_expert_ffn", "moe_lore_surrogate",
-            "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_offload_plan",
+            "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_dispatch",
+            "moe_undispatch", "moe_undispatch_backward", "moe_route_backward_size",
+            "moe_route_backward", "moe_distill_topk_size", "moe_distill_topk", "moe_offload_plan",
             "moe_offload_workspace_size", "moe_host_ffn_workspace_size", "moe_host_expert_ffn",
             "moe_layer_forward_offload")
 
@@ -359,6 +369,124 @@ def moe_layer_forward_noalloc(dims, T, x, weights, resident, resident_stride, mo
                                           ctypes.byref(ws_struct), _ptr(resident), resident_stride,
                                           _mode(mode), _ptr(out), _stream(stream)),
            "moe_layer_forward_noalloc")
+
+
+# ---------------------------------------------------------------- training --
+_TORCH_DTYPES = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+_MOE_DTYPES = {v: k for k, v in _TORCH_DTYPES.items()}
+
+
+def _arg(name, t, n, dtype, optional=False):
+    """Address of a device tensor of at least n elements of `dtype` on the
+    current device (where the stream is); None where optional."""
+    if t is None and optional:
+        return None
+    p = _ptr(t) if t is not None else None
+    if p is None:
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} lives on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return p
+
+
+def _row_dtype(t):
+    if t is None:
+        raise TypeError("expected a torch.Tensor")
+    if t.dtype not in _MOE_DTYPES:
+        raise TypeError(f"expected float32 or bfloat16 rows, got {t.dtype}")
+    return _MOE_DTYPES[t.dtype]
+
+
+def _ws(ws):
+    return (None, 0) if ws is None or ws.numel() == 0 else (_arg("ws", ws, 0, torch.uint8), ws.numel())
+
+
+def moe_dispatch(dims, T, x, inv, x_perm, stream=None):
+    d = _dims(dims)
+    dt, P = _TORCH_DTYPES[d.dtype], T * d.top_k
+    _check(_lib.moe_dispatch(ctypes.byref(d), T, _arg("x", x, T * d.hidden, dt),
+                             _arg("inv", inv, P, torch.int32),
+                             _arg("x_perm", x_perm, P * d.hidden, dt), _stream(stream)),
+           "moe_dispatch")
+
+
+def moe_undispatch(dims, T, y_perm, inv, topk_w, out, add=None, stream=None):
+    """topk_w None: every weight is 1 (the gradient of moe_dispatch)."""
+    d = _dims(dims)
+    dt, P, H = _TORCH_DTYPES[d.dtype], T * d.top_k, d.hidden
+    row = _row_dtype(y_perm)
+    _check(_lib.moe_undispatch(ctypes.byref(d), T, _arg("y_perm", y_perm, P * H, y_perm.dtype), row,
+                               _arg("inv", inv, P, torch.int32),
+                               _arg("topk_w", topk_w, P, torch.float32, True),
+                               _arg("add", add, T * H, dt, True), _arg("out", out, T * H, dt),
+                               _stream(stream)), "moe_undispatch")
+
+
+def moe_undispatch_backward(dims, T, dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=None):
+    """dy_perm or dtopk_w may be None (then topk_w or y_perm may be too)."""
+    d = _dims(dims)
+    dt, P, H = _TORCH_DTYPES[d.dtype], T * d.top_k, d.hidden
+    rows = y_perm if y_perm is not None else dy_perm
+    row = _row_dtype(rows)
+    _check(_lib.moe_undispatch_backward(
+        ctypes.byref(d), T, _arg("dout", dout, T * H, dt),
+        _arg("y_perm", y_perm, P * H, rows.dtype, True), row, _arg("inv", inv, P, torch.int32),
+        _arg("topk_w", topk_w, P, torch.float32, True),
+        _arg("dy_perm", dy_perm, P * H, rows.dtype, True),
+        _arg("dtopk_w", dtopk_w, P, torch.float32, True), _stream(stream)),
+        "moe_undispatch_backward")
+
+
+def moe_route_backward_size(dims, T) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_route_backward_size(ctypes.byref(_dims(dims)), T, ctypes.byref(n)),
+           "moe_route_backward_size")
+    return n.value
+
+
+def moe_route_backward(dims, T, x, w_router, topk_ids, logits, dtopk_w, dlogits, dx, dw_router, ws,
+                       dlogits_add=None, dx_add=None, accumulate_dw=False, stream=None):
+    d = _dims(dims)
+    dt, f32, P, H, E = _TORCH_DTYPES[d.dtype], torch.float32, T * d.top_k, d.hidden, d.n_experts
+    ws_p, ws_n = _ws(ws)
+    _check(_lib.moe_route_backward(
+        ctypes.byref(d), T, _arg("x", x, T * H, dt, True),
+        _arg("w_router", w_router, E * H, dt, True),
+        _arg("topk_ids", topk_ids, P, torch.int32, True), _arg("logits", logits, T * E, f32, True),
+        _arg("dtopk_w", dtopk_w, P, f32, True), _arg("dlogits_add", dlogits_add, T * E, f32, True),
+        _arg("dlogits", dlogits, T * E, f32), _arg("dx_add", dx_add, T * H, dt, True),
+        _arg("dx", dx, T * H, dt, True), _arg("dw_router", dw_router, E * H, f32, True),
+        int(accumulate_dw), ws_p, ws_n, _stream(stream)), "moe_route_backward")
+
+
+def moe_distill_topk_size(T, V) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_distill_topk_size(T, V, ctypes.byref(n)), "moe_distill_topk_size")
+    return n.value
+
+
+def moe_distill_topk(T, V, K, student, teacher_ids, teacher_logits, loss, dstudent=None, ws=None,
+                     teacher_lse=None, token_w=None, temperature=1.0, scale=1.0, ld=None,
+                     stream=None):
+    """ld: elements from one row of student (and dstudent) to the next; None:
+    the length of student's last axis."""
+    row = _row_dtype(student)
+    ld = student.shape[-1] if ld is None else int(ld)
+    n = (T - 1) * ld + V if T > 0 else 0
+    ws_p, ws_n = _ws(ws)
+    _check(_lib.moe_distill_topk(
+        T, V, ld, K, _arg("student", student, n, student.dtype), row,
+        _arg("teacher_ids", teacher_ids, T * K, torch.int32),
+        _arg("teacher_logits", teacher_logits, T * K, torch.float32),
+        _arg("teacher_lse", teacher_lse, T, torch.float32, True),
+        _arg("token_w", token_w, T, torch.float32, True), float(temperature), float(scale),
+        _arg("loss", loss, T, torch.float32), _arg("dstudent", dstudent, n, student.dtype, True),
+        ws_p, ws_n, _stream(stream)), "moe_distill_topk")
 
 
 # ------------------------------------------------- exact miss execution --

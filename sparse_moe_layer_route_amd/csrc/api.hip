@@ -73,6 +73,24 @@ hipError_t launch_combine_rows(const moe_dims_t& d, int T, const void* y_perm, b
 hipError_t launch_lore(const moe_dims_t& d, int T, const void* x, const int32_t* ids,
                        const uint8_t* exact, const void* lore_A, const void* lore_B,
                        float* lore_out, hipStream_t s);
+hipError_t launch_dispatch(const moe_dims_t& d, int T, const void* x, const int32_t* inv,
+                           void* x_perm, hipStream_t s);
+hipError_t launch_undispatch(const moe_dims_t& d, int T, const void* y_perm, bool rows_bf16,
+                             const int32_t* inv, const float* topk_w, const void* add, void* out,
+                             hipStream_t s);
+hipError_t launch_undispatch_backward(const moe_dims_t& d, int T, const void* dout,
+                                      const void* y_perm, bool rows_bf16, const int32_t* inv,
+                                      const float* topk_w, void* dy, float* dw, hipStream_t s);
+int64_t route_backward_ws_bytes(const moe_dims_t& d, int T);
+hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, const void* w_router,
+                                 const int32_t* ids, const float* logits, const float* dtopk_w,
+                                 const float* dlogits_add, float* dlogits, const void* dx_add,
+                                 void* dx, float* dw, int accumulate, void* ws, hipStream_t s);
+int64_t distill_ws_bytes(int T, int V);
+hipError_t launch_distill(int T, int V, int64_t ld, int K, const void* student, bool is_bf16,
+                          const int32_t* ids, const float* t_logits, const float* t_lse,
+                          const float* token_w, float tau, float scale, float* loss,
+                          void* dstudent, void* ws, hipStream_t s);
 int floe_slices(int n_keep);
 int floe_max_inter();
 int floe_max_hidden();
@@ -107,6 +125,11 @@ inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
 inline bool ok_opt(const void* p) { return p == nullptr || aligned16(p); }
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+// Whether two buffers share a byte (a null one shares none).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  return a && b && a0 < b0 + nb && b0 < a0 + na;
+}
 
 moe_status_t check_dims(const moe_dims_t* d) {
   if (!d) return MOE_EINVAL;
@@ -572,6 +595,182 @@ moe_status_t moe_combine(const moe_dims_t* dims, int32_t T, const float* y_perm,
   return hip_status(launch_combine(*dims, T, y_perm, inv, topk_w, exact, nullptr, y_shared,
                                    shared_gate, lore_out, nullptr, nullptr, nullptr, out,
                                    (hipStream_t)stream));
+}
+
+// ---- training: tokens sorted by expert and back, router gradient, distillation
+
+namespace {
+
+inline size_t dtype_bytes(moe_dtype_t t) { return t == MOE_BF16 ? 2 : 4; }
+
+// Sorted rows hold T * top_k * hidden elements, indexed below 2^31; the
+// intermediate sizes play no part here.
+inline bool rows_fit(const moe_dims_t& d, int64_t T) {
+  return T <= kMaxTokens && T * d.top_k * d.hidden < (int64_t(1) << 31);
+}
+
+moe_status_t check_rows(const moe_dims_t* d, int32_t T, moe_dtype_t row_dtype) {
+  const moe_status_t st = check_dims(d);
+  if (st != MOE_OK) return st;
+  if (T < 0 || (row_dtype != MOE_F32 && row_dtype != MOE_BF16)) return MOE_EINVAL;
+  if (d->dtype == MOE_F32 && row_dtype == MOE_BF16) return MOE_EUNSUPPORTED;
+  return rows_fit(*d, T) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+}  // namespace
+
+moe_status_t moe_dispatch(const moe_dims_t* dims, int32_t T, const void* x, const int32_t* inv,
+                          void* x_perm, void* stream) {
+  const moe_status_t st = check_rows(dims, T, dims ? dims->dtype : MOE_F32);
+  if (st != MOE_OK || T == 0) return st;
+  if (!ok_ptr(x) || !ok_ptr(inv) || !ok_ptr(x_perm)) return MOE_EINVAL;
+  const size_t P = (size_t)T * dims->top_k, xb = (size_t)T * dims->hidden * dtype_bytes(dims->dtype);
+  const size_t rb = xb * dims->top_k;
+  if (overlap(x_perm, rb, x, xb) || overlap(x_perm, rb, inv, P * 4)) return MOE_EINVAL;
+  return hip_status(launch_dispatch(*dims, T, x, inv, x_perm, (hipStream_t)stream));
+}
+
+moe_status_t moe_undispatch(const moe_dims_t* dims, int32_t T, const void* y_perm,
+                            moe_dtype_t row_dtype, const int32_t* inv, const float* topk_w_opt,
+                            const void* add_opt, void* out, void* stream) {
+  const moe_status_t st = check_rows(dims, T, row_dtype);
+  if (st != MOE_OK || T == 0) return st;
+  if (!ok_ptr(y_perm) || !ok_ptr(inv) || !ok_opt(topk_w_opt) || !ok_opt(add_opt) || !ok_ptr(out))
+    return MOE_EINVAL;
+  const size_t P = (size_t)T * dims->top_k, H = dims->hidden;
+  const size_t ob = (size_t)T * H * dtype_bytes(dims->dtype);
+  if (overlap(out, ob, y_perm, P * H * dtype_bytes(row_dtype)) || overlap(out, ob, inv, P * 4) ||
+      overlap(out, ob, topk_w_opt, P * 4) || (add_opt != out && overlap(out, ob, add_opt, ob)))
+    return MOE_EINVAL;
+  return hip_status(launch_undispatch(*dims, T, y_perm, row_dtype == MOE_BF16, inv, topk_w_opt,
+                                      add_opt, out, (hipStream_t)stream));
+}
+
+moe_status_t moe_undispatch_backward(const moe_dims_t* dims, int32_t T, const void* dout,
+                                     const void* y_perm_opt, moe_dtype_t row_dtype,
+                                     const int32_t* inv, const float* topk_w_opt,
+                                     void* dy_perm_opt, float* dtopk_w_opt, void* stream) {
+  const moe_status_t st = check_rows(dims, T, row_dtype);
+  if (st != MOE_OK || T == 0) return st;
+  if (!ok_ptr(dout) || !ok_opt(y_perm_opt) || !ok_ptr(inv) || !ok_opt(topk_w_opt) ||
+      !ok_opt(dy_perm_opt) || !ok_opt(dtopk_w_opt))
+    return MOE_EINVAL;
+  if (!dy_perm_opt && !dtopk_w_opt) return MOE_EINVAL;
+  if ((dy_perm_opt && !topk_w_opt) || (dtopk_w_opt && !y_perm_opt)) return MOE_EINVAL;
+  const size_t P = (size_t)T * dims->top_k, H = dims->hidden;
+  const size_t db = (size_t)T * H * dtype_bytes(dims->dtype), rb = P * H * dtype_bytes(row_dtype);
+  const struct { const void* p; size_t n; } in[] = {
+      {dout, db}, {y_perm_opt, rb}, {inv, P * 4}, {topk_w_opt, P * 4}};
+  for (const auto& i : in)
+    if (overlap(dy_perm_opt, rb, i.p, i.n) || overlap(dtopk_w_opt, P * 4, i.p, i.n))
+      return MOE_EINVAL;
+  if (overlap(dy_perm_opt, rb, dtopk_w_opt, P * 4)) return MOE_EINVAL;
+  return hip_status(launch_undispatch_backward(*dims, T, dout, y_perm_opt, row_dtype == MOE_BF16,
+                                               inv, topk_w_opt, dy_perm_opt, dtopk_w_opt,
+                                               (hipStream_t)stream));
+}
+
+moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* bytes) {
+  const moe_status_t st = check_rows(dims, T, dims ? dims->dtype : MOE_F32);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_EINVAL;
+  *bytes = (size_t)route_backward_ws_bytes(*dims, T);
+  return MOE_OK;
+}
+
+moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x_opt,
+                                const void* w_router_opt, const int32_t* topk_ids_opt,
+                                const float* logits_opt, const float* dtopk_w_opt,
+                                const float* dlogits_add_opt, float* dlogits,
+                                const void* dx_add_opt, void* dx_opt, float* dw_router_opt,
+                                int32_t accumulate_dw, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t st = check_rows(dims, T, dims ? dims->dtype : MOE_F32);
+  if (st != MOE_OK) return st;
+  if (accumulate_dw != 0 && accumulate_dw != 1) return MOE_EINVAL;
+  if (T == 0) {  // an empty sum
+    if (!ok_opt(dw_router_opt)) return MOE_EINVAL;
+    if (!dw_router_opt || accumulate_dw) return MOE_OK;
+    return hip_status(launch_route_backward(*dims, 0, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                            nullptr, nullptr, nullptr, nullptr, dw_router_opt, 0,
+                                            nullptr, (hipStream_t)stream));
+  }
+  if (!ok_opt(x_opt) || !ok_opt(w_router_opt) || !ok_opt(topk_ids_opt) || !ok_opt(logits_opt) ||
+      !ok_opt(dtopk_w_opt) || !ok_opt(dlogits_add_opt) || !ok_ptr(dlogits) || !ok_opt(dx_add_opt) ||
+      !ok_opt(dx_opt) || !ok_opt(dw_router_opt) || !ok_opt(ws))
+    return MOE_EINVAL;
+  if (!dtopk_w_opt && !dlogits_add_opt) return MOE_EINVAL;
+  if (dtopk_w_opt && (!topk_ids_opt || !logits_opt)) return MOE_EINVAL;
+  if (dx_opt ? !w_router_opt : dx_add_opt != nullptr) return MOE_EINVAL;
+  if (dw_router_opt && !x_opt) return MOE_EINVAL;
+  const size_t H = dims->hidden, E = dims->n_experts, b = dtype_bytes(dims->dtype);
+  const size_t xb = (size_t)T * H * b, lb = (size_t)T * E * 4, kb = (size_t)T * dims->top_k * 4;
+  const size_t need = dw_router_opt ? (size_t)route_backward_ws_bytes(*dims, T) : 0;
+  if (need > 0 && !ws) return MOE_EINVAL;
+  if (ws_bytes < need) return MOE_EWORKSPACE;
+  const struct { const void* p; size_t n; } in[] = {
+      {x_opt, xb}, {w_router_opt, E * H * b}, {topk_ids_opt, kb}, {logits_opt, lb},
+      {dtopk_w_opt, kb}, {dlogits_add_opt, lb}, {dx_add_opt, xb}};
+  const struct { const void* p; size_t n; } out[] = {
+      {dlogits, lb}, {dx_opt, xb}, {dw_router_opt, E * H * 4}, {need ? ws : nullptr, need}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& r : in) {
+      const bool same = out[i].p == r.p && ((i == 0 && r.p == dlogits_add_opt) ||
+                                            (i == 1 && r.p == dx_add_opt));
+      if (!same && overlap(out[i].p, out[i].n, r.p, r.n)) return MOE_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MOE_EINVAL;
+  }
+  return hip_status(launch_route_backward(*dims, T, x_opt, w_router_opt, topk_ids_opt, logits_opt,
+                                          dtopk_w_opt, dlogits_add_opt, dlogits, dx_add_opt, dx_opt,
+                                          dw_router_opt, accumulate_dw, ws, (hipStream_t)stream));
+}
+
+moe_status_t moe_distill_topk_size(int32_t T, int32_t V, size_t* bytes) {
+  if (!bytes || T < 0 || V <= 0) return MOE_EINVAL;
+  if (T > kMaxTokens || V > MOE_DISTILL_MAX_CLASSES) return MOE_EUNSUPPORTED;
+  *bytes = (size_t)distill_ws_bytes(T, V);
+  return MOE_OK;
+}
+
+moe_status_t moe_distill_topk(int32_t T, int32_t V, int64_t ld, int32_t K, const void* student,
+                              moe_dtype_t dtype, const int32_t* teacher_ids,
+                              const float* teacher_logits, const float* teacher_lse_opt,
+                              const float* token_w_opt, float temperature, float scale,
+                              float* loss, void* dstudent_opt, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (T < 0 || V <= 0 || K <= 0 || ld < V) return MOE_EINVAL;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(scale)) return MOE_EINVAL;
+  if (T > kMaxTokens || V > MOE_DISTILL_MAX_CLASSES || K > MOE_DISTILL_MAX_TOP ||
+      ld > (int64_t(1) << 31) || temperature < 0x1p-20f || temperature > 0x1p20f)
+    return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(student) || !ok_ptr(teacher_ids) || !ok_ptr(teacher_logits) ||
+      !ok_opt(teacher_lse_opt) || !ok_opt(token_w_opt) || !ok_ptr(loss) || !ok_opt(dstudent_opt) ||
+      !ok_opt(ws))
+    return MOE_EINVAL;
+  const size_t need = (size_t)distill_ws_bytes(T, V);
+  if (need > 0 && !ws) return MOE_EINVAL;
+  if (ws_bytes < need) return MOE_EWORKSPACE;
+  // rows end at column V: the last row needs no padding behind it
+  const size_t sb = ((size_t)(T - 1) * ld + V) * dtype_bytes(dtype);
+  const size_t kb = (size_t)T * K * 4, tb = (size_t)T * 4;
+  const struct { const void* p; size_t n; } in[] = {
+      {student, sb}, {teacher_ids, kb}, {teacher_logits, kb}, {teacher_lse_opt, tb}, {token_w_opt, tb}};
+  const struct { const void* p; size_t n; } out[] = {
+      {loss, tb}, {dstudent_opt, sb}, {need ? ws : nullptr, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& r : in)
+      if (!(i == 1 && r.p == student && dstudent_opt == student) &&
+          overlap(out[i].p, out[i].n, r.p, r.n))
+        return MOE_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MOE_EINVAL;
+  }
+  return hip_status(launch_distill(T, V, ld, K, student, dtype == MOE_BF16, teacher_ids,
+                                   teacher_logits, teacher_lse_opt, token_w_opt, temperature, scale,
+                                   loss, dstudent_opt, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,275 @@
+// Tokens sorted by expert and back, with the slot weights applied, and the
+// gradient:
+//   dispatch             x_perm[inv[t,j]] = x[t]
+//   undispatch           out[t] = add[t] + sum_j w[t,j] y_perm[inv[t,j]]
+//   undispatch backward  dy_perm[inv[t,j]] = w[t,j] dout[t],
+//                        dw[t,j] = <dout[t], y_perm[inv[t,j]]>
+// The gradient of dispatch is undispatch without weights.  All three walk the
+// tokens, not the sorted rows: x, out and dout move once, and each sorted row
+// is touched by exactly one token, so nothing is accumulated in memory and the
+// sums run over the slots in slot order.  Every kernel is bound by the bytes
+// of the T*k sorted rows.  A row is cut into units of eight elements (16 bytes
+// of bf16, 32 of fp32; hidden % 64 == 0, so a row is whole units).
+// Slots with inv outside 0..T*k-1 (pairs that are not computed) move nothing.
+#include <algorithm>
+
+#include "common.h"
+
+namespace moe {
+
+constexpr int DISPATCH_THREADS = 256;
+
+template <typename T> struct unit8;  // eight elements as loaded
+template <> struct unit8<bf16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+  __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_uint4(f2_to_bf16x2(v[0], v[1]), f2_to_bf16x2(v[2], v[3]), f2_to_bf16x2(v[4], v[5]),
+                   f2_to_bf16x2(v[6], v[7]));
+  }
+};
+template <> struct unit8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) = a;
+    *reinterpret_cast<float4*>(p + 4) = b;
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+// One thread per (token, unit), flat over the batch.
+template <typename T>
+__global__ void __launch_bounds__(DISPATCH_THREADS)
+dispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P, const T* __restrict__ x,
+                const int32_t* __restrict__ inv, T* __restrict__ x_perm) {
+  const uint32_t g = blockIdx.x * DISPATCH_THREADS + threadIdx.x;
+  if (g >= n) return;
+  const uint32_t t = g / units, u = g - t * units;
+  unit8<T> v;
+  v.load(x + (int64_t)g * 8);
+  for (int j = 0; j < k; ++j) {
+    const uint32_t row = (uint32_t)inv[(int64_t)t * k + j];
+    if (row < P) v.store(x_perm + (int64_t)row * H + u * 8);
+  }
+}
+
+// One thread per (token, unit): the loads of all slots' rows go out together,
+// then the sum runs in slot order in fp32 and is rounded once.  add may be
+// out itself (a thread reads its unit before it writes it).
+template <typename T, typename Ty>
+__global__ void __launch_bounds__(DISPATCH_THREADS)
+undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
+                  const Ty* __restrict__ y_perm, const int32_t* __restrict__ inv,
+                  const float* __restrict__ topk_w, const T* add, T* out) {
+  const uint32_t g = blockIdx.x * DISPATCH_THREADS + threadIdx.x;
+  if (g >= n) return;
+  const uint32_t t = g / units, u = g - t * units;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (add) {
+    unit8<T> a;
+    a.load(add + (int64_t)g * 8);
+    a.get(acc);
+  }
+  unit8<Ty> v[MOE_MAX_TOPK];
+  float w[MOE_MAX_TOPK];
+  bool live[MOE_MAX_TOPK];
+#pragma unroll
+  for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+    const int64_t o = (int64_t)t * k + j;
+    const uint32_t row = j < k ? (uint32_t)inv[o] : 0xFFFFFFFFu;
+    live[j] = row < P;
+    w[j] = 1.f;
+    if (live[j]) {
+      v[j].load(y_perm + (int64_t)row * H + u * 8);
+      if (topk_w) w[j] = topk_w[o];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+    if (!live[j]) continue;
+    float f[8];
+    v[j].get(f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[j], f[c], acc[c]);
+  }
+  unit8<T> o;
+  o.set(acc);
+  o.store(out + (int64_t)g * 8);
+}
+
+// One group of G lanes per token (G the power of two that covers the row's
+// units, at most a wave): each lane walks its units with all slots' rows in
+// flight, then the lanes' partial dots meet in a fixed tree.
+template <typename T, typename Ty, int G, bool DY, bool DW>
+__global__ void __launch_bounds__(DISPATCH_THREADS)
+undispatch_bwd_kernel(int T_, int units, int H, int k, uint32_t P, const T* __restrict__ dout,
+                      const Ty* __restrict__ y_perm, const int32_t* __restrict__ inv,
+                      const float* __restrict__ topk_w, Ty* __restrict__ dy_perm,
+                      float* __restrict__ dtopk_w) {
+  const int l = threadIdx.x % G;
+  const int t = blockIdx.x * (DISPATCH_THREADS / G) + threadIdx.x / G;
+  if (t >= T_) return;  // whole groups leave together
+  uint32_t row[MOE_MAX_TOPK];
+  float w[MOE_MAX_TOPK], dot[MOE_MAX_TOPK];
+#pragma unroll
+  for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+    const int64_t o = (int64_t)t * k + j;
+    row[j] = j < k ? (uint32_t)inv[o] : 0xFFFFFFFFu;
+    w[j] = DY && j < k ? topk_w[o] : 0.f;
+    dot[j] = 0.f;
+  }
+  for (int u = l; u < units; u += G) {
+    unit8<T> d;
+    d.load(dout + (int64_t)t * H + u * 8);
+    unit8<Ty> y[MOE_MAX_TOPK];
+    if (DW) {
+#pragma unroll
+      for (int j = 0; j < MOE_MAX_TOPK; ++j)
+        if (row[j] < P) y[j].load(y_perm + (int64_t)row[j] * H + u * 8);
+    }
+    float df[8];
+    d.get(df);
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+      if (row[j] >= P) continue;
+      if (DW) {
+        float f[8];
+        y[j].get(f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dot[j] = fmaf(df[c], f[c], dot[j]);
+      }
+      if (DY) {
+        float o[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[c] = w[j] * df[c];
+        unit8<Ty> ov;
+        ov.set(o);
+        ov.store(dy_perm + (int64_t)row[j] * H + u * 8);
+      }
+    }
+  }
+  if (DW) {
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+      if (j >= k) break;
+      float s = dot[j];
+#pragma unroll
+      for (int m = G / 2; m > 0; m >>= 1) s += __shfl_xor(s, m, G);
+      if (l == 0) dtopk_w[(int64_t)t * k + j] = s;
+    }
+  }
+}
+
+template <typename T>
+static void dispatch_t(const moe_dims_t& d, int T_, const void* x, const int32_t* inv, void* x_perm,
+                       hipStream_t s) {
+  const uint32_t units = d.hidden / 8, n = (uint32_t)T_ * units;
+  dispatch_kernel<T><<<(n + DISPATCH_THREADS - 1) / DISPATCH_THREADS, DISPATCH_THREADS, 0, s>>>(
+      n, units, d.hidden, d.top_k, (uint32_t)T_ * d.top_k, (const T*)x, inv, (T*)x_perm);
+}
+
+hipError_t launch_dispatch(const moe_dims_t& d, int T, const void* x, const int32_t* inv,
+                           void* x_perm, hipStream_t s) {
+  if (d.dtype == MOE_BF16)
+    dispatch_t<bf16>(d, T, x, inv, x_perm, s);
+  else
+    dispatch_t<float>(d, T, x, inv, x_perm, s);
+  return hipGetLastError();
+}
+
+template <typename T, typename Ty>
+static void undispatch_t(const moe_dims_t& d, int T_, const void* y, const int32_t* inv,
+                         const float* w, const void* add, void* out, hipStream_t s) {
+  const uint32_t units = d.hidden / 8, n = (uint32_t)T_ * units;
+  undispatch_kernel<T, Ty>
+      <<<(n + DISPATCH_THREADS - 1) / DISPATCH_THREADS, DISPATCH_THREADS, 0, s>>>(
+          n, units, d.hidden, d.top_k, (uint32_t)T_ * d.top_k, (const Ty*)y, inv, w, (const T*)add,
+          (T*)out);
+}
+
+hipError_t launch_undispatch(const moe_dims_t& d, int T, const void* y_perm, bool rows_bf16,
+                             const int32_t* inv, const float* topk_w, const void* add, void* out,
+                             hipStream_t s) {
+  if (d.dtype != MOE_BF16)
+    undispatch_t<float, float>(d, T, y_perm, inv, topk_w, add, out, s);
+  else if (rows_bf16)
+    undispatch_t<bf16, bf16>(d, T, y_perm, inv, topk_w, add, out, s);
+  else
+    undispatch_t<bf16, float>(d, T, y_perm, inv, topk_w, add, out, s);
+  return hipGetLastError();
+}
+
+struct UndispatchBwd {
+  const moe_dims_t& d;
+  int T;
+  const void *dout, *y_perm;
+  const int32_t* inv;
+  const float* w;
+  void* dy;
+  float* dw;
+  hipStream_t s;
+};
+
+template <typename T, typename Ty, int G, bool DY, bool DW>
+static void bwd_launch(const UndispatchBwd& a) {
+  constexpr int per = DISPATCH_THREADS / G;
+  undispatch_bwd_kernel<T, Ty, G, DY, DW><<<(a.T + per - 1) / per, DISPATCH_THREADS, 0, a.s>>>(
+      a.T, a.d.hidden / 8, a.d.hidden, a.d.top_k, (uint32_t)a.T * a.d.top_k, (const T*)a.dout,
+      (const Ty*)a.y_perm, a.inv, a.w, (Ty*)a.dy, a.dw);
+}
+template <typename T, typename Ty, int G>
+static void bwd_outputs(const UndispatchBwd& a) {
+  if (a.dy && a.dw)
+    bwd_launch<T, Ty, G, true, true>(a);
+  else if (a.dy)
+    bwd_launch<T, Ty, G, true, false>(a);
+  else
+    bwd_launch<T, Ty, G, false, true>(a);
+}
+template <typename T, typename Ty>
+static void bwd_group(const UndispatchBwd& a) {
+  const int units = a.d.hidden / 8;
+  if (units <= 8)
+    bwd_outputs<T, Ty, 8>(a);
+  else if (units <= 16)
+    bwd_outputs<T, Ty, 16>(a);
+  else if (units <= 32)
+    bwd_outputs<T, Ty, 32>(a);
+  else
+    bwd_outputs<T, Ty, 64>(a);
+}
+
+// At least one of dy and dw is not null; y_perm is read only for dw, topk_w
+// only for dy.
+hipError_t launch_undispatch_backward(const moe_dims_t& d, int T, const void* dout,
+                                      const void* y_perm, bool rows_bf16, const int32_t* inv,
+                                      const float* topk_w, void* dy, float* dw, hipStream_t s) {
+  const UndispatchBwd a{d, T, dout, y_perm, inv, topk_w, dy, dw, s};
+  if (d.dtype != MOE_BF16)
+    bwd_group<float, float>(a);
+  else if (rows_bf16)
+    bwd_group<bf16, bf16>(a);
+  else
+    bwd_group<bf16, float>(a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

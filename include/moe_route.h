@@ -448,7 +448,8 @@ moe_status_t moe_undispatch_backward(const moe_dims_t* dims, int32_t T, const vo
                                      const int32_t* inv, const float* topk_w_opt,
                                      void* dy_perm_opt, float* dtopk_w_opt, void* stream);
 
-/* Bytes of workspace moe_route_backward needs for dw_router (host output). */
+/* Bytes of workspace moe_route_backward needs for dx or dw_router (host output;
+ * may be 0). */
 moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* bytes /* host */);
 
 /* Gradient of the router l = x W_r^T and of moe_route's weights:
@@ -463,9 +464,9 @@ moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* 
  * dlogits_add counts (a given gradient of the logits, such as
  * moe_distill_topk's; topk_ids and logits may then be NULL).  One of the two
  * must be given.  dlogits_add_opt may be dlogits itself, dx_add_opt dx itself.
- * dx_opt needs w_router, dw_router_opt needs x and ws
+ * dx_opt needs w_router, dw_router_opt needs x, and both need ws
  * (moe_route_backward_size); either may be NULL.  T = 0 clears dw_router
- * unless it accumulates, and enqueues nothing else. */
+ * unless it accumulates, and enqueues nothing else.  E * hidden < 2^31. */
 moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x_opt,
                                 const void* w_router_opt, const int32_t* topk_ids_opt,
                                 const float* logits_opt, const float* dtopk_w_opt,

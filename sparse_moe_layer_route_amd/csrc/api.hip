@@ -617,6 +617,13 @@ moe_status_t check_rows(const moe_dims_t* d, int32_t T, moe_dtype_t row_dtype) {
   return rows_fit(*d, T) ? MOE_OK : MOE_EUNSUPPORTED;
 }
 
+// The router's matrix is indexed below 2^31 elements as well.
+moe_status_t check_router(const moe_dims_t* d, int32_t T) {
+  const moe_status_t st = check_rows(d, T, d ? d->dtype : MOE_F32);
+  if (st != MOE_OK) return st;
+  return (int64_t)d->n_experts * d->hidden < (int64_t(1) << 31) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
 }  // namespace
 
 moe_status_t moe_dispatch(const moe_dims_t* dims, int32_t T, const void* x, const int32_t* inv,
@@ -671,7 +678,7 @@ moe_status_t moe_undispatch_backward(const moe_dims_t* dims, int32_t T, const vo
 }
 
 moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* bytes) {
-  const moe_status_t st = check_rows(dims, T, dims ? dims->dtype : MOE_F32);
+  const moe_status_t st = check_router(dims, T);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_EINVAL;
   *bytes = (size_t)route_backward_ws_bytes(*dims, T);
@@ -684,7 +691,7 @@ moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x
                                 const float* dlogits_add_opt, float* dlogits,
                                 const void* dx_add_opt, void* dx_opt, float* dw_router_opt,
                                 int32_t accumulate_dw, void* ws, size_t ws_bytes, void* stream) {
-  const moe_status_t st = check_rows(dims, T, dims ? dims->dtype : MOE_F32);
+  const moe_status_t st = check_router(dims, T);
   if (st != MOE_OK) return st;
   if (accumulate_dw != 0 && accumulate_dw != 1) return MOE_EINVAL;
   if (T == 0) {  // an empty sum
@@ -704,7 +711,7 @@ moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x
   if (dw_router_opt && !x_opt) return MOE_EINVAL;
   const size_t H = dims->hidden, E = dims->n_experts, b = dtype_bytes(dims->dtype);
   const size_t xb = (size_t)T * H * b, lb = (size_t)T * E * 4, kb = (size_t)T * dims->top_k * 4;
-  const size_t need = dw_router_opt ? (size_t)route_backward_ws_bytes(*dims, T) : 0;
+  const size_t need = dw_router_opt || dx_opt ? (size_t)route_backward_ws_bytes(*dims, T) : 0;
   if (need > 0 && !ws) return MOE_EINVAL;
   if (ws_bytes < need) return MOE_EWORKSPACE;
   const struct { const void* p; size_t n; } in[] = {

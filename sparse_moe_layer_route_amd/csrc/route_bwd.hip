@@ -8,131 +8,496 @@
 //   with G_v the sum of dtopk_w over the slots of expert v and n_v their number
 //   (0 or 1 for moe_route's ids; an expert named twice counts twice).
 //   dx = dx_add + dl W_r,  dW_r = dl^T x.
+//
+// Three launches: the logits' gradient (route_dlogits_kernel), both products
+// in one grid (route_products_kernel), and the sum of dW's token ranges when
+// there is more than one.  The products read x once and write dx once, which
+// bounds them (E <= 64: 4 E flops for four bytes of bf16).
+//
+// bf16 layers run v_mfma_f32_16x16x32_bf16 on x and W as they are; dl is fp32
+// and goes in as bf16 parts whose sum it is: three for dW (fp32 out, what is
+// left out is 2^-24 of dl), two for dx (2^-16, against an output step of
+// 2^-8).  The parts are written by the first launch as whole operand
+// fragments.  Both operands want eight consecutive k (tokens for dW, experts
+// for dx) in a lane, while x and W are contiguous along H: a lane loads four
+// columns of eight rows (8 bytes each; 16 lanes cover a 128-byte line) and
+// interleaves them in registers into the fragments of four column tiles, tile
+// c holding columns 4n + c, so nothing passes through LDS on the way in.
+// fp32 layers run v_mfma_f32_16x16x4_f32, whose operands are single values.
 #include <algorithm>
 
 #include "common.h"
 
 namespace moe {
 
-constexpr int RBWD_THREADS = 256;
-constexpr int RBWD_SPLIT_TOKENS = 256;
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// One wave per token, lane = expert; dlogits_add may be dlogits itself.
+constexpr int RBWD_THREADS = 512;
+constexpr int RBWD_WAVES = RBWD_THREADS / MOE_WAVE;
+constexpr int RBWD_STEP = 32;   // tokens of one dW step (the K of one bf16 MFMA)
+constexpr int RBWD_COLS = 64;   // columns of H a wave owns
+constexpr int RBWD_DW_PARTS = 3, RBWD_DX_PARTS = 2;
+
+// Shapes of one call.  mt: 16-expert tiles, ks: 32-expert k steps of dx.
+struct RouteBwdPlan {
+  int mt, ks, steps, ncg;
+  int splits;              // token ranges of dW
+  int dx_tiles;            // 16-token tiles of one dx wave
+  int dw_blocks, dx_blocks;
+  size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments, dW partials
+};
+
+// A dx wave takes enough token tiles that about RBWD_DX_WAVES waves run.
+#ifndef RBWD_DX_WAVES
+#define RBWD_DX_WAVES 4096
+#endif
+#ifndef RBWD_DW_BLOCKS
+#define RBWD_DW_BLOCKS 512
+#endif
+
+static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
+  RouteBwdPlan p{};
+  p.mt = (d.n_experts + 15) / 16;
+  p.ks = (p.mt + 1) / 2;
+  p.steps = (T + RBWD_STEP - 1) / RBWD_STEP;
+  p.ncg = d.hidden / RBWD_COLS;
+  // each range gives every wave of its block a step at least
+  const int most = std::max(1, (p.steps + RBWD_WAVES - 1) / RBWD_WAVES);
+  p.splits = std::min(most, std::max(1, RBWD_DW_BLOCKS / p.ncg));
+  const int tiles = 2 * p.steps;
+  p.dx_tiles = std::min(16, std::max(1, (int)((int64_t)tiles * p.ncg / RBWD_DX_WAVES)));
+  p.dw_blocks = p.splits * p.ncg;
+  const int64_t waves = (int64_t)((tiles + p.dx_tiles - 1) / p.dx_tiles) * p.ncg;
+  p.dx_blocks = (int)((waves + RBWD_WAVES - 1) / RBWD_WAVES);
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    const size_t at = o;
+    o = (o + n + 255) & ~(size_t)255;
+    return at;
+  };
+  if (d.dtype == MOE_BF16) {
+    p.fx = take((size_t)tiles * p.ks * RBWD_DX_PARTS * 1024);
+    p.fw = take((size_t)p.steps * p.mt * RBWD_DW_PARTS * 1024);
+  }
+  if (p.splits > 1) p.part = take((size_t)p.splits * d.n_experts * d.hidden * 4);
+  p.total = o;
+  return p;
+}
+
+// Part i of v as bf16: v rounded, then what is left rounded, and so on.
+__device__ __forceinline__ uint16_t bf16_part(float v, int i) {
+  uint16_t b = f_to_bf16(v);
+  for (; i > 0; --i) {
+    const float h = bf16_to_f(b);
+    v = __builtin_isinf(h) ? 0.f : v - h;  // inf - inf would turn inf into NaN
+    b = f_to_bf16(v);
+  }
+  return b;
+}
+
+// One block per 32 tokens, one wave per token, lane = expert; dlogits_add may
+// be dlogits itself.  fx / fw (null for fp32 layers): the block's fragments,
+//   fx [16-token tile][k step][part][lane]: token lane % 16, experts
+//     32 s + 8 (lane / 16) .. +7 (zero past T and E),
+//   fw [32-token step][expert tile][part][lane]: expert lane % 16, tokens
+//     8 (lane / 16) .. +7.
 __global__ void __launch_bounds__(RBWD_THREADS)
 route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict__ ids,
                      const float* __restrict__ logits, const float* __restrict__ dtopk_w,
-                     const float* dlogits_add, float* dlogits) {
-  const int lane = lane_id();
-  const int t = blockIdx.x * (RBWD_THREADS / MOE_WAVE) + (threadIdx.x >> 6);
-  if (t >= T) return;
+                     const float* dlogits_add, float* dlogits, int mt, int ks,
+                     uint4* __restrict__ fx, uint4* __restrict__ fw) {
+  __shared__ float tile[RBWD_STEP][MOE_MAX_EXPERTS + 1];
+  const int lane = lane_id(), wv = threadIdx.x >> 6;
   const bool in = lane < E;
-  const int64_t o = (int64_t)t * E + lane;
-  float dl = 0.f;
-  if (dtopk_w) {
-    const float l = in ? logits[o] : 0.f;
-    float G = 0.f, n = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int e = ids[(int64_t)t * k + j];
-      const float g = dtopk_w[(int64_t)t * k + j];
-      if (e == lane && in) {
-        G += g;
-        n += 1.f;
+#pragma unroll
+  for (int r = 0; r < RBWD_STEP / RBWD_WAVES; ++r) {
+    const int tt = wv * (RBWD_STEP / RBWD_WAVES) + r;
+    const int t = blockIdx.x * RBWD_STEP + tt;
+    float dl = 0.f;
+    if (t < T) {
+      const int64_t o = (int64_t)t * E + lane;
+      const float add = dlogits_add && in ? dlogits_add[o] : 0.f;
+      if (dtopk_w) {
+        const float l = in ? logits[o] : 0.f;
+        float G = 0.f, n = 0.f;
+        for (int j = 0; j < k; ++j) {
+          const int e = ids[(int64_t)t * k + j];
+          const float g = dtopk_w[(int64_t)t * k + j];
+          if (e == lane && in) {
+            G += g;
+            n += 1.f;
+          }
+        }
+        const bool part = in && (!renorm || n > 0.f);
+        const float m = wave_max(part ? l : -__builtin_inff());
+        const float z = part ? expf(l - m) : 0.f;
+        const float mult = renorm ? n : 1.f;
+        const float s = wave_sum(part ? mult * z : 0.f);
+        const float p = part ? z / s : 0.f;
+        const float c = wave_sum(n > 0.f ? G * p : 0.f);
+        dl = part ? p * (G - mult * c) : 0.f;
+      }
+      dl += add;
+      if (in) dlogits[o] = dl;
+    }
+    tile[tt][lane] = in ? dl : 0.f;
+  }
+  if (!fx && !fw) return;
+  __syncthreads();
+  const int nx = fx ? 2 * ks * RBWD_DX_PARTS * 64 : 0, nw = fw ? mt * RBWD_DW_PARTS * 64 : 0;
+  for (int i = threadIdx.x; i < nx + nw; i += RBWD_THREADS) {
+    uint16_t v[8];
+    if (i < nx) {
+      const int l = i & 63, part = (i >> 6) % RBWD_DX_PARTS, f = (i >> 6) / RBWD_DX_PARTS;
+      const int s = f % ks, half = f / ks;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[c] = bf16_part(tile[16 * half + (l & 15)][32 * s + 8 * (l >> 4) + c], part);
+    } else {
+      const int l = i & 63, f = (i - nx) >> 6, part = f % RBWD_DW_PARTS, m = f / RBWD_DW_PARTS;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[c] = bf16_part(tile[8 * (l >> 4) + c][16 * m + (l & 15)], part);
+    }
+    uint4 o;
+    o.x = v[0] | ((uint32_t)v[1] << 16);
+    o.y = v[2] | ((uint32_t)v[3] << 16);
+    o.z = v[4] | ((uint32_t)v[5] << 16);
+    o.w = v[6] | ((uint32_t)v[7] << 16);
+    if (i < nx)
+      fx[(int64_t)blockIdx.x * nx + i] = o;
+    else
+      fw[(int64_t)blockIdx.x * nw + (i - nx)] = o;
+  }
+}
+
+// Four columns of eight rows -> fragment c = 0..3: column c, the eight rows in
+// k order.
+__device__ __forceinline__ bf16x8_t column_frag(const uint2 (&v)[8], int c) {
+  const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+  uint4 o;
+  if (c < 2) {
+    o.x = __builtin_amdgcn_perm(v[1].x, v[0].x, sel);
+    o.y = __builtin_amdgcn_perm(v[3].x, v[2].x, sel);
+    o.z = __builtin_amdgcn_perm(v[5].x, v[4].x, sel);
+    o.w = __builtin_amdgcn_perm(v[7].x, v[6].x, sel);
+  } else {
+    o.x = __builtin_amdgcn_perm(v[1].y, v[0].y, sel);
+    o.y = __builtin_amdgcn_perm(v[3].y, v[2].y, sel);
+    o.z = __builtin_amdgcn_perm(v[5].y, v[4].y, sel);
+    o.w = __builtin_amdgcn_perm(v[7].y, v[6].y, sel);
+  }
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+
+// Rows r0 + 8 (lane / 16) .. +7 below n_rows (zero from there on), four
+// columns each.
+__device__ __forceinline__ void load_rows8(const bf16* __restrict__ p, int r0, int n_rows, int H,
+                                           uint2 (&v)[8]) {
+  const int r = r0 + 8 * (lane_id() >> 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = make_uint2(0u, 0u);
+    if (r + i < n_rows) v[i] = *reinterpret_cast<const uint2*>(p + (int64_t)(r + i) * H);
+  }
+}
+
+struct RouteBwdArgs {
+  int T, H, E, ncg, steps, splits, dx_tiles, dw_blocks;
+  const float* dl;
+  const uint4 *fx, *fw;
+  float *part, *dw;
+  int accumulate;
+};
+
+// acc[m][c] += the 32 tokens of `step`: experts 16 m .. +15 by columns 4n + c.
+template <int MT>
+__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ xc,
+                                         int s0, int s1, f32x4_t (&acc)[MT][4]) {
+  const int lane = lane_id();
+  if (s0 >= s1) return;
+  uint2 v[8];
+  load_rows8(xc, s0 * RBWD_STEP, a.T, a.H, v);
+  for (int s = s0; s < s1; s += RBWD_WAVES) {
+    bf16x8_t b[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) b[c] = column_frag(v, c);
+    if (s + RBWD_WAVES < s1) load_rows8(xc, (s + RBWD_WAVES) * RBWD_STEP, a.T, a.H, v);
+    const uint4* f = a.fw + (int64_t)s * MT * RBWD_DW_PARTS * 64 + lane;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int p = RBWD_DW_PARTS - 1; p >= 0; --p) {  // smallest part first
+        const bf16x8_t af = __builtin_bit_cast(bf16x8_t, f[(m * RBWD_DW_PARTS + p) * 64]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, b[c], acc[m][c], 0, 0, 0);
+      }
+  }
+}
+template <int MT>
+__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ xc,
+                                         int s0, int s1, f32x4_t (&acc)[MT][4]) {
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+  for (int s = s0; s < s1; s += RBWD_WAVES) {
+    float4 v[8];
+    float d[8][MT];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int t = s * RBWD_STEP + 4 * q + g;
+      v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < a.T) v[q] = *reinterpret_cast<const float4*>(xc + (int64_t)t * a.H);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int e = 16 * m + n;
+        d[q][m] = t < a.T && e < a.E ? a.dl[(int64_t)t * a.E + e] : 0.f;
       }
     }
-    const bool part = in && (!renorm || n > 0.f);
-    const float m = wave_max(part ? l : -__builtin_inff());
-    const float z = part ? expf(l - m) : 0.f;
-    const float mult = renorm ? n : 1.f;
-    const float s = wave_sum(part ? mult * z : 0.f);
-    const float p = part ? z / s : 0.f;
-    const float c = wave_sum(n > 0.f ? G * p : 0.f);
-    dl = part ? p * (G - mult * c) : 0.f;
-  }
-  if (in) {
-    if (dlogits_add) dl += dlogits_add[o];
-    dlogits[o] = dl;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].x, acc[m][0], 0, 0, 0);
+        acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].y, acc[m][1], 0, 0, 0);
+        acc[m][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].z, acc[m][2], 0, 0, 0);
+        acc[m][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].w, acc[m][3], 0, 0, 0);
+      }
   }
 }
 
-// dx: one thread per (token, eight columns), summed over the experts in order.
-template <typename T>
-__global__ void __launch_bounds__(RBWD_THREADS)
-route_dx_kernel(uint32_t n, uint32_t units, int H, int E, const float* __restrict__ dl,
-                const T* __restrict__ w, const T* dx_add, T* dx) {
-  const uint32_t g = blockIdx.x * RBWD_THREADS + threadIdx.x;
-  if (g >= n) return;
-  const uint32_t t = g / units, u = g - t * units;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (dx_add) elem<T>::load8(dx_add + (int64_t)g * 8, acc);
-  for (int e = 0; e < E; ++e) {
-    float wv[8];
-    elem<T>::load8(w + (int64_t)e * H + u * 8, wv);
-    const float d = dl[(int64_t)t * E + e];
+// dW of 64 columns over one range of tokens: the eight waves take the range's
+// steps in turn and their tiles meet in LDS, the upper four added to the lower
+// four first, then the four summed in order.
+template <typename T, int MT>
+__device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
+                                         const T* __restrict__ x, float* lds) {
+  const int split = item / a.ncg, cg = item - split * a.ncg;
+  const int lane = lane_id(), wv = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int per = (a.steps + a.splits - 1) / a.splits;
+  const int s0 = split * per, s1 = min(a.steps, s0 + per);
+  f32x4_t acc[MT][4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = fmaf(d, wv[c], acc[c]);
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  dw_steps<MT>(a, x + cg * RBWD_COLS + 4 * n, s0 + wv, s1, acc);
+  constexpr int TILE = 16 * MT * RBWD_COLS;
+  float* mine = lds + (wv & 3) * TILE + 4 * n;
+  if (wv >= 4) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(mine + (16 * m + 4 * g + i) * RBWD_COLS) =
+            make_float4(acc[m][0][i], acc[m][1][i], acc[m][2][i], acc[m][3][i]);
   }
+  __syncthreads();
+  if (wv < 4) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) elem<T>::store(dx, (int64_t)g * 8 + c, acc[c]);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float4* q = reinterpret_cast<float4*>(mine + (16 * m + 4 * g + i) * RBWD_COLS);
+        const float4 o = *q;
+        *q = make_float4(acc[m][0][i] + o.x, acc[m][1][i] + o.y, acc[m][2][i] + o.z,
+                         acc[m][3][i] + o.w);
+      }
+  }
+  __syncthreads();
+  const bool direct = a.splits == 1;
+  for (int u = threadIdx.x; u < TILE / 4; u += RBWD_THREADS) {
+    const int e = u / (RBWD_COLS / 4), h = cg * RBWD_COLS + (u % (RBWD_COLS / 4)) * 4;
+    if (e >= a.E) break;
+    const float4* q = reinterpret_cast<const float4*>(lds) + u;
+    const float4 v0 = q[0], v1 = q[TILE / 4], v2 = q[TILE / 2], v3 = q[3 * TILE / 4];
+    float4 o = make_float4(((v0.x + v1.x) + v2.x) + v3.x, ((v0.y + v1.y) + v2.y) + v3.y,
+                           ((v0.z + v1.z) + v2.z) + v3.z, ((v0.w + v1.w) + v2.w) + v3.w);
+    float4* dst = reinterpret_cast<float4*>(
+        direct ? a.dw + (int64_t)e * a.H + h : a.part + ((int64_t)split * a.E + e) * a.H + h);
+    if (direct && a.accumulate) {
+      const float4 b = *dst;
+      o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
+    }
+    *dst = o;
+  }
 }
 
-// dW partials: one thread per (expert, eight columns) and range of tokens.
-template <typename T>
-__global__ void __launch_bounds__(RBWD_THREADS)
-route_dw_kernel(int T_, int units, int H, int E, const float* __restrict__ dl,
-                const T* __restrict__ x, float* __restrict__ part) {
-  const int g = blockIdx.x * RBWD_THREADS + threadIdx.x;
-  if (g >= E * units) return;
-  const int e = g / units, u = g - e * units;
-  const int t0 = blockIdx.y * RBWD_SPLIT_TOKENS, t1 = min(T_, t0 + RBWD_SPLIT_TOKENS);
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int t = t0; t < t1; ++t) {
-    float xv[8];
-    elem<T>::load8(x + (int64_t)t * H + u * 8, xv);
-    const float d = dl[(int64_t)t * E + e];
+// dx of 64 columns by 16-token tiles, one wave: the products are formed as
+// (W^T)(dl^T), so a lane ends with 16 consecutive columns of one token.
+template <int MT>
+__device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
+                                         const bf16* __restrict__ w, const bf16* dx_add, bf16* dx) {
+  constexpr int KS = (MT + 1) / 2;
+  const int range = item / a.ncg, cg = item - range * a.ncg;
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+  const int t0 = range * a.dx_tiles, t1 = min(2 * a.steps, t0 + a.dx_tiles);
+  bf16x8_t wf[KS][4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = fmaf(d, xv[c], acc[c]);
+  for (int s = 0; s < KS; ++s) {
+    uint2 v[8];
+    load_rows8(w + cg * RBWD_COLS + 4 * n, 32 * s, a.E, a.H, v);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) wf[s][c] = column_frag(v, c);
   }
-  float* o = part + ((int64_t)blockIdx.y * E + e) * H + u * 8;
+  for (int tl = t0; tl < t1; ++tl) {
+    const int t = tl * 16 + n;
+    const int64_t o = (int64_t)t * a.H + cg * RBWD_COLS + 16 * g;
+    const uint4* f = a.fx + (int64_t)tl * KS * RBWD_DX_PARTS * 64 + lane;
+    f32x4_t acc[4];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) o[c] = acc[c];
+    for (int c = 0; c < 4; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (dx_add && t < a.T) {
+      float d0[8], d1[8];
+      elem<bf16>::load8(dx_add + o, d0);
+      elem<bf16>::load8(dx_add + o + 8, d1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[c] = f32x4_t{d0[c], d0[4 + c], d1[c], d1[4 + c]};
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int p = RBWD_DX_PARTS - 1; p >= 0; --p) {
+        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, f[(s * RBWD_DX_PARTS + p) * 64]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[s][c], b, acc[c], 0, 0, 0);
+      }
+    if (t < a.T) {
+      uint4 u[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        u[h] = make_uint4(f2_to_bf16x2(acc[0][2 * h], acc[1][2 * h]),
+                          f2_to_bf16x2(acc[2][2 * h], acc[3][2 * h]),
+                          f2_to_bf16x2(acc[0][2 * h + 1], acc[1][2 * h + 1]),
+                          f2_to_bf16x2(acc[2][2 * h + 1], acc[3][2 * h + 1]));
+      reinterpret_cast<uint4*>(dx + o)[0] = u[0];
+      reinterpret_cast<uint4*>(dx + o)[1] = u[1];
+    }
+  }
+}
+// fp32: k step 4q + r holds experts 16 q + 4 (lane / 16) + r on both sides, so
+// a lane's four steps of one q are four consecutive experts of its token.
+template <int MT>
+__device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
+                                         const float* __restrict__ w, const float* dx_add,
+                                         float* dx) {
+  const int range = item / a.ncg, cg = item - range * a.ncg;
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+  const int t0 = range * a.dx_tiles, t1 = min(2 * a.steps, t0 + a.dx_tiles);
+  float4 wf[MT][4];
+#pragma unroll
+  for (int q = 0; q < MT; ++q)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = 16 * q + 4 * g + r;
+      wf[q][r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < a.E)
+        wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * RBWD_COLS + 4 * n);
+    }
+  for (int tl = t0; tl < t1; ++tl) {
+    const int t = tl * 16 + n;
+    const int64_t o = (int64_t)t * a.H + cg * RBWD_COLS + 16 * g;
+    f32x4_t acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (dx_add && t < a.T) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 d = *reinterpret_cast<const float4*>(dx_add + o + 4 * i);
+        acc[0][i] = d.x;
+        acc[1][i] = d.y;
+        acc[2][i] = d.z;
+        acc[3][i] = d.w;
+      }
+    }
+    float d[MT][4];
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = 16 * q + 4 * g + r;
+        d[q][r] = t < a.T && e < a.E ? a.dl[(int64_t)t * a.E + e] : 0.f;
+      }
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].x, d[q][r], acc[0], 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].y, d[q][r], acc[1], 0, 0, 0);
+        acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].z, d[q][r], acc[2], 0, 0, 0);
+        acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].w, d[q][r], acc[3], 0, 0, 0);
+      }
+    if (t < a.T) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(dx + o + 4 * i) =
+            make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
+    }
+  }
+}
+
+// Work items in contiguous eighths of the list per XCD (blocks go round-robin
+// over the eight): the items of one token range share its fragments in L2.
+__device__ __forceinline__ int xcd_item(int b, int n) {
+  const int per = (n + 7) >> 3;
+  return (b & 7) * per + (b >> 3);
+}
+
+// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx.
+template <typename T, int MT>
+__global__ void __launch_bounds__(RBWD_THREADS)
+route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
+                      const T* __restrict__ w, const T* dx_add, T* dx) {
+  __shared__ __align__(16) float lds[4 * 16 * MT * RBWD_COLS];
+  const int nw = (a.dw_blocks + 7) & ~7;
+  if ((int)blockIdx.x < nw) {
+    const int item = xcd_item(blockIdx.x, a.dw_blocks);
+    if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
+  } else {
+    const int nx = (dx_items + RBWD_WAVES - 1) / RBWD_WAVES;
+    const int b = xcd_item(blockIdx.x - nw, nx);
+    const int item = b * RBWD_WAVES + (threadIdx.x >> 6);
+    if (b < nx && item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
+  }
 }
 
 // dW = (dW +) the sum of the ranges' partials, in range order.
-__global__ void __launch_bounds__(RBWD_THREADS)
-route_dw_sum_kernel(int64_t n, int splits, const float* __restrict__ part, int accumulate,
-                    float* __restrict__ dw) {
-  const int64_t i = (int64_t)blockIdx.x * RBWD_THREADS + threadIdx.x;
-  if (i >= n) return;
-  float s = accumulate ? dw[i] : 0.f;
-  for (int p = 0; p < splits; ++p) s += part[(int64_t)p * n + i];
+__global__ void __launch_bounds__(256)
+route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
+                    float4* __restrict__ dw) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 s = accumulate ? dw[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < splits; ++p) {
+    const float4 v = part[(int64_t)p * n4 + i];
+    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  }
   dw[i] = s;
 }
 
-static int dw_splits(int T) { return (T + RBWD_SPLIT_TOKENS - 1) / RBWD_SPLIT_TOKENS; }
-
 int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
-  return (int64_t)dw_splits(T) * d.n_experts * d.hidden * 4;
+  return T > 0 ? (int64_t)route_bwd_plan(d, T).total : 0;
 }
 
 template <typename T>
-static hipError_t route_bwd_t(const moe_dims_t& d, int T_, const T* x, const T* w, const float* dl,
-                              const T* dx_add, T* dx, float* dw, int accumulate, float* ws,
-                              hipStream_t s) {
-  const int H = d.hidden, E = d.n_experts, units = H / 8;
-  if (dx && T_ > 0) {
-    const uint32_t n = (uint32_t)T_ * units;
-    route_dx_kernel<T><<<(n + RBWD_THREADS - 1) / RBWD_THREADS, RBWD_THREADS, 0, s>>>(
-        n, units, H, E, dl, w, dx_add, dx);
+static void launch_products(const RouteBwdPlan& p, const RouteBwdArgs& a, int dx_items, const void* x,
+                            const void* w, const void* dx_add, void* dx, hipStream_t s) {
+  const int nx = (dx_items + RBWD_WAVES - 1) / RBWD_WAVES;
+  const int grid = ((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7);
+  auto go = [&](auto kernel) {
+    kernel<<<grid, RBWD_THREADS, 0, s>>>(a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add,
+                                         (T*)dx);
+  };
+  switch (p.mt) {
+    case 1: go(route_products_kernel<T, 1>); break;
+    case 2: go(route_products_kernel<T, 2>); break;
+    case 3: go(route_products_kernel<T, 3>); break;
+    default: go(route_products_kernel<T, 4>); break;
   }
-  if (dw) {
-    const int splits = dw_splits(T_);
-    if (splits > 0) route_dw_kernel<T><<<dim3((E * units + RBWD_THREADS - 1) / RBWD_THREADS, splits), RBWD_THREADS,
-                         0, s>>>(T_, units, H, E, dl, x, ws);
-    const int64_t n = (int64_t)E * H;
-    route_dw_sum_kernel<<<(unsigned)((n + RBWD_THREADS - 1) / RBWD_THREADS), RBWD_THREADS, 0, s>>>(
-        n, splits, ws, accumulate, dw);
-  }
-  return hipGetLastError();
 }
 
 // dx and dw may be null; x is read only for dw, w_router only for dx.  An
@@ -141,18 +506,37 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
                                  const int32_t* ids, const float* logits, const float* dtopk_w,
                                  const float* dlogits_add, float* dlogits, const void* dx_add,
                                  void* dx, float* dw, int accumulate, void* ws, hipStream_t s) {
-  if (T > 0) {
-    constexpr int per = RBWD_THREADS / MOE_WAVE;
-    route_dlogits_kernel<<<(T + per - 1) / per, RBWD_THREADS, 0, s>>>(
-        T, d.n_experts, d.top_k, d.renormalize, ids, logits, dtopk_w, dlogits_add, dlogits);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const int n4 = d.n_experts * d.hidden / 4;
+  const unsigned sum_blocks = (unsigned)((n4 + 255) / 256);
+  if (T == 0) {
+    if (dw) route_dw_sum_kernel<<<sum_blocks, 256, 0, s>>>(n4, 0, nullptr, accumulate, (float4*)dw);
+    return hipGetLastError();
   }
-  if (d.dtype == MOE_BF16)
-    return route_bwd_t<bf16>(d, T, (const bf16*)x, (const bf16*)w_router, dlogits,
-                             (const bf16*)dx_add, (bf16*)dx, dw, accumulate, (float*)ws, s);
-  return route_bwd_t<float>(d, T, (const float*)x, (const float*)w_router, dlogits,
-                            (const float*)dx_add, (float*)dx, dw, accumulate, (float*)ws, s);
+  const RouteBwdPlan p = route_bwd_plan(d, T);
+  const bool packs = d.dtype == MOE_BF16;
+  char* base = static_cast<char*>(ws);
+  uint4* fx = packs && dx ? reinterpret_cast<uint4*>(base + p.fx) : nullptr;
+  uint4* fw = packs && dw ? reinterpret_cast<uint4*>(base + p.fw) : nullptr;
+  route_dlogits_kernel<<<p.steps, RBWD_THREADS, 0, s>>>(T, d.n_experts, d.top_k, d.renormalize, ids,
+                                                        logits, dtopk_w, dlogits_add, dlogits, p.mt,
+                                                        p.ks, fx, fw);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!dx && !dw)) return e;
+  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles,
+                       dw ? p.dw_blocks : 0, dlogits, fx, fw,
+                       p.splits > 1 ? reinterpret_cast<float*>(base + p.part) : nullptr, dw, accumulate};
+  const int dx_items = dx ? (2 * p.steps + p.dx_tiles - 1) / p.dx_tiles * p.ncg : 0;
+  if (packs)
+    launch_products<bf16>(p, a, dx_items, x, w_router, dx_add, dx, s);
+  else
+    launch_products<float>(p, a, dx_items, x, w_router, dx_add, dx, s);
+  e = hipGetLastError();
+  if (e == hipSuccess && dw && p.splits > 1) {
+    route_dw_sum_kernel<<<sum_blocks, 256, 0, s>>>(n4, p.splits, (const float4*)a.part, accumulate,
+                                                   (float4*)dw);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace moe

@@ -244,7 +244,7 @@ def test_route_backward(T, H, E, k, dtype, renorm, form):
     # each product alone
     dx3, dw3 = torch.empty_like(dx), torch.empty_like(dw)
     if dxa is None:
-        M.moe_route_backward(d, T, None, w, None, None, None, dl2, dx3, None, None, dlogits_add=dl)
+        M.moe_route_backward(d, T, None, w, None, None, None, dl2, dx3, None, ws, dlogits_add=dl)
         assert torch.equal(dx3, dx) and torch.equal(dl2, dl)
     M.moe_route_backward(d, T, x, None, None, None, None, dl2, None, dw3, ws, dlogits_add=dl)
     assert torch.equal(dw3, dw)

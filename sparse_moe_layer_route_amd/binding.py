@@ -183,9 +183,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream for it (0.3
+# against 3 us a call); not every torch build has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(stream)
@@ -376,22 +383,33 @@ _TORCH_DTYPES = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 _MOE_DTYPES = {v: k for k, v in _TORCH_DTYPES.items()}
 
 
-def _arg(name, t, n, dtype, optional=False):
-    """Address of a device tensor of at least n elements of `dtype` on the
-    current device (where the stream is); None where optional."""
-    if t is None and optional:
+def _device(stream):
+    """The current GPU, which the stream has to belong to; -2, no tensor's
+    device, before torch has touched one."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the current GPU is {dev}")
+    return dev
+
+
+def _arg(dev, name, t, n, dtype, optional=False):
+    """Address of a contiguous tensor of at least n elements of `dtype` on
+    GPU `dev`; None where optional."""
+    if isinstance(t, torch.Tensor):
+        if (t.dtype is dtype and t.numel() >= n and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    elif t is None and optional:
         return None
-    p = _ptr(t) if t is not None else None
-    if p is None:
+    else:
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() < n:
         raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} lives on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return p
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    raise ValueError(f"{name} lives on {t.device}, not on the current GPU")
 
 
 def _row_dtype(t):
@@ -402,43 +420,43 @@ def _row_dtype(t):
     return _MOE_DTYPES[t.dtype]
 
 
-def _ws(ws):
-    return (None, 0) if ws is None or ws.numel() == 0 else (_arg("ws", ws, 0, torch.uint8), ws.numel())
+def _ws(dev, ws):
+    return (None, 0) if ws is None or ws.numel() == 0 else (_arg(dev, "ws", ws, 0, torch.uint8), ws.numel())
 
 
 def moe_dispatch(dims, T, x, inv, x_perm, stream=None):
-    d = _dims(dims)
+    d, dev = _dims(dims), _device(stream)
     dt, P = _TORCH_DTYPES[d.dtype], T * d.top_k
-    _check(_lib.moe_dispatch(ctypes.byref(d), T, _arg("x", x, T * d.hidden, dt),
-                             _arg("inv", inv, P, torch.int32),
-                             _arg("x_perm", x_perm, P * d.hidden, dt), _stream(stream)),
+    _check(_lib.moe_dispatch(ctypes.byref(d), T, _arg(dev, "x", x, T * d.hidden, dt),
+                             _arg(dev, "inv", inv, P, torch.int32),
+                             _arg(dev, "x_perm", x_perm, P * d.hidden, dt), _stream(stream)),
            "moe_dispatch")
 
 
 def moe_undispatch(dims, T, y_perm, inv, topk_w, out, add=None, stream=None):
     """topk_w None: every weight is 1 (the gradient of moe_dispatch)."""
-    d = _dims(dims)
+    d, dev = _dims(dims), _device(stream)
     dt, P, H = _TORCH_DTYPES[d.dtype], T * d.top_k, d.hidden
     row = _row_dtype(y_perm)
-    _check(_lib.moe_undispatch(ctypes.byref(d), T, _arg("y_perm", y_perm, P * H, y_perm.dtype), row,
-                               _arg("inv", inv, P, torch.int32),
-                               _arg("topk_w", topk_w, P, torch.float32, True),
-                               _arg("add", add, T * H, dt, True), _arg("out", out, T * H, dt),
+    _check(_lib.moe_undispatch(ctypes.byref(d), T, _arg(dev, "y_perm", y_perm, P * H, y_perm.dtype), row,
+                               _arg(dev, "inv", inv, P, torch.int32),
+                               _arg(dev, "topk_w", topk_w, P, torch.float32, True),
+                               _arg(dev, "add", add, T * H, dt, True), _arg(dev, "out", out, T * H, dt),
                                _stream(stream)), "moe_undispatch")
 
 
 def moe_undispatch_backward(dims, T, dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=None):
     """dy_perm or dtopk_w may be None (then topk_w or y_perm may be too)."""
-    d = _dims(dims)
+    d, dev = _dims(dims), _device(stream)
     dt, P, H = _TORCH_DTYPES[d.dtype], T * d.top_k, d.hidden
     rows = y_perm if y_perm is not None else dy_perm
     row = _row_dtype(rows)
     _check(_lib.moe_undispatch_backward(
-        ctypes.byref(d), T, _arg("dout", dout, T * H, dt),
-        _arg("y_perm", y_perm, P * H, rows.dtype, True), row, _arg("inv", inv, P, torch.int32),
-        _arg("topk_w", topk_w, P, torch.float32, True),
-        _arg("dy_perm", dy_perm, P * H, rows.dtype, True),
-        _arg("dtopk_w", dtopk_w, P, torch.float32, True), _stream(stream)),
+        ctypes.byref(d), T, _arg(dev, "dout", dout, T * H, dt),
+        _arg(dev, "y_perm", y_perm, P * H, rows.dtype, True), row, _arg(dev, "inv", inv, P, torch.int32),
+        _arg(dev, "topk_w", topk_w, P, torch.float32, True),
+        _arg(dev, "dy_perm", dy_perm, P * H, rows.dtype, True),
+        _arg(dev, "dtopk_w", dtopk_w, P, torch.float32, True), _stream(stream)),
         "moe_undispatch_backward")
 
 
@@ -451,16 +469,16 @@ def moe_route_backward_size(dims, T) -> int:
 
 def moe_route_backward(dims, T, x, w_router, topk_ids, logits, dtopk_w, dlogits, dx, dw_router, ws,
                        dlogits_add=None, dx_add=None, accumulate_dw=False, stream=None):
-    d = _dims(dims)
+    d, dev = _dims(dims), _device(stream)
     dt, f32, P, H, E = _TORCH_DTYPES[d.dtype], torch.float32, T * d.top_k, d.hidden, d.n_experts
-    ws_p, ws_n = _ws(ws)
+    ws_p, ws_n = _ws(dev, ws)
     _check(_lib.moe_route_backward(
-        ctypes.byref(d), T, _arg("x", x, T * H, dt, True),
-        _arg("w_router", w_router, E * H, dt, True),
-        _arg("topk_ids", topk_ids, P, torch.int32, True), _arg("logits", logits, T * E, f32, True),
-        _arg("dtopk_w", dtopk_w, P, f32, True), _arg("dlogits_add", dlogits_add, T * E, f32, True),
-        _arg("dlogits", dlogits, T * E, f32), _arg("dx_add", dx_add, T * H, dt, True),
-        _arg("dx", dx, T * H, dt, True), _arg("dw_router", dw_router, E * H, f32, True),
+        ctypes.byref(d), T, _arg(dev, "x", x, T * H, dt, True),
+        _arg(dev, "w_router", w_router, E * H, dt, True),
+        _arg(dev, "topk_ids", topk_ids, P, torch.int32, True), _arg(dev, "logits", logits, T * E, f32, True),
+        _arg(dev, "dtopk_w", dtopk_w, P, f32, True), _arg(dev, "dlogits_add", dlogits_add, T * E, f32, True),
+        _arg(dev, "dlogits", dlogits, T * E, f32), _arg(dev, "dx_add", dx_add, T * H, dt, True),
+        _arg(dev, "dx", dx, T * H, dt, True), _arg(dev, "dw_router", dw_router, E * H, f32, True),
         int(accumulate_dw), ws_p, ws_n, _stream(stream)), "moe_route_backward")
 
 
@@ -475,17 +493,17 @@ def moe_distill_topk(T, V, K, student, teacher_ids, teacher_logits, loss, dstude
                      stream=None):
     """ld: elements from one row of student (and dstudent) to the next; None:
     the length of student's last axis."""
-    row = _row_dtype(student)
+    row, dev = _row_dtype(student), _device(stream)
     ld = student.shape[-1] if ld is None else int(ld)
     n = (T - 1) * ld + V if T > 0 else 0
-    ws_p, ws_n = _ws(ws)
+    ws_p, ws_n = _ws(dev, ws)
     _check(_lib.moe_distill_topk(
-        T, V, ld, K, _arg("student", student, n, student.dtype), row,
-        _arg("teacher_ids", teacher_ids, T * K, torch.int32),
-        _arg("teacher_logits", teacher_logits, T * K, torch.float32),
-        _arg("teacher_lse", teacher_lse, T, torch.float32, True),
-        _arg("token_w", token_w, T, torch.float32, True), float(temperature), float(scale),
-        _arg("loss", loss, T, torch.float32), _arg("dstudent", dstudent, n, student.dtype, True),
+        T, V, ld, K, _arg(dev, "student", student, n, student.dtype), row,
+        _arg(dev, "teacher_ids", teacher_ids, T * K, torch.int32),
+        _arg(dev, "teacher_logits", teacher_logits, T * K, torch.float32),
+        _arg(dev, "teacher_lse", teacher_lse, T, torch.float32, True),
+        _arg(dev, "token_w", token_w, T, torch.float32, True), float(temperature), float(scale),
+        _arg(dev, "loss", loss, T, torch.float32), _arg(dev, "dstudent", dstudent, n, student.dtype, True),
         ws_p, ws_n, _stream(stream)), "moe_distill_topk")
 
 

@@ -85,18 +85,23 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   return p;
 }
 
-// Part i of v as bf16: v rounded, then what is left rounded, and so on.
-__device__ __forceinline__ uint16_t bf16_part(float v, int i) {
-  uint16_t b = f_to_bf16(v);
-  for (; i > 0; --i) {
-    const float h = bf16_to_f(b);
+// v = hi + mid + lo with each part a bf16: v rounded, what is left rounded, and
+// so on.
+struct Parts3 {
+  uint16_t p[3];
+};
+__device__ __forceinline__ Parts3 bf16_parts(float v) {
+  Parts3 o;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    o.p[i] = f_to_bf16(v);
+    const float h = bf16_to_f(o.p[i]);
     v = __builtin_isinf(h) ? 0.f : v - h;  // inf - inf would turn inf into NaN
-    b = f_to_bf16(v);
   }
-  return b;
+  return o;
 }
 
-// One block per 32 tokens, one wave per token, lane = expert; dlogits_add may
+// One block per 32 tokens, lane = expert, four tokens a wave; dlogits_add may
 // be dlogits itself.  fx / fw (null for fp32 layers): the block's fragments,
 //   fx [16-token tile][k step][part][lane]: token lane % 16, experts
 //     32 s + 8 (lane / 16) .. +7 (zero past T and E),
@@ -108,67 +113,88 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
                      const float* dlogits_add, float* dlogits, int mt, int ks,
                      uint4* __restrict__ fx, uint4* __restrict__ fw) {
   __shared__ float tile[RBWD_STEP][MOE_MAX_EXPERTS + 1];
+  constexpr int R = RBWD_STEP / RBWD_WAVES;  // tokens of one wave
   const int lane = lane_id(), wv = threadIdx.x >> 6;
   const bool in = lane < E;
+  // Every load of the wave's tokens first (tokens past T, lanes past E and
+  // slots past k read the last one): lane j holds slot j's id and gradient.
+  // Each stage then runs over all R tokens, whose chains are independent.
+  float l[R], dl[R], g[R];
+  int id[R];
+  const int t0 = blockIdx.x * RBWD_STEP + wv * R;
+  if (dtopk_w) {
 #pragma unroll
-  for (int r = 0; r < RBWD_STEP / RBWD_WAVES; ++r) {
-    const int tt = wv * (RBWD_STEP / RBWD_WAVES) + r;
-    const int t = blockIdx.x * RBWD_STEP + tt;
-    float dl = 0.f;
-    if (t < T) {
-      const int64_t o = (int64_t)t * E + lane;
-      const float add = dlogits_add && in ? dlogits_add[o] : 0.f;
-      if (dtopk_w) {
-        const float l = in ? logits[o] : 0.f;
-        float G = 0.f, n = 0.f;
-        for (int j = 0; j < k; ++j) {
-          const int e = ids[(int64_t)t * k + j];
-          const float g = dtopk_w[(int64_t)t * k + j];
-          if (e == lane && in) {
-            G += g;
-            n += 1.f;
-          }
-        }
-        const bool part = in && (!renorm || n > 0.f);
-        const float m = wave_max(part ? l : -__builtin_inff());
-        const float z = part ? expf(l - m) : 0.f;
-        const float mult = renorm ? n : 1.f;
-        const float s = wave_sum(part ? mult * z : 0.f);
-        const float p = part ? z / s : 0.f;
-        const float c = wave_sum(n > 0.f ? G * p : 0.f);
-        dl = part ? p * (G - mult * c) : 0.f;
-      }
-      dl += add;
-      if (in) dlogits[o] = dl;
+    for (int r = 0; r < R; ++r) {
+      const int64_t t = min(t0 + r, T - 1);
+      l[r] = logits[t * E + min(lane, E - 1)];
+      const int64_t o = t * k + min(lane, k - 1);
+      id[r] = ids[o];
+      g[r] = dtopk_w[o];
     }
-    tile[tt][lane] = in ? dl : 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    dl[r] = dlogits_add ? dlogits_add[(int64_t)min(t0 + r, T - 1) * E + min(lane, E - 1)] : 0.f;
+  if (dtopk_w) {
+    float G[R], n[R], z[R], s[R], c[R];
+    bool part[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      G[r] = n[r] = 0.f;
+      for (int j = 0; j < k; ++j) {
+        const int e = __builtin_amdgcn_readlane(id[r], j);
+        const float gj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g[r]), j));
+        G[r] += e == lane ? gj : 0.f;
+        n[r] += e == lane ? 1.f : 0.f;
+      }
+      part[r] = in && (!renorm || n[r] > 0.f);
+      s[r] = part[r] ? l[r] : -__builtin_inff();
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      z[r] = part[r] ? expf(l[r] - wave_max(s[r])) : 0.f;
+      s[r] = renorm ? n[r] * z[r] : z[r];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float p = z[r] / wave_sum(s[r]);
+      z[r] = part[r] ? p : 0.f;
+      c[r] = in && n[r] > 0.f ? G[r] * p : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float cr = wave_sum(c[r]);
+      dl[r] += part[r] ? z[r] * (G[r] - (renorm ? n[r] : 1.f) * cr) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool on = in && t0 + r < T;
+    if (on) dlogits[(int64_t)(t0 + r) * E + lane] = dl[r];
+    tile[wv * R + r][lane] = on ? dl[r] : 0.f;
   }
   if (!fx && !fw) return;
   __syncthreads();
-  const int nx = fx ? 2 * ks * RBWD_DX_PARTS * 64 : 0, nw = fw ? mt * RBWD_DW_PARTS * 64 : 0;
+  // one thread per fragment slot, all of its parts
+  const int nx = fx ? 2 * ks * 64 : 0, nw = fw ? mt * 64 : 0;
   for (int i = threadIdx.x; i < nx + nw; i += RBWD_THREADS) {
-    uint16_t v[8];
-    if (i < nx) {
-      const int l = i & 63, part = (i >> 6) % RBWD_DX_PARTS, f = (i >> 6) / RBWD_DX_PARTS;
-      const int s = f % ks, half = f / ks;
+    const bool to_x = i < nx;
+    const int l16 = i & 15, g8 = 8 * ((i >> 4) & 3), f = (to_x ? i : i - nx) >> 6;
+    const int half = ks == 2 ? f >> 1 : f, st = ks == 2 ? f & 1 : 0;
+    Parts3 v[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        v[c] = bf16_part(tile[16 * half + (l & 15)][32 * s + 8 * (l >> 4) + c], part);
-    } else {
-      const int l = i & 63, f = (i - nx) >> 6, part = f % RBWD_DW_PARTS, m = f / RBWD_DW_PARTS;
+    for (int c = 0; c < 8; ++c)
+      v[c] = bf16_parts(to_x ? tile[16 * half + l16][32 * st + g8 + c] : tile[g8 + c][16 * f + l16]);
+    const int parts = to_x ? RBWD_DX_PARTS : RBWD_DW_PARTS;
+    uint4* dst = to_x ? fx + ((int64_t)blockIdx.x * 2 * ks + f) * RBWD_DX_PARTS * 64
+                      : fw + ((int64_t)blockIdx.x * mt + f) * RBWD_DW_PARTS * 64;
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        v[c] = bf16_part(tile[8 * (l >> 4) + c][16 * m + (l & 15)], part);
-    }
-    uint4 o;
-    o.x = v[0] | ((uint32_t)v[1] << 16);
-    o.y = v[2] | ((uint32_t)v[3] << 16);
-    o.z = v[4] | ((uint32_t)v[5] << 16);
-    o.w = v[6] | ((uint32_t)v[7] << 16);
-    if (i < nx)
-      fx[(int64_t)blockIdx.x * nx + i] = o;
-    else
-      fw[(int64_t)blockIdx.x * nw + (i - nx)] = o;
+    for (int p = 0; p < 3; ++p)
+      if (p < parts)
+        dst[p * 64 + (i & 63)] = make_uint4(v[0].p[p] | ((uint32_t)v[1].p[p] << 16),
+                                            v[2].p[p] | ((uint32_t)v[3].p[p] << 16),
+                                            v[4].p[p] | ((uint32_t)v[5].p[p] << 16),
+                                            v[6].p[p] | ((uint32_t)v[7].p[p] << 16));
   }
 }
 
@@ -196,10 +222,15 @@ __device__ __forceinline__ bf16x8_t column_frag(const uint2 (&v)[8], int c) {
 __device__ __forceinline__ void load_rows8(const bf16* __restrict__ p, int r0, int n_rows, int H,
                                            uint2 (&v)[8]) {
   const int r = r0 + 8 * (lane_id() >> 4);
+  if (r0 + RBWD_STEP <= n_rows) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = make_uint2(0u, 0u);
-    if (r + i < n_rows) v[i] = *reinterpret_cast<const uint2*>(p + (int64_t)(r + i) * H);
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint2*>(p + (int64_t)(r + i) * H);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = make_uint2(0u, 0u);
+      if (r + i < n_rows) v[i] = *reinterpret_cast<const uint2*>(p + (int64_t)(r + i) * H);
+    }
   }
 }
 
@@ -211,29 +242,42 @@ struct RouteBwdArgs {
   int accumulate;
 };
 
-// acc[m][c] += the 32 tokens of `step`: experts 16 m .. +15 by columns 4n + c.
+// acc[m][c] += the tokens of steps s0, s0 + 8, .. below s1: experts 16 m .. +15
+// by columns 4n + c.  Loads retire in order, so a step's fragments are asked
+// for before the rows of the step after the next: waiting for them leaves two
+// steps' rows in flight.
+template <int MT>
+__device__ __forceinline__ void dw_step(const RouteBwdArgs& a, const bf16* __restrict__ xc, int s,
+                                        int s1, uint2 (&v)[8], f32x4_t (&acc)[MT][4]) {
+  const uint4* f = a.fw + (int64_t)s * MT * RBWD_DW_PARTS * 64 + lane_id();
+  uint4 af[MT][RBWD_DW_PARTS];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int p = 0; p < RBWD_DW_PARTS; ++p) af[m][p] = f[(m * RBWD_DW_PARTS + p) * 64];
+  bf16x8_t b[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) b[c] = column_frag(v, c);
+  if (s + 2 * RBWD_WAVES < s1) load_rows8(xc, (s + 2 * RBWD_WAVES) * RBWD_STEP, a.T, a.H, v);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int p = RBWD_DW_PARTS - 1; p >= 0; --p)  // smallest part first
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, af[m][p]),
+                                                            b[c], acc[m][c], 0, 0, 0);
+}
 template <int MT>
 __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ xc,
                                          int s0, int s1, f32x4_t (&acc)[MT][4]) {
-  const int lane = lane_id();
   if (s0 >= s1) return;
-  uint2 v[8];
-  load_rows8(xc, s0 * RBWD_STEP, a.T, a.H, v);
-  for (int s = s0; s < s1; s += RBWD_WAVES) {
-    bf16x8_t b[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) b[c] = column_frag(v, c);
-    if (s + RBWD_WAVES < s1) load_rows8(xc, (s + RBWD_WAVES) * RBWD_STEP, a.T, a.H, v);
-    const uint4* f = a.fw + (int64_t)s * MT * RBWD_DW_PARTS * 64 + lane;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int p = RBWD_DW_PARTS - 1; p >= 0; --p) {  // smallest part first
-        const bf16x8_t af = __builtin_bit_cast(bf16x8_t, f[(m * RBWD_DW_PARTS + p) * 64]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, b[c], acc[m][c], 0, 0, 0);
-      }
+  uint2 v0[8], v1[8];
+  load_rows8(xc, s0 * RBWD_STEP, a.T, a.H, v0);
+  if (s0 + RBWD_WAVES < s1) load_rows8(xc, (s0 + RBWD_WAVES) * RBWD_STEP, a.T, a.H, v1);
+  for (int s = s0; s < s1; s += 2 * RBWD_WAVES) {
+    dw_step<MT>(a, xc, s, s1, v0, acc);
+    if (s + RBWD_WAVES < s1) dw_step<MT>(a, xc, s + RBWD_WAVES, s1, v1, acc);
   }
 }
 template <int MT>
@@ -324,7 +368,13 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
 }
 
 // dx of 64 columns by 16-token tiles, one wave: the products are formed as
-// (W^T)(dl^T), so a lane ends with 16 consecutive columns of one token.
+// (W^T)(dl^T), so a lane ends with 16 columns of one token, rows 4 g + i of
+// the tiles c = 0..3.  Operand row n takes columns dx_cols(n) + c, which makes
+// them two runs of eight, 8 g and 32 + 8 g: each 16-byte store then covers 64
+// contiguous bytes of a token with four lanes.
+__device__ __forceinline__ int dx_cols(int n) {
+  return 8 * (n >> 2) + 4 * (n & 1) + 32 * ((n >> 1) & 1);
+}
 template <int MT>
 __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
                                          const bf16* __restrict__ w, const bf16* dx_add, bf16* dx) {
@@ -336,45 +386,59 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     uint2 v[8];
-    load_rows8(w + cg * RBWD_COLS + 4 * n, 32 * s, a.E, a.H, v);
+    load_rows8(w + cg * RBWD_COLS + dx_cols(n), 32 * s, a.E, a.H, v);
 #pragma unroll
     for (int c = 0; c < 4; ++c) wf[s][c] = column_frag(v, c);
   }
+  // a tile's fragments and addend are asked for before the tile before it is
+  // stored: loads and stores retire in one order
+  constexpr int NF = KS * RBWD_DX_PARTS;
+  uint4 f[NF], add[2];
+  auto load = [&](int tl) {
+    const uint4* src = a.fx + (int64_t)tl * NF * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) f[i] = src[i * 64];
+    add[0] = add[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (dx_add && tl * 16 + n < a.T) {
+      const uint4* q = reinterpret_cast<const uint4*>(dx_add + (int64_t)(tl * 16 + n) * a.H +
+                                                      cg * RBWD_COLS + 8 * g);
+      add[0] = q[0];
+      add[1] = q[4];
+    }
+  };
+  load(t0);
   for (int tl = t0; tl < t1; ++tl) {
     const int t = tl * 16 + n;
-    const int64_t o = (int64_t)t * a.H + cg * RBWD_COLS + 16 * g;
-    const uint4* f = a.fx + (int64_t)tl * KS * RBWD_DX_PARTS * 64 + lane;
     f32x4_t acc[4];
+    // acc[c][i]: column 4 (i % 2) + c of run i / 2
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (dx_add && t < a.T) {
-      float d0[8], d1[8];
-      elem<bf16>::load8(dx_add + o, d0);
-      elem<bf16>::load8(dx_add + o + 8, d1);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        acc[c] = f32x4_t{d0[c], d0[4 + c], d1[c], d1[4 + c]};
-      }
+    for (int h = 0; h < 2; ++h) {
+      acc[0][2 * h] = bf16_lo(add[h].x);
+      acc[1][2 * h] = bf16_hi(add[h].x);
+      acc[2][2 * h] = bf16_lo(add[h].y);
+      acc[3][2 * h] = bf16_hi(add[h].y);
+      acc[0][2 * h + 1] = bf16_lo(add[h].z);
+      acc[1][2 * h + 1] = bf16_hi(add[h].z);
+      acc[2][2 * h + 1] = bf16_lo(add[h].w);
+      acc[3][2 * h + 1] = bf16_hi(add[h].w);
     }
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int p = RBWD_DX_PARTS - 1; p >= 0; --p) {
-        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, f[(s * RBWD_DX_PARTS + p) * 64]);
+      for (int p = RBWD_DX_PARTS - 1; p >= 0; --p)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[s][c], b, acc[c], 0, 0, 0);
-      }
+          acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              wf[s][c], __builtin_bit_cast(bf16x8_t, f[s * RBWD_DX_PARTS + p]), acc[c], 0, 0, 0);
+    if (tl + 1 < t1) load(tl + 1);
     if (t < a.T) {
-      uint4 u[2];
+      uint4* q = reinterpret_cast<uint4*>(dx + (int64_t)t * a.H + cg * RBWD_COLS + 8 * g);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        u[h] = make_uint4(f2_to_bf16x2(acc[0][2 * h], acc[1][2 * h]),
+        q[4 * h] = make_uint4(f2_to_bf16x2(acc[0][2 * h], acc[1][2 * h]),
                           f2_to_bf16x2(acc[2][2 * h], acc[3][2 * h]),
                           f2_to_bf16x2(acc[0][2 * h + 1], acc[1][2 * h + 1]),
                           f2_to_bf16x2(acc[2][2 * h + 1], acc[3][2 * h + 1]));
-      reinterpret_cast<uint4*>(dx + o)[0] = u[0];
-      reinterpret_cast<uint4*>(dx + o)[1] = u[1];
     }
   }
 }

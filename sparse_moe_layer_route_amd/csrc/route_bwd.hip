@@ -33,10 +33,14 @@ namespace moe {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int RBWD_THREADS = 512;
+constexpr int RBWD_THREADS = 512;  // of the logits' gradient
 constexpr int RBWD_WAVES = RBWD_THREADS / MOE_WAVE;
+constexpr int PROD_THREADS = 256;  // of the products
+constexpr int PROD_WAVES = PROD_THREADS / MOE_WAVE;
 constexpr int RBWD_STEP = 32;   // tokens of one dW step (the K of one bf16 MFMA)
-constexpr int RBWD_COLS = 64;   // columns of H a wave owns
+// Column tiles of 16 a wave owns (H % 64 == 0: the last wave of a bf16 row may
+// own 64 columns past the end, which it neither keeps nor stores).
+template <typename T> constexpr int rbwd_nc() { return sizeof(T) == 2 ? 8 : 4; }
 constexpr int RBWD_DW_PARTS = 3, RBWD_DX_PARTS = 2;
 
 // Shapes of one call.  mt: 16-expert tiles, ks: 32-expert k steps of dx.
@@ -44,16 +48,15 @@ struct RouteBwdPlan {
   int mt, ks, steps, ncg;
   int splits;              // token ranges of dW
   int dx_tiles;            // 16-token tiles of one dx wave
-  int dw_blocks, dx_blocks;
   size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments, dW partials
 };
 
 // A dx wave takes enough token tiles that about RBWD_DX_WAVES waves run.
 #ifndef RBWD_DX_WAVES
-#define RBWD_DX_WAVES 4096
+#define RBWD_DX_WAVES 1024
 #endif
 #ifndef RBWD_DW_BLOCKS
-#define RBWD_DW_BLOCKS 512
+#define RBWD_DW_BLOCKS 256
 #endif
 
 static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
@@ -61,15 +64,14 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   p.mt = (d.n_experts + 15) / 16;
   p.ks = (p.mt + 1) / 2;
   p.steps = (T + RBWD_STEP - 1) / RBWD_STEP;
-  p.ncg = d.hidden / RBWD_COLS;
-  // each range gives every wave of its block a step at least
-  const int most = std::max(1, (p.steps + RBWD_WAVES - 1) / RBWD_WAVES);
+  const int cols = d.dtype == MOE_BF16 ? 16 * rbwd_nc<bf16>() : 16 * rbwd_nc<float>();
+  p.ncg = (d.hidden + cols - 1) / cols;
+  // each range gives every set of its block's waves a step at least
+  const int ways = p.mt > 1 ? PROD_WAVES / 2 : PROD_WAVES;
+  const int most = std::max(1, (p.steps + ways - 1) / ways);
   p.splits = std::min(most, std::max(1, RBWD_DW_BLOCKS / p.ncg));
   const int tiles = 2 * p.steps;
   p.dx_tiles = std::min(16, std::max(1, (int)((int64_t)tiles * p.ncg / RBWD_DX_WAVES)));
-  p.dw_blocks = p.splits * p.ncg;
-  const int64_t waves = (int64_t)((tiles + p.dx_tiles - 1) / p.dx_tiles) * p.ncg;
-  p.dx_blocks = (int)((waves + RBWD_WAVES - 1) / RBWD_WAVES);
   size_t o = 0;
   auto take = [&](size_t n) {
     const size_t at = o;
@@ -198,38 +200,35 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
   }
 }
 
-// Four columns of eight rows -> fragment c = 0..3: column c, the eight rows in
-// k order.
-__device__ __forceinline__ bf16x8_t column_frag(const uint2 (&v)[8], int c) {
+// Eight columns of eight rows -> fragment c: column c, the eight rows in k
+// order.
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ bf16x8_t column_frag(const uint4 (&v)[8], int c) {
   const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+  const int w = c >> 1;
   uint4 o;
-  if (c < 2) {
-    o.x = __builtin_amdgcn_perm(v[1].x, v[0].x, sel);
-    o.y = __builtin_amdgcn_perm(v[3].x, v[2].x, sel);
-    o.z = __builtin_amdgcn_perm(v[5].x, v[4].x, sel);
-    o.w = __builtin_amdgcn_perm(v[7].x, v[6].x, sel);
-  } else {
-    o.x = __builtin_amdgcn_perm(v[1].y, v[0].y, sel);
-    o.y = __builtin_amdgcn_perm(v[3].y, v[2].y, sel);
-    o.z = __builtin_amdgcn_perm(v[5].y, v[4].y, sel);
-    o.w = __builtin_amdgcn_perm(v[7].y, v[6].y, sel);
-  }
+  o.x = __builtin_amdgcn_perm(word_of(v[1], w), word_of(v[0], w), sel);
+  o.y = __builtin_amdgcn_perm(word_of(v[3], w), word_of(v[2], w), sel);
+  o.z = __builtin_amdgcn_perm(word_of(v[5], w), word_of(v[4], w), sel);
+  o.w = __builtin_amdgcn_perm(word_of(v[7], w), word_of(v[6], w), sel);
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
-// Rows r0 + 8 (lane / 16) .. +7 below n_rows (zero from there on), four
+// Rows r0 + 8 (lane / 16) .. +7 below n_rows (zero from there on), eight
 // columns each.
 __device__ __forceinline__ void load_rows8(const bf16* __restrict__ p, int r0, int n_rows, int H,
-                                           uint2 (&v)[8]) {
+                                           uint4 (&v)[8]) {
   const int r = r0 + 8 * (lane_id() >> 4);
   if (r0 + RBWD_STEP <= n_rows) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint2*>(p + (int64_t)(r + i) * H);
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(r + i) * H);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[i] = make_uint2(0u, 0u);
-      if (r + i < n_rows) v[i] = *reinterpret_cast<const uint2*>(p + (int64_t)(r + i) * H);
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r + i < n_rows) v[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(r + i) * H);
     }
   }
 }
@@ -242,66 +241,83 @@ struct RouteBwdArgs {
   int accumulate;
 };
 
-// acc[m][c] += the tokens of steps s0, s0 + 8, .. below s1: experts 16 m .. +15
-// by columns 4n + c.  Loads retire in order, so a step's fragments are asked
-// for before the rows of the step after the next: waiting for them leaves two
+// How the four waves of a dW block share a range of tokens: MH halves of the
+// expert tiles (MW each) by WAYS interleaved sets of steps.  Halving the tiles
+// holds a wave to 256 registers (one wave's 64 experts by 128 columns are 128
+// accumulators alone), so a dx block runs beside it on the CU; the two waves
+// of a pair read the same rows of x, the second time from near caches.
+template <int MT> struct DwShape {
+  static constexpr int MH = MT > 1 ? 2 : 1, MW = (MT + MH - 1) / MH, WAYS = PROD_WAVES / MH;
+};
+
+// acc[m][c] += the tokens of steps s0, s0 + WAYS, .. below s1: experts of tile
+// m0 + m by the lanes' column c.  Loads retire in order: a step's fragments are
+// asked for before the rows two steps on, so waiting for them leaves two
 // steps' rows in flight.
 template <int MT>
-__device__ __forceinline__ void dw_step(const RouteBwdArgs& a, const bf16* __restrict__ xc, int s,
-                                        int s1, uint2 (&v)[8], f32x4_t (&acc)[MT][4]) {
-  const uint4* f = a.fw + (int64_t)s * MT * RBWD_DW_PARTS * 64 + lane_id();
-  uint4 af[MT][RBWD_DW_PARTS];
+__device__ __forceinline__ void dw_step(const RouteBwdArgs& a, const bf16* __restrict__ xc, int m0,
+                                        int s, int s1, uint4 (&v)[8],
+                                        f32x4_t (&acc)[DwShape<MT>::MW][8]) {
+  constexpr int MW = DwShape<MT>::MW, WAYS = DwShape<MT>::WAYS;
+  uint4 af[MW][RBWD_DW_PARTS];
+  const uint4* f = a.fw + ((int64_t)s * MT + m0) * RBWD_DW_PARTS * 64 + lane_id();
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MW; ++m)
+    if (m0 + m < MT) {
 #pragma unroll
-    for (int p = 0; p < RBWD_DW_PARTS; ++p) af[m][p] = f[(m * RBWD_DW_PARTS + p) * 64];
-  bf16x8_t b[4];
+      for (int p = 0; p < RBWD_DW_PARTS; ++p) af[m][p] = f[(m * RBWD_DW_PARTS + p) * 64];
+    }
+  bf16x8_t b[8];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) b[c] = column_frag(v, c);
-  if (s + 2 * RBWD_WAVES < s1) load_rows8(xc, (s + 2 * RBWD_WAVES) * RBWD_STEP, a.T, a.H, v);
+  for (int c = 0; c < 8; ++c) b[c] = column_frag(v, c);
+  if (s + 2 * WAYS < s1) load_rows8(xc, (s + 2 * WAYS) * RBWD_STEP, a.T, a.H, v);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MW; ++m)
+    if (m0 + m < MT) {
 #pragma unroll
-    for (int p = RBWD_DW_PARTS - 1; p >= 0; --p)  // smallest part first
+      for (int p = RBWD_DW_PARTS - 1; p >= 0; --p)  // smallest part first
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, af[m][p]),
-                                                            b[c], acc[m][c], 0, 0, 0);
+        for (int c = 0; c < 8; ++c)
+          acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8_t, af[m][p]), b[c], acc[m][c], 0, 0, 0);
+    }
 }
 template <int MT>
-__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ xc,
-                                         int s0, int s1, f32x4_t (&acc)[MT][4]) {
+__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ xc, int m0,
+                                         int s0, int s1, f32x4_t (&acc)[DwShape<MT>::MW][8]) {
+  constexpr int WAYS = DwShape<MT>::WAYS;
   if (s0 >= s1) return;
-  uint2 v0[8], v1[8];
+  uint4 v0[8], v1[8];
   load_rows8(xc, s0 * RBWD_STEP, a.T, a.H, v0);
-  if (s0 + RBWD_WAVES < s1) load_rows8(xc, (s0 + RBWD_WAVES) * RBWD_STEP, a.T, a.H, v1);
-  for (int s = s0; s < s1; s += 2 * RBWD_WAVES) {
-    dw_step<MT>(a, xc, s, s1, v0, acc);
-    if (s + RBWD_WAVES < s1) dw_step<MT>(a, xc, s + RBWD_WAVES, s1, v1, acc);
+  if (s0 + WAYS < s1) load_rows8(xc, (s0 + WAYS) * RBWD_STEP, a.T, a.H, v1);
+  for (int s = s0; s < s1; s += 2 * WAYS) {
+    dw_step<MT>(a, xc, m0, s, s1, v0, acc);
+    if (s + WAYS < s1) dw_step<MT>(a, xc, m0, s + WAYS, s1, v1, acc);
   }
 }
 template <int MT>
-__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ xc,
-                                         int s0, int s1, f32x4_t (&acc)[MT][4]) {
+__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ xc, int m0,
+                                         int s0, int s1, f32x4_t (&acc)[DwShape<MT>::MW][4]) {
+  constexpr int MW = DwShape<MT>::MW;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
-  for (int s = s0; s < s1; s += RBWD_WAVES) {
+  for (int s = s0; s < s1; s += DwShape<MT>::WAYS) {
     float4 v[8];
-    float d[8][MT];
+    float d[8][MW];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int t = s * RBWD_STEP + 4 * q + g;
       v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < a.T) v[q] = *reinterpret_cast<const float4*>(xc + (int64_t)t * a.H);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int e = 16 * m + n;
+      for (int m = 0; m < MW; ++m) {
+        const int e = 16 * (m0 + m) + n;
         d[q][m] = t < a.T && e < a.E ? a.dl[(int64_t)t * a.E + e] : 0.f;
       }
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < MW; ++m) {
         acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].x, acc[m][0], 0, 0, 0);
         acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].y, acc[m][1], 0, 0, 0);
         acc[m][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].z, acc[m][2], 0, 0, 0);
@@ -310,140 +326,138 @@ __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __r
   }
 }
 
-// dW of 64 columns over one range of tokens: the eight waves take the range's
-// steps in turn and their tiles meet in LDS, the upper four added to the lower
-// four first, then the four summed in order.
+template <typename T, int MT>
+constexpr int dw_lds_floats() {
+  using S = DwShape<MT>;
+  return (S::WAYS - 1) * S::MH * 16 * S::MW * 16 * rbwd_nc<T>();
+}
+
+// dW of a wave's columns over one range of tokens.  The waves of way 1 and up
+// leave their tiles in LDS, those of way 0 add them in way order and store.
 template <typename T, int MT>
 __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
                                          const T* __restrict__ x, float* lds) {
+  using S = DwShape<MT>;
+  constexpr int NC = rbwd_nc<T>(), COLS = 16 * NC, MW = S::MW, TILE = 16 * MW * COLS;
   const int split = item / a.ncg, cg = item - split * a.ncg;
   const int lane = lane_id(), wv = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int half = wv % S::MH, way = wv / S::MH, m0 = half * MW;
   const int per = (a.steps + a.splits - 1) / a.splits;
   const int s0 = split * per, s1 = min(a.steps, s0 + per);
-  f32x4_t acc[MT][4];
+  f32x4_t acc[MW][NC];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MW; ++m)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  dw_steps<MT>(a, x + cg * RBWD_COLS + 4 * n, s0 + wv, s1, acc);
-  constexpr int TILE = 16 * MT * RBWD_COLS;
-  float* mine = lds + (wv & 3) * TILE + 4 * n;
-  if (wv >= 4) {
+    for (int c = 0; c < NC; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // lanes past H read the row's last columns; their results are dropped below
+  dw_steps<MT>(a, x + min(cg * COLS + NC * n, a.H - NC), m0, s0 + way, s1, acc);
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MW; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(mine + (16 * m + 4 * g + i) * RBWD_COLS) =
-            make_float4(acc[m][0][i], acc[m][1][i], acc[m][2][i], acc[m][3][i]);
-  }
-  __syncthreads();
-  if (wv < 4) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float4* q = reinterpret_cast<float4*>(mine + (16 * m + 4 * g + i) * RBWD_COLS);
-        const float4 o = *q;
-        *q = make_float4(acc[m][0][i] + o.x, acc[m][1][i] + o.y, acc[m][2][i] + o.z,
-                         acc[m][3][i] + o.w);
-      }
-  }
+        for (int c = 0; c < NC; c += 4)
+          f(16 * m + 4 * g + i, NC * n + c,
+            make_float4(acc[m][c][i], acc[m][c + 1][i], acc[m][c + 2][i], acc[m][c + 3][i]));
+  };
+  auto slot = [&](int w, int r, int c) {
+    return reinterpret_cast<float4*>(lds + ((w - 1) * S::MH + half) * TILE + r * COLS + c);
+  };
+  if (way > 0) each([&](int r, int c, float4 v) { *slot(way, r, c) = v; });
   __syncthreads();
+  if (way > 0) return;
   const bool direct = a.splits == 1;
-  for (int u = threadIdx.x; u < TILE / 4; u += RBWD_THREADS) {
-    const int e = u / (RBWD_COLS / 4), h = cg * RBWD_COLS + (u % (RBWD_COLS / 4)) * 4;
-    if (e >= a.E) break;
-    const float4* q = reinterpret_cast<const float4*>(lds) + u;
-    const float4 v0 = q[0], v1 = q[TILE / 4], v2 = q[TILE / 2], v3 = q[3 * TILE / 4];
-    float4 o = make_float4(((v0.x + v1.x) + v2.x) + v3.x, ((v0.y + v1.y) + v2.y) + v3.y,
-                           ((v0.z + v1.z) + v2.z) + v3.z, ((v0.w + v1.w) + v2.w) + v3.w);
-    float4* dst = reinterpret_cast<float4*>(
-        direct ? a.dw + (int64_t)e * a.H + h : a.part + ((int64_t)split * a.E + e) * a.H + h);
-    if (direct && a.accumulate) {
-      const float4 b = *dst;
-      o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
+  float* out = direct ? a.dw : a.part + (int64_t)split * a.E * a.H;
+  each([&](int r, int c, float4 v) {
+    const int e = 16 * m0 + r, h = cg * COLS + c;
+    if (e >= a.E || h >= a.H) return;
+#pragma unroll
+    for (int w = 1; w < S::WAYS; ++w) {
+      const float4 o = *slot(w, r, c);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
     }
-    *dst = o;
-  }
+    float4* dst = reinterpret_cast<float4*>(out + (int64_t)e * a.H + h);
+    if (direct && a.accumulate) {
+      const float4 o = *dst;
+      v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+    }
+    *dst = v;
+  });
 }
 
-// dx of 64 columns by 16-token tiles, one wave: the products are formed as
-// (W^T)(dl^T), so a lane ends with 16 columns of one token, rows 4 g + i of
-// the tiles c = 0..3.  Operand row n takes columns dx_cols(n) + c, which makes
-// them two runs of eight, 8 g and 32 + 8 g: each 16-byte store then covers 64
-// contiguous bytes of a token with four lanes.
-__device__ __forceinline__ int dx_cols(int n) {
-  return 8 * (n >> 2) + 4 * (n & 1) + 32 * ((n >> 1) & 1);
-}
+// dx of a wave's columns by 16-token tiles: the products are formed as
+// (W^T)(dl^T), so a lane ends with rows 4 g + i of the tiles c = 0..7 for one
+// token.  Operand row r takes columns 8 (r / 4) + 32 (r % 4) + c: the rows of a
+// lane are four runs of eight columns, 8 g + 32 i, and each 16-byte store
+// covers 64 contiguous bytes of a token with four lanes.
 template <int MT>
 __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
                                          const bf16* __restrict__ w, const bf16* dx_add, bf16* dx) {
-  constexpr int KS = (MT + 1) / 2;
+  constexpr int KS = (MT + 1) / 2, NF = KS * RBWD_DX_PARTS;
   const int range = item / a.ncg, cg = item - range * a.ncg;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   const int t0 = range * a.dx_tiles, t1 = min(2 * a.steps, t0 + a.dx_tiles);
-  bf16x8_t wf[KS][4];
+  bf16x8_t wf[KS][8];
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
-    uint2 v[8];
-    load_rows8(w + cg * RBWD_COLS + dx_cols(n), 32 * s, a.E, a.H, v);
+    uint4 v[8];
+    load_rows8(w + min(cg * 128 + 8 * (n >> 2) + 32 * (n & 3), a.H - 8), 32 * s, a.E, a.H, v);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) wf[s][c] = column_frag(v, c);
+    for (int c = 0; c < 8; ++c) wf[s][c] = column_frag(v, c);
   }
+  const int h = cg * 128 + 8 * g;                 // the lane's runs: h + 32 i
+  const int runs = min(4, (a.H - cg * 128) / 32); // 2 or 4 of them inside H
   // a tile's fragments and addend are asked for before the tile before it is
   // stored: loads and stores retire in one order
-  constexpr int NF = KS * RBWD_DX_PARTS;
-  uint4 f[NF], add[2];
+  uint4 f[NF], add[4];
   auto load = [&](int tl) {
     const uint4* src = a.fx + (int64_t)tl * NF * 64 + lane;
 #pragma unroll
     for (int i = 0; i < NF; ++i) f[i] = src[i * 64];
-    add[0] = add[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (dx_add && tl * 16 + n < a.T) {
-      const uint4* q = reinterpret_cast<const uint4*>(dx_add + (int64_t)(tl * 16 + n) * a.H +
-                                                      cg * RBWD_COLS + 8 * g);
-      add[0] = q[0];
-      add[1] = q[4];
+    if (dx_add) {
+      const uint4* q = reinterpret_cast<const uint4*>(
+          dx_add + (int64_t)min(tl * 16 + n, a.T - 1) * a.H + h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < runs) add[i] = q[4 * i];
     }
   };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add[i] = make_uint4(0u, 0u, 0u, 0u);
   load(t0);
   for (int tl = t0; tl < t1; ++tl) {
     const int t = tl * 16 + n;
-    f32x4_t acc[4];
-    // acc[c][i]: column 4 (i % 2) + c of run i / 2
+    f32x4_t acc[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      acc[0][2 * h] = bf16_lo(add[h].x);
-      acc[1][2 * h] = bf16_hi(add[h].x);
-      acc[2][2 * h] = bf16_lo(add[h].y);
-      acc[3][2 * h] = bf16_hi(add[h].y);
-      acc[0][2 * h + 1] = bf16_lo(add[h].z);
-      acc[1][2 * h + 1] = bf16_hi(add[h].z);
-      acc[2][2 * h + 1] = bf16_lo(add[h].w);
-      acc[3][2 * h + 1] = bf16_hi(add[h].w);
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[2 * q][i] = bf16_lo(word_of(add[i], q));
+        acc[2 * q + 1][i] = bf16_hi(word_of(add[i], q));
+      }
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int p = RBWD_DX_PARTS - 1; p >= 0; --p)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 8; ++c)
           acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               wf[s][c], __builtin_bit_cast(bf16x8_t, f[s * RBWD_DX_PARTS + p]), acc[c], 0, 0, 0);
     if (tl + 1 < t1) load(tl + 1);
     if (t < a.T) {
-      uint4* q = reinterpret_cast<uint4*>(dx + (int64_t)t * a.H + cg * RBWD_COLS + 8 * g);
+      uint4* q = reinterpret_cast<uint4*>(dx + (int64_t)t * a.H + h);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        q[4 * h] = make_uint4(f2_to_bf16x2(acc[0][2 * h], acc[1][2 * h]),
-                          f2_to_bf16x2(acc[2][2 * h], acc[3][2 * h]),
-                          f2_to_bf16x2(acc[0][2 * h + 1], acc[1][2 * h + 1]),
-                          f2_to_bf16x2(acc[2][2 * h + 1], acc[3][2 * h + 1]));
+      for (int i = 0; i < 4; ++i)
+        if (i < runs)
+          q[4 * i] = make_uint4(f2_to_bf16x2(acc[0][i], acc[1][i]), f2_to_bf16x2(acc[2][i], acc[3][i]),
+                                f2_to_bf16x2(acc[4][i], acc[5][i]), f2_to_bf16x2(acc[6][i], acc[7][i]));
     }
   }
 }
 // fp32: k step 4q + r holds experts 16 q + 4 (lane / 16) + r on both sides, so
 // a lane's four steps of one q are four consecutive experts of its token.
+// Operand row r takes columns 4 r + c: a lane ends with 16 consecutive ones.
 template <int MT>
 __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
                                          const float* __restrict__ w, const float* dx_add,
@@ -459,11 +473,11 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
       const int e = 16 * q + 4 * g + r;
       wf[q][r] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (e < a.E)
-        wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * RBWD_COLS + 4 * n);
+        wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * 64 + 4 * n);
     }
   for (int tl = t0; tl < t1; ++tl) {
     const int t = tl * 16 + n;
-    const int64_t o = (int64_t)t * a.H + cg * RBWD_COLS + 16 * g;
+    const int64_t o = (int64_t)t * a.H + cg * 64 + 16 * g;
     f32x4_t acc[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -510,32 +524,33 @@ __device__ __forceinline__ int xcd_item(int b, int n) {
   return (b & 7) * per + (b >> 3);
 }
 
-// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx.
+// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx: both
+// fit a CU together, so one's loads and the other's stores overlap.
 template <typename T, int MT>
-__global__ void __launch_bounds__(RBWD_THREADS)
+__global__ void __launch_bounds__(PROD_THREADS, 2)
 route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
                       const T* __restrict__ w, const T* dx_add, T* dx) {
-  __shared__ __align__(16) float lds[4 * 16 * MT * RBWD_COLS];
+  __shared__ __align__(16) float lds[dw_lds_floats<T, MT>()];
   const int nw = (a.dw_blocks + 7) & ~7;
   if ((int)blockIdx.x < nw) {
     const int item = xcd_item(blockIdx.x, a.dw_blocks);
     if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
   } else {
-    const int nx = (dx_items + RBWD_WAVES - 1) / RBWD_WAVES;
+    const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
     const int b = xcd_item(blockIdx.x - nw, nx);
-    const int item = b * RBWD_WAVES + (threadIdx.x >> 6);
+    const int item = b * PROD_WAVES + (threadIdx.x >> 6);
     if (b < nx && item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
   }
 }
 
 // dW = (dW +) the sum of the ranges' partials, in range order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(PROD_THREADS)
 route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
                     float4* __restrict__ dw) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int i = blockIdx.x * PROD_THREADS + threadIdx.x;
   if (i >= n4) return;
   float4 s = accumulate ? dw[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int p = 0; p < splits; ++p) {
     const float4 v = part[(int64_t)p * n4 + i];
     s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
@@ -547,20 +562,29 @@ int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
   return T > 0 ? (int64_t)route_bwd_plan(d, T).total : 0;
 }
 
+template <typename T, int MT>
+static hipError_t launch_products(const RouteBwdArgs& a, int dx_items, const void* x, const void* w,
+                                  const void* dx_add, void* dx, hipStream_t s) {
+  const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
+  route_products_kernel<T, MT>
+      <<<((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7), PROD_THREADS, 0, s>>>(
+          a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.dw || a.splits == 1) return e;
+  const int n4 = (int)((int64_t)a.E * a.H / 4);
+  route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
+      n4, a.splits, (const float4*)a.part, a.accumulate, (float4*)a.dw);
+  return hipGetLastError();
+}
 template <typename T>
-static void launch_products(const RouteBwdPlan& p, const RouteBwdArgs& a, int dx_items, const void* x,
-                            const void* w, const void* dx_add, void* dx, hipStream_t s) {
-  const int nx = (dx_items + RBWD_WAVES - 1) / RBWD_WAVES;
-  const int grid = ((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7);
-  auto go = [&](auto kernel) {
-    kernel<<<grid, RBWD_THREADS, 0, s>>>(a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add,
-                                         (T*)dx);
-  };
-  switch (p.mt) {
-    case 1: go(route_products_kernel<T, 1>); break;
-    case 2: go(route_products_kernel<T, 2>); break;
-    case 3: go(route_products_kernel<T, 3>); break;
-    default: go(route_products_kernel<T, 4>); break;
+static hipError_t launch_products_t(int mt, const RouteBwdArgs& a, int dx_items, const void* x,
+                                    const void* w, const void* dx_add, void* dx,
+                                    hipStream_t s) {
+  switch (mt) {
+    case 1: return launch_products<T, 1>(a, dx_items, x, w, dx_add, dx, s);
+    case 2: return launch_products<T, 2>(a, dx_items, x, w, dx_add, dx, s);
+    case 3: return launch_products<T, 3>(a, dx_items, x, w, dx_add, dx, s);
+    default: return launch_products<T, 4>(a, dx_items, x, w, dx_add, dx, s);
   }
 }
 
@@ -570,10 +594,11 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
                                  const int32_t* ids, const float* logits, const float* dtopk_w,
                                  const float* dlogits_add, float* dlogits, const void* dx_add,
                                  void* dx, float* dw, int accumulate, void* ws, hipStream_t s) {
-  const int n4 = d.n_experts * d.hidden / 4;
-  const unsigned sum_blocks = (unsigned)((n4 + 255) / 256);
   if (T == 0) {
-    if (dw) route_dw_sum_kernel<<<sum_blocks, 256, 0, s>>>(n4, 0, nullptr, accumulate, (float4*)dw);
+    const int n4 = (int)((int64_t)d.n_experts * d.hidden / 4);
+    if (dw)
+      route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
+          n4, 0, nullptr, accumulate, (float4*)dw);
     return hipGetLastError();
   }
   const RouteBwdPlan p = route_bwd_plan(d, T);
@@ -584,23 +609,14 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
   route_dlogits_kernel<<<p.steps, RBWD_THREADS, 0, s>>>(T, d.n_experts, d.top_k, d.renormalize, ids,
                                                         logits, dtopk_w, dlogits_add, dlogits, p.mt,
                                                         p.ks, fx, fw);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!dx && !dw)) return e;
-  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles,
-                       dw ? p.dw_blocks : 0, dlogits, fx, fw,
+  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles, dw ? p.splits * p.ncg : 0,
+                       dlogits, fx, fw,
                        p.splits > 1 ? reinterpret_cast<float*>(base + p.part) : nullptr, dw, accumulate};
   const int dx_items = dx ? (2 * p.steps + p.dx_tiles - 1) / p.dx_tiles * p.ncg : 0;
-  if (packs)
-    launch_products<bf16>(p, a, dx_items, x, w_router, dx_add, dx, s);
-  else
-    launch_products<float>(p, a, dx_items, x, w_router, dx_add, dx, s);
-  e = hipGetLastError();
-  if (e == hipSuccess && dw && p.splits > 1) {
-    route_dw_sum_kernel<<<sum_blocks, 256, 0, s>>>(n4, p.splits, (const float4*)a.part, accumulate,
-                                                   (float4*)dw);
-    e = hipGetLastError();
-  }
-  return e;
+  if (packs) return launch_products_t<bf16>(p.mt, a, dx_items, x, w_router, dx_add, dx, s);
+  return launch_products_t<float>(p.mt, a, dx_items, x, w_router, dx_add, dx, s);
 }
 
 }  // namespace moe

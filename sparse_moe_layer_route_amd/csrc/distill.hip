@@ -15,24 +15,26 @@
 // the loss is that of lse_tail times (q_T - p_T) only.
 //
 // The student's row is the traffic: read once, its gradient written once.
-//   wave kernel   V <= 512 and K <= 64 (a router over its experts): one wave
-//                 per row, the row in registers, no barriers.
-//   block kernel  one block per row, which it holds in registers as loaded
-//                 (bf16 stays packed) between the maximum, the sum and the
-//                 gradient, so memory sees it once.  Exponentials are formed
-//                 twice rather than kept: that would double the registers.
+//   group kernel  short rows (a router over its experts): 16 or 64 lanes per
+//                 row, the row in registers, no barriers.
+//   block kernel  one block per row, which it holds in registers between the
+//                 maximum, the sum and the gradient, so memory sees it once.
 //   two launches  rows cut into segments, a block each, when the rows alone
 //                 would not fill the GPU or are longer than a block holds: the
 //                 first leaves each segment's sums in the workspace, the second
 //                 joins them and reads its segment again.
-// A row is walked in units of 16 bytes of memory, whatever its alignment; the
-// elements of the first and last unit that belong to other rows, and the
-// teacher's classes, are marked in a bitmap in LDS that the loops test a unit
-// at a time.
+// A block walks a row in units of 16 bytes of memory, whatever its alignment.
+// The teacher's classes, and the elements of other rows in the first and last
+// unit, are set to -inf in the registers before the passes, which then need no
+// tests; the teacher's classes get their own gradient after a barrier.
 #include <algorithm>
-#include <cmath>
 
 #include "common.h"
+
+// z = logit / tau is compared and subtracted in several places: as a rounded
+// value, the same in all of them.  Fused into a subtraction its rounding error
+// would be left over, which beside logits of the type's lowest value is huge.
+#pragma clang fp contract(off)
 
 namespace moe {
 
@@ -46,7 +48,7 @@ struct DistillArgs {
   const float* t_lse;    // may be null
   const float* token_w;  // may be null
   double inv_tau;
-  float c_hi, c_lo;  // log2(e) / tau = c_hi + c_lo, c_lo > 0
+  float c;  // log2(e) / tau
   float scale;
   float* loss;
   int segs, seg_units;    // of a row; seg_units 16-byte units each
@@ -58,100 +60,154 @@ struct SegStat {
   float m, s;  // tail: maximum logit, sum of exp((logit - m) / tau)
   double zm, hs;  // teacher's classes: maximum z, sum of exp(z - zm), each class once
   double A, P;  // sum of p (log p - (z - ref)) with ref = zm (0 if that is -inf), sum of p
-  double cnt;   // number of the teacher's classes
+  int cnt;      // number of the teacher's classes
 };
 
+// The wave reductions of common.h on doubles, a half at a time.
+template <int CTRL, int ROWS, bool BOUND_ZERO>
+__device__ __forceinline__ double dpp_move_d(double old, double v) {
+  const int2 o = __builtin_bit_cast(int2, old), x = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{dpp_move<CTRL, ROWS, BOUND_ZERO>(o.x, x.x),
+                                         dpp_move<CTRL, ROWS, BOUND_ZERO>(o.y, x.y)});
+}
+__device__ __forceinline__ double lane63_d(double v) {
+  const int2 x = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_readlane(x.x, 63),
+                                         __builtin_amdgcn_readlane(x.y, 63)});
+}
 __device__ __forceinline__ double wave_sum_d(double v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  v += dpp_move_d<0x111, 0xf, true>(0.0, v);
+  v += dpp_move_d<0x112, 0xf, true>(0.0, v);
+  v += dpp_move_d<0x114, 0xf, true>(0.0, v);
+  v += dpp_move_d<0x118, 0xf, true>(0.0, v);
+  v += dpp_move_d<0x142, 0xa, false>(0.0, v);
+  v += dpp_move_d<0x143, 0xc, false>(0.0, v);
+  return lane63_d(v);
 }
 __device__ __forceinline__ double wave_max_d(double v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v = fmax(v, __shfl_xor(v, m, 64));
-  return v;
+  v = fmax(v, dpp_move_d<0x111, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x112, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x114, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x118, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x142, 0xa, false>(v, v));
+  v = fmax(v, dpp_move_d<0x143, 0xc, false>(v, v));
+  return lane63_d(v);
 }
 
-// exp((s - m) / tau): the difference is exact or rounded once, and the factor
-// log2(e) / tau is held in two floats, so no error is common to all terms.
-// s = -inf gives 0 (both parts of the factor are positive), NaN stays NaN.
+// exp((s - m) / tau).  The difference first: s and m of the type's lowest value
+// then still give 1, and the rounding of the factor counts by |s - m| only.
 __device__ __forceinline__ float distill_exp(float s, float m, const DistillArgs& a) {
-  const float d = s - m;
-  return __builtin_amdgcn_exp2f(fmaf(d, a.c_hi, d * a.c_lo));
-}
-
-__device__ __forceinline__ double log_add(double a, double b) {
-  if (a != a || b != b) return a + b;  // fmax and fmin would drop a NaN
-  const double hi = fmax(a, b), lo = fmin(a, b);
-  return hi == NEG_INF ? hi : hi + log1p(exp(lo - hi));
+  return __builtin_amdgcn_exp2f((s - m) * a.c);
 }
 
 // Everything the gradient needs of a row, and its loss.
 struct RowResult {
-  double top, lse;  // lse of z - top
+  double zm, qh;  // a teacher's class: q = exp(z - zm) qh
   double M;
   float m, f;  // a tail class's gradient is f exp((logit - m) / tau)
   float loss;
 };
 
-// Joined sums of a row (every lane of the wave passes and gets the same).
-//   m, S: tail; zm, hs: teacher's classes; A: sum of p (log p - (z - top))
+// From the joined sums of a row: m, S of the tail; zm, hs of the teacher's
+// classes; A = sum of p (log p - (z - top)), top = max(m / tau, zm).  All is
+// taken relative to top: beside a maximum of the type's lowest value a
+// logarithm would be lost.  All -inf: NaN from here on.
 __device__ __forceinline__ RowResult finish_row(const DistillArgs& a, double c, double mass, float m,
                                                 double S, double zm, double hs, double A, double top,
                                                 bool has_tail) {
   RowResult r;
-  // all against the larger of the two maxima (all -inf: NaN from here on)
-  const double zt = (double)m * a.inv_tau;
-  const double lse_t = S == 0.0 ? NEG_INF : (zt - top) + log(S);
-  const double lse_h = hs == 0.0 ? NEG_INF : (zm - top) + log(hs);
-  const double lse = log_add(lse_t, lse_h);
-  const double qt = has_tail ? exp(lse_t - lse) : 0.0;
+  const double dt = (double)m * a.inv_tau - top;
+  const double et = exp(dt), eh = exp(zm - top), W = S * et + hs * eh, iW = 1.0 / W;
   const double pt = a.t_lse && has_tail ? fmax(0.0, 1.0 - mass) : 0.0;
-  double kl = A + mass * lse;
-  if (pt > 0.0) kl += pt * (log(pt) - lse_t + lse);
+  double kl = A + mass * log(W);
+  if (pt > 0.0) kl += pt * (log(pt * W / S) - dt);
   const double g = c * a.inv_tau;
-  r.top = top;
-  r.lse = lse;
+  r.zm = zm;
+  r.qh = eh * iW;
   r.M = mass + pt;
   r.m = m == -__builtin_inff() ? 0.f : m;
-  r.f = (float)(S == 0.0 ? 0.0 * qt : g * (qt * r.M - pt) / S);
+  r.f = (float)(S == 0.0 ? 0.0 * W : g * (r.M * et * iW - pt / S));
   r.loss = (float)(c * kl);
   return r;
 }
+// Gradient of a teacher's class of value z and joined mass p.
+__device__ __forceinline__ float head_grad(const DistillArgs& a, double c, const RowResult& r, double z,
+                                           double p) {
+  const double e = z == NEG_INF ? 0.0 : exp(z - r.zm);
+  return (float)(c * a.inv_tau * (e * r.qh * r.M - p));
+}
 
-// ------------------------------------------------------ one wave per row ---
-constexpr int DISTILL_WAVE_V = 512;  // 8 elements a lane
-constexpr int DISTILL_WAVES = 4;     // rows of a block
+// --------------------------------------------- a group of lanes per row ---
+// Reductions over groups of 16 or 64 lanes, the result in every lane.  Within
+// 16: exchanges by 1, 2, then mirrored halves and rows.
+template <int G> __device__ __forceinline__ double group_sum_d(double v) {
+  if (G == 64) return wave_sum_d(v);
+  v += dpp_move_d<0xB1, 0xf, false>(v, v);   // quad_perm 1,0,3,2
+  v += dpp_move_d<0x4E, 0xf, false>(v, v);   // quad_perm 2,3,0,1
+  v += dpp_move_d<0x141, 0xf, false>(v, v);  // row_half_mirror
+  v += dpp_move_d<0x140, 0xf, false>(v, v);  // row_mirror
+  return v;
+}
+template <int G> __device__ __forceinline__ double group_max_d(double v) {
+  if (G == 64) return wave_max_d(v);
+  v = fmax(v, dpp_move_d<0xB1, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x4E, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x141, 0xf, false>(v, v));
+  v = fmax(v, dpp_move_d<0x140, 0xf, false>(v, v));
+  return v;
+}
+template <int CTRL> __device__ __forceinline__ float dpp_move_f(float v) {
+  const int x = __float_as_int(v);
+  return __int_as_float(dpp_move<CTRL, 0xf, false>(x, x));
+}
+template <int G> __device__ __forceinline__ float group_max(float v) {
+  if (G == 64) return wave_max(v);
+  v = fmaxf(v, dpp_move_f<0xB1>(v));
+  v = fmaxf(v, dpp_move_f<0x4E>(v));
+  v = fmaxf(v, dpp_move_f<0x141>(v));
+  return fmaxf(v, dpp_move_f<0x140>(v));
+}
+template <int G> __device__ __forceinline__ float group_sum(float v) {
+  if (G == 64) return wave_sum(v);
+  v += dpp_move_f<0xB1>(v);
+  v += dpp_move_f<0x4E>(v);
+  v += dpp_move_f<0x141>(v);
+  return v + dpp_move_f<0x140>(v);
+}
 
-template <typename T, int NE>
-__global__ void __launch_bounds__(DISTILL_WAVES * MOE_WAVE)
-distill_wave_kernel(DistillArgs a, const T* student, T* dstudent) {
-  __shared__ uint32_t s_bits[DISTILL_WAVES][NE * 2];
-  const int lane = lane_id(), wv = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * DISTILL_WAVES + wv;
-  if (t >= a.T) return;  // no barrier below
+constexpr int GROUP_THREADS = 256;
+
+// Rows of at most G * NE classes and G teacher entries, G lanes each.
+template <typename T, int G, int NE>
+__global__ void __launch_bounds__(GROUP_THREADS)
+distill_group_kernel(DistillArgs a, const T* student, T* dstudent) {
+  constexpr int ROWS = GROUP_THREADS / G, WORDS = (G * NE + 31) / 32;
+  __shared__ uint32_t s_bits[ROWS][WORDS];
+  const int l = threadIdx.x % G, base = lane_id() - l;  // lane in the group, its first lane
+  const int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
+  if (t >= a.T) return;  // no barrier below, and no exchange between groups
   const T* row = student + t * a.ld;
   T* drow = dstudent ? dstudent + t * a.ld : nullptr;
-  uint32_t* bits = s_bits[wv];
+  uint32_t* bits = s_bits[threadIdx.x / G];
   const double c = (double)a.scale * (a.token_w ? (double)a.token_w[t] : 1.0);
   auto clear = [&] {
-    if (lane == 0) a.loss[t] = 0.f;
+    if (l == 0) a.loss[t] = 0.f;
     if (drow)
-      for (int v = lane; v < a.V; v += 64) elem<T>::store(drow, v, 0.f);
+      for (int v = l; v < a.V; v += G) elem<T>::store(drow, v, 0.f);
   };
   if (c == 0.0) return clear();  // a masked row is not read
   float s[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int v = lane + 64 * i;
+    const int v = l + G * i;
     s[i] = v < a.V ? elem<T>::load(row, v) : 0.f;
   }
   // lane k holds entry k
-  const bool slot = lane < a.K;
-  const int id = slot ? a.ids[t * a.K + lane] : -1;
-  const double u = slot ? (double)a.t_logits[t * a.K + lane] * a.inv_tau : 0.0;
+  const bool slot = l < a.K;
+  const int id = slot ? a.ids[t * a.K + l] : -1;
+  const double u = slot ? (double)a.t_logits[t * a.K + l] * a.inv_tau : 0.0;
   const double t_lse = a.t_lse ? (double)a.t_lse[t] : 0.0;
-  if (lane < NE * 2) bits[lane] = 0u;
+  for (int i = l; i < WORDS; i += G) bits[i] = 0u;
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   const bool ok = (unsigned)id < (unsigned)a.V;
   uint32_t old = 0u;
@@ -159,75 +215,79 @@ distill_wave_kernel(DistillArgs a, const T* student, T* dstudent) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   const bool dup = __any(ok && ((old >> (id & 31)) & 1u));
   const double z = ok ? (double)elem<T>::load(row, id) * a.inv_tau : NEG_INF;
-  // own: the first entry of its class; more: the masses of the later ones
+  // own: the first entry of its class
   bool own = ok;
   if (dup)
     for (int j = 0; j < a.K; ++j) {
-      const int idj = __shfl(id, j);  // by the whole wave
-      if (j < lane && idj == id) own = false;
+      const int idj = __shfl(id, base + j);  // by the whole group
+      if (j < l && idj == id) own = false;
     }
   // teacher: log p = (u - ref) - log_sum, in this order (beside a maximum of
   // the type's lowest value the logarithm would be lost)
-  const double um = wave_max_d(ok ? u : NEG_INF);
   const bool has_p = ok && u != NEG_INF;
-  double ref = t_lse, log_sum = 0.0;
-  if (!a.t_lse) {
-    ref = um;
-    if (um > NEG_INF || um != um) log_sum = log(wave_sum_d(has_p ? exp(u - um) : 0.0));
+  double p, lp;
+  if (a.t_lse) {
+    lp = u - t_lse;
+    p = has_p ? exp(lp) : 0.0;
+  } else {
+    const double um = group_max_d<G>(ok ? u : NEG_INF);
+    const double e = has_p ? exp(u - um) : 0.0, sum = group_sum_d<G>(e);
+    lp = (u - um) - log(sum);
+    p = e / sum;
+    if (sum == 0.0) return clear();  // no entry to learn from
   }
-  const double lp = has_p ? (u - ref) - log_sum : NEG_INF;
-  const double p = has_p ? exp(lp) : 0.0;
-  const double mass = wave_sum_d(p);
-  if (!a.t_lse && mass == 0.0) return clear();  // no entry to learn from
+  const double mass = group_sum_d<G>(p);
   double p_class = p;
   if (dup)
     for (int j = 0; j < a.K; ++j) {
-      const double pj = __shfl(p, j);
-      const int idj = __shfl(id, j);
-      if (j != lane && idj == id) p_class += pj;
+      const double pj = __shfl(p, base + j);
+      const int idj = __shfl(id, base + j);
+      if (j != l && idj == id) p_class += pj;
     }
-  const double zm = wave_max_d(z);
-  const double hs = wave_sum_d(own && z != NEG_INF ? exp(z - zm) : 0.0);
-  const int cnt = __popcll(__ballot(own));
+  const double zm = group_max_d<G>(z);
+  const double ez = z != NEG_INF ? exp(z - zm) : 0.0;
+  const double hs = group_sum_d<G>(own ? ez : 0.0);
+  const int cnt = __popcll((__ballot(own) >> base) & (~0ull >> (64 - G)));
   // tail
   float m = -__builtin_inff(), sum = 0.f;
   bool tail[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int v = lane + 64 * i;
+    const int v = l + G * i;
     tail[i] = v < a.V && !((bits[v >> 5] >> (v & 31)) & 1u);
     if (tail[i]) m = fmaxf(m, s[i]);
   }
-  m = wave_max(m);
+  m = group_max<G>(m);
   const float ms = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     s[i] = tail[i] ? distill_exp(s[i], ms, a) : 0.f;
     sum += s[i];
   }
-  const double S = (double)wave_sum(sum);
+  const double S = (double)group_sum<G>(sum);
   const double top = fmax((double)m * a.inv_tau, zm);
-  const double A = wave_sum_d(has_p ? p * (lp - (z - top)) : 0.0);
+  const double A = group_sum_d<G>(has_p ? p * (lp - (z - top)) : 0.0);
   const RowResult r = finish_row(a, c, mass, m, S, zm, hs, A, top, cnt < a.V);
-  if (lane == 0) a.loss[t] = r.loss;
+  if (l == 0) a.loss[t] = r.loss;
   if (!drow) return;
 #pragma unroll
   for (int i = 0; i < NE; ++i)
-    if (tail[i]) elem<T>::store(drow, lane + 64 * i, r.f * s[i]);
-  if (own)
-    elem<T>::store(drow, id, (float)(c * a.inv_tau * (exp((z - r.top) - r.lse) * r.M - p_class)));
+    if (tail[i]) elem<T>::store(drow, l + G * i, r.f * s[i]);
+  if (own) elem<T>::store(drow, id, (float)(c * a.inv_tau * (ez * r.qh * r.M - p_class)));
 }
 
 // ------------------------------------------------- one block per segment ---
 template <typename T> struct raw_unit {
   static constexpr int EPU = 16 / sizeof(T);  // elements of a unit
 };
+__device__ __forceinline__ uint32_t unit_word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 __device__ __forceinline__ float unit_elem(const uint4& v, int i, bf16) {
-  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-  return i & 1 ? bf16_hi(w) : bf16_lo(w);
+  return i & 1 ? bf16_hi(unit_word(v, i >> 1)) : bf16_lo(unit_word(v, i >> 1));
 }
 __device__ __forceinline__ float unit_elem(const uint4& v, int i, float) {
-  return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  return __uint_as_float(unit_word(v, i));
 }
 __device__ __forceinline__ uint4 make_unit(const float (&o)[8], bf16) {
   return make_uint4(f2_to_bf16x2(o[0], o[1]), f2_to_bf16x2(o[2], o[3]), f2_to_bf16x2(o[4], o[5]),
@@ -237,16 +297,62 @@ __device__ __forceinline__ uint4 make_unit(const float (&o)[4], float) {
   return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
                     __float_as_uint(o[3]));
 }
+// -inf into the elements whose bit is set.
+__device__ __forceinline__ uint32_t mask_word(uint32_t w, uint32_t k, bf16) {
+  if (k & 1u) w = (w & 0xFFFF0000u) | 0xFF80u;
+  if (k & 2u) w = (w & 0xFFFFu) | 0xFF800000u;
+  return w;
+}
+__device__ __forceinline__ uint32_t mask_word(uint32_t w, uint32_t k, float) {
+  return (k & 1u) ? 0xFF800000u : w;
+}
+template <typename T> __device__ __forceinline__ uint4 mask_unit(const uint4& v, uint32_t k) {
+  constexpr int PER = 4 / sizeof(T);  // elements of a word
+  return make_uint4(mask_word(v.x, k, T{}), mask_word(v.y, k >> PER, T{}),
+                    mask_word(v.z, k >> (2 * PER), T{}), mask_word(v.w, k >> (3 * PER), T{}));
+}
 
 enum { DISTILL_ROW = 0, DISTILL_STATS = 1, DISTILL_GRAD = 2 };
 
+// Maximum of a thread's units.  bf16 pairs are compared as they are stored:
+// as signed integers positive values keep their order and beat negative ones,
+// so the result is the maximum wherever it is not negative (a NaN of positive
+// sign comes out, and through; a negative one reaches the sum).
+template <int NU> __device__ __forceinline__ float units_max(const uint4 (&x)[NU], float) {
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, unit_elem(x[i], e, 0.f));
+  return m;
+}
+template <int NU> __device__ __forceinline__ float units_max(const uint4 (&x)[NU], bf16) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 k = {-32768, -32768};
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      k = __builtin_elementwise_max(k, __builtin_bit_cast(s16x2, unit_word(x[i], w)));
+  const int b = max((int)k.x, (int)k.y);
+  if (b >= 0) return bf16_to_f((uint16_t)b);
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, unit_elem(x[i], e, bf16{}));
+  return m;
+}
+
 // Segment blockIdx.x of row blockIdx.y (DISTILL_ROW: row blockIdx.x), NT
-// threads of at most NU units each.
-template <typename T, int NT, int NU, int PHASE>
-__global__ void __launch_bounds__(NT)
+// threads of at most NU units each.  OCC: waves a SIMD should hold.
+template <typename T, int NT, int NU, int PHASE, int OCC>
+__global__ void __launch_bounds__(NT, OCC)
 distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   constexpr int EPU = raw_unit<T>::EPU, NW = NT / MOE_WAVE;
   constexpr uint32_t ALL = (1u << EPU) - 1u;
+  // the sum's exponentials are kept for the gradient where they fit
+  constexpr bool KEEP = PHASE == DISTILL_ROW && NU * EPU <= 64;
   extern __shared__ double smem[];
   const int K = a.K, V = a.V, tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
   double* s_lp = smem;                   // [K] log p
@@ -262,43 +368,52 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   const int seg = PHASE == DISTILL_ROW ? 0 : blockIdx.x;
   const T* row = student + t * a.ld;
   T* drow = dstudent ? dstudent + t * a.ld : nullptr;
-  // unit u holds elements u * EPU - ph .. +EPU-1 of the row
+  // unit u holds elements u * EPU - ph .. +EPU-1 of the row; the first and the
+  // last may hold elements of other rows too
   const int ph = (int)((t * a.ld) & (EPU - 1));
-  const int u0 = seg * a.seg_units, u1 = min(u0 + a.seg_units, (V + ph + EPU - 1) / EPU);
+  const int all_units = (V + ph + EPU - 1) / EPU;
+  const int u0 = seg * a.seg_units, u1 = min(u0 + a.seg_units, all_units);
   const int n_units = max(u1 - u0, 0);
+  const int edge0 = ph ? 0 : -1, edge1 = (V + ph) % EPU ? all_units - 1 : -1;
   const double c = (double)a.scale * (a.token_w ? (double)a.token_w[t] : 1.0);
-  auto whole = [&](int u) { return u * EPU >= ph && (u + 1) * EPU <= V + ph; };
+  auto put = [&](int u, const float (&o)[EPU]) {
+    if (u != edge0 && u != edge1) {
+      *reinterpret_cast<uint4*>(drow + (u * EPU - ph)) = make_unit(o, T{});
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPU; ++e)
+        if ((unsigned)(u * EPU - ph + e) < (unsigned)V) elem<T>::store(drow, u * EPU - ph + e, o[e]);
+    }
+  };
   auto clear = [&] {
     if (PHASE == DISTILL_STATS) return;
     if (tid == 0 && seg == 0) a.loss[t] = 0.f;
     if (!drow) return;
-    for (int u = u0 + tid; u < u1; u += NT) {
-      if (whole(u))
-        *reinterpret_cast<uint4*>(drow + (u * EPU - ph)) = make_uint4(0u, 0u, 0u, 0u);
-      else
-        for (int v = max(u * EPU - ph, 0); v < min((u + 1) * EPU - ph, V); ++v)
-          elem<T>::store(drow, v, 0.f);
-    }
+    float o[EPU];
+#pragma unroll
+    for (int e = 0; e < EPU; ++e) o[e] = 0.f;
+    for (int u = u0 + tid; u < u1; u += NT) put(u, o);
   };
   if (c == 0.0) return clear();  // a masked row is not read
   uint4 x[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = u0 + i * NT + tid;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    // units past the segment count as -inf
+    x[i] = mask_unit<T>(make_uint4(0u, 0u, 0u, 0u), ALL);
     if (u >= u1) continue;
-    if (whole(u)) {
+    if (u != edge0 && u != edge1) {
       x[i] = *reinterpret_cast<const uint4*>(row + (u * EPU - ph));
-    } else {  // the elements of other rows are marked below
+    } else {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int e = 0; e < EPU; ++e) {
         const int v = u * EPU - ph + e;
-        if (v < 0 || v >= V) continue;
+        if ((unsigned)v >= (unsigned)V) continue;  // marked below
         if (sizeof(T) == 2)
           w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[v] << (16 * (e & 1));
         else
-          w[e] = reinterpret_cast<const uint32_t*>(row)[v];
+          w[e % 4] = reinterpret_cast<const uint32_t*>(row)[v];
       }
       x[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -306,7 +421,7 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   if (tid == 0) s_dup = 0;
   for (int i = tid; i < (n_units * EPU + 31) / 32; i += NT) bits[i] = 0u;
   __syncthreads();
-  // bit of element v: v + ph - u0 * EPU
+  // bit of element v: v - b0
   const int b0 = u0 * EPU - ph, nb = n_units * EPU;
   for (int i = tid; i < K; i += NT) {
     const int id = a.ids[t * K + i];
@@ -334,55 +449,58 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
         if (s_id[j] == s_id[i]) return false;
     return true;
   };
-  auto marks = [&](int i) -> uint32_t {  // of the thread's unit i
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
     const int q = (i * NT + tid) * EPU;
-    return (bits[q >> 5] >> (q & 31)) & ALL;
-  };
+    if (u0 + i * NT + tid >= u1) continue;
+    const uint32_t k = (bits[q >> 5] >> (q & 31)) & ALL;
+    if (k) x[i] = mask_unit<T>(x[i], k);
+  }
   if (wv == 0) {
-    double um = NEG_INF;
-    for (int i = lane; i < K; i += 64)
-      if (s_id[i] >= 0) um = fmax(um, s_lp[i]);
-    um = wave_max_d(um);
     // log p = (u - ref) - log_sum, in this order: beside a maximum of the
     // type's lowest value the logarithm would be lost
-    double ref = um, log_sum = 0.0;
+    double ref, log_sum = 0.0;
     if (a.t_lse) {
       ref = (double)a.t_lse[t];
     } else {
-      double e = 0.0;
+      double um = NEG_INF, e = 0.0;
       for (int i = lane; i < K; i += 64)
-        if (s_id[i] >= 0 && s_lp[i] != NEG_INF) e += exp(s_lp[i] - um);
+        if (s_id[i] >= 0) um = fmax(um, s_lp[i]);
+      ref = wave_max_d(um);
+      for (int i = lane; i < K; i += 64)
+        if (s_id[i] >= 0 && s_lp[i] != NEG_INF) e += exp(s_lp[i] - ref);
       log_sum = log(wave_sum_d(e));
     }
-    double mass = 0.0, zm = NEG_INF;
-    for (int i = lane; i < K; i += 64) {
-      if (s_id[i] < 0) continue;
-      s_lp[i] = s_lp[i] == NEG_INF ? NEG_INF : (s_lp[i] - ref) - log_sum;
-      mass += exp(s_lp[i]);
-      if (here(i)) zm = fmax(zm, s_z[i]);
+    double zm = NEG_INF;
+    if (PHASE != DISTILL_GRAD) {
+      for (int i = lane; i < K; i += 64)
+        if (here(i)) zm = fmax(zm, s_z[i]);
+      zm = wave_max_d(zm);
+    }
+    const double zr = zm == NEG_INF ? 0.0 : zm;
+    double mass = 0.0, hs = 0.0, A = 0.0, P = 0.0;
+    int cnt = 0;
+    for (int i0 = 0; i0 < K; i0 += 64) {
+      const int i = i0 + lane;
+      const bool ok = i < K && s_id[i] >= 0, in = ok && here(i), first = in && own(i);
+      const double lp = ok && s_lp[i] != NEG_INF ? (s_lp[i] - ref) - log_sum : NEG_INF;
+      const double p = exp(lp);
+      if (ok) s_lp[i] = lp;
+      mass += p;
+      if (PHASE == DISTILL_GRAD) continue;
+      cnt += __popcll(__ballot(first));
+      if (first && s_z[i] != NEG_INF) hs += exp(s_z[i] - zm);
+      if (in && lp != NEG_INF) {
+        P += p;
+        A += p * (lp - (s_z[i] - zr));
+      }
     }
     mass = wave_sum_d(mass);
     if (lane == 0) s_mass = mass;
     if (PHASE != DISTILL_GRAD) {
-      zm = wave_max_d(zm);
-      const double zr = zm == NEG_INF ? 0.0 : zm;
-      double hs = 0.0, A = 0.0, P = 0.0, cnt = 0.0;
-      for (int i = lane; i < K; i += 64) {
-        if (!here(i)) continue;
-        if (own(i)) {
-          cnt += 1.0;
-          if (s_z[i] != NEG_INF) hs += exp(s_z[i] - zm);
-        }
-        if (s_lp[i] != NEG_INF) {
-          const double p = exp(s_lp[i]);
-          P += p;
-          A += p * (s_lp[i] - (s_z[i] - zr));
-        }
-      }
       hs = wave_sum_d(hs);
       A = wave_sum_d(A);
-      P = wave_sum_d(P);
-      cnt = wave_sum_d(cnt);
+      P = PHASE == DISTILL_ROW ? mass : wave_sum_d(P);
       if (lane == 0) {
         s_stat.zm = zm;
         s_stat.hs = hs;
@@ -392,22 +510,9 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
       }
     }
   }
+  float ex[KEEP ? NU : 1][EPU];
   if (PHASE != DISTILL_GRAD) {
-    float m = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      if (u0 + i * NT + tid >= u1) continue;
-      const uint32_t k = marks(i);
-      if (k == 0u) {
-#pragma unroll
-        for (int e = 0; e < EPU; ++e) m = fmaxf(m, unit_elem(x[i], e, T{}));
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPU; ++e)
-          if (!((k >> e) & 1u)) m = fmaxf(m, unit_elem(x[i], e, T{}));
-      }
-    }
-    m = wave_max(m);
+    float m = wave_max(units_max(x, T{}));
     if (lane == 0) s_max[wv] = m;
     __syncthreads();
     m = s_max[0];
@@ -417,15 +522,13 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      if (u0 + i * NT + tid >= u1) continue;
-      const uint32_t k = marks(i);
-      if (k == 0u) {
+      if (i * NT < n_units) {
 #pragma unroll
-        for (int e = 0; e < EPU; ++e) sum += distill_exp(unit_elem(x[i], e, T{}), ms, a);
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPU; ++e)
-          if (!((k >> e) & 1u)) sum += distill_exp(unit_elem(x[i], e, T{}), ms, a);
+        for (int e = 0; e < EPU; ++e) {
+          const float v = distill_exp(unit_elem(x[i], e, T{}), ms, a);
+          if (KEEP) ex[KEEP ? i : 0][e] = v;
+          sum += v;
+        }
       }
     }
     sum = wave_sum(sum);
@@ -446,30 +549,43 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   if (!a.t_lse && mass == 0.0) return clear();  // no entry to learn from
   if (wv == 0) {
     // join the segments (one: the block's own)
-    const SegStat* st = PHASE == DISTILL_ROW ? &s_stat : a.stats + t * a.segs;
-    const int n = PHASE == DISTILL_ROW ? 1 : a.segs;
-    float m = -__builtin_inff();
-    double zm = NEG_INF;
-    for (int i = lane; i < n; i += 64) {
-      m = fmaxf(m, st[i].m);
-      zm = fmax(zm, st[i].zm);
+    float m;
+    double zm, top, S, hs, A;
+    int cnt;
+    if (PHASE == DISTILL_ROW) {
+      m = s_stat.m;
+      zm = s_stat.zm;
+      top = fmax((double)m * a.inv_tau, zm);
+      S = (double)s_stat.s;
+      hs = s_stat.hs;
+      A = mass == 0.0 ? 0.0 : s_stat.A - mass * ((zm == NEG_INF ? 0.0 : zm) - top);
+      cnt = s_stat.cnt;
+    } else {
+      const SegStat* st = a.stats + t * a.segs;
+      m = -__builtin_inff();
+      zm = NEG_INF;
+      for (int i = lane; i < a.segs; i += 64) {
+        m = fmaxf(m, st[i].m);
+        zm = fmax(zm, st[i].zm);
+      }
+      m = wave_max(m);
+      zm = wave_max_d(zm);
+      top = fmax((double)m * a.inv_tau, zm);
+      S = hs = A = 0.0;
+      cnt = 0;
+      for (int i = lane; i < a.segs; i += 64) {
+        const SegStat q = st[i];
+        if (q.s != 0.f) S += (double)q.s * exp(((double)q.m - (double)m) * a.inv_tau);
+        if (q.hs != 0.0) hs += q.hs * exp(q.zm - zm);
+        if (q.P != 0.0) A += q.A - q.P * ((q.zm == NEG_INF ? 0.0 : q.zm) - top);
+        cnt += q.cnt;
+      }
+      S = wave_sum_d(S);
+      hs = wave_sum_d(hs);
+      A = wave_sum_d(A);
+      cnt = __builtin_amdgcn_readlane(wave_incl_scan_i(cnt), 63);
     }
-    m = wave_max(m);
-    zm = wave_max_d(zm);
-    const double top = fmax((double)m * a.inv_tau, zm);
-    double S = 0.0, hs = 0.0, A = 0.0, cnt = 0.0;
-    for (int i = lane; i < n; i += 64) {
-      const SegStat q = st[i];
-      if (q.s != 0.f) S += (double)q.s * exp(((double)q.m - (double)m) * a.inv_tau);
-      if (q.hs != 0.0) hs += q.hs * exp(q.zm - zm);
-      if (q.P != 0.0) A += q.A - q.P * ((q.zm == NEG_INF ? 0.0 : q.zm) - top);
-      cnt += q.cnt;
-    }
-    S = wave_sum_d(S);
-    hs = wave_sum_d(hs);
-    A = wave_sum_d(A);
-    cnt = wave_sum_d(cnt);
-    const RowResult r = finish_row(a, c, mass, m, S, zm, hs, A, top, cnt < (double)V);
+    const RowResult r = finish_row(a, c, mass, m, S, zm, hs, A, top, cnt < V);
     if (lane == 0) {
       s_row = r;
       if (seg == 0) a.loss[t] = r.loss;
@@ -482,26 +598,20 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   for (int i = 0; i < NU; ++i) {
     const int u = u0 + i * NT + tid;
     if (u >= u1) continue;
-    const uint32_t k = marks(i);
     float o[EPU];
 #pragma unroll
-    for (int e = 0; e < EPU; ++e) o[e] = r.f * distill_exp(unit_elem(x[i], e, T{}), r.m, a);
-    if (k == 0u) {
-      *reinterpret_cast<uint4*>(drow + (u * EPU - ph)) = make_unit(o, T{});
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPU; ++e)
-        if (!((k >> e) & 1u)) elem<T>::store(drow, u * EPU - ph + e, o[e]);
-    }
+    for (int e = 0; e < EPU; ++e)
+      o[e] = r.f * (KEEP ? ex[KEEP ? i : 0][e] : distill_exp(unit_elem(x[i], e, T{}), r.m, a));
+    put(u, o);
   }
+  __syncthreads();  // the teacher's classes over what the units wrote there
   for (int i = tid; i < K; i += NT) {
     if (!here(i) || !own(i)) continue;
     double p = exp(s_lp[i]);
     if (s_dup)
       for (int j = i + 1; j < K; ++j)
         if (s_id[j] == s_id[i]) p += exp(s_lp[j]);
-    elem<T>::store(drow, s_id[i],
-                   (float)(c * a.inv_tau * (exp((s_z[i] - r.top) - r.lse) * r.M - p)));
+    elem<T>::store(drow, s_id[i], head_grad(a, c, r, s_z[i], p));
   }
 }
 
@@ -545,22 +655,20 @@ int64_t distill_ws_bytes(int T, int V) {
   return most;
 }
 
-template <typename T, int NT, int NU, int PHASE>
+template <typename T, int NT, int NU, int PHASE, int OCC>
 static void block_launch(const DistillArgs& a, dim3 grid, const T* student, T* dstudent, hipStream_t s) {
   const size_t lds = (size_t)a.K * 20 + (size_t)(a.seg_units * raw_unit<T>::EPU + 31) / 32 * 4;
-  distill_block_kernel<T, NT, NU, PHASE><<<grid, NT, lds, s>>>(a, student, dstudent);
+  distill_block_kernel<T, NT, NU, PHASE, OCC><<<grid, NT, lds, s>>>(a, student, dstudent);
 }
 
 template <typename T>
 static hipError_t distill_t(DistillArgs a, const T* student, T* dstudent, void* ws, hipStream_t s) {
-  if (a.V <= DISTILL_WAVE_V && a.K <= MOE_WAVE) {
-    const int grid = (a.T + DISTILL_WAVES - 1) / DISTILL_WAVES, thr = DISTILL_WAVES * MOE_WAVE;
-    if (a.V <= 64)
-      distill_wave_kernel<T, 1><<<grid, thr, 0, s>>>(a, student, dstudent);
-    else
-      distill_wave_kernel<T, 8><<<grid, thr, 0, s>>>(a, student, dstudent);
+  auto group = [&](auto kernel, int rows) {
+    kernel<<<(a.T + rows - 1) / rows, GROUP_THREADS, 0, s>>>(a, student, dstudent);
     return hipGetLastError();
-  }
+  };
+  if (a.K <= 16 && a.V <= 64) return group(distill_group_kernel<T, 16, 4>, GROUP_THREADS / 16);
+  if (a.K <= 64 && a.V <= 512) return group(distill_group_kernel<T, 64, 8>, GROUP_THREADS / 64);
   const int units = row_units(a.V, sizeof(T));
   distill_segments(a.T, units, &a.segs, &a.seg_units);
   if (a.segs > 1) {
@@ -578,21 +686,21 @@ static hipError_t distill_t(DistillArgs a, const T* student, T* dstudent, void* 
       b.loss += t0;
       b.stats += (int64_t)t0 * a.segs;
       const int64_t at = (int64_t)t0 * a.ld;
-      block_launch<T, SEG_NT, SEG_NU, DISTILL_STATS>(b, dim3(a.segs, n), student + at, nullptr, s);
+      block_launch<T, SEG_NT, SEG_NU, DISTILL_STATS, 1>(b, dim3(a.segs, n), student + at, nullptr, s);
       hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      block_launch<T, SEG_NT, SEG_NU, DISTILL_GRAD>(b, dim3(dstudent ? a.segs : 1, n), student + at,
+      block_launch<T, SEG_NT, SEG_NU, DISTILL_GRAD, 1>(b, dim3(dstudent ? a.segs : 1, n), student + at,
                                                     dstudent ? dstudent + at : nullptr, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;
   }
-  if (units <= 256 * 4)
-    block_launch<T, 256, 4, DISTILL_ROW>(a, a.T, student, dstudent, s);
-  else if (units <= 256 * 16)
-    block_launch<T, 256, 16, DISTILL_ROW>(a, a.T, student, dstudent, s);
+  if (units <= 256 * 8)
+    block_launch<T, 256, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
+  else if (units <= 512 * 8)
+    block_launch<T, 512, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
   else
-    block_launch<T, 1024, 16, DISTILL_ROW>(a, a.T, student, dstudent, s);
+    block_launch<T, 1024, 16, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
   return hipGetLastError();
 }
 
@@ -600,11 +708,8 @@ hipError_t launch_distill(int T, int V, int64_t ld, int K, const void* student, 
                           const int32_t* ids, const float* t_logits, const float* t_lse,
                           const float* token_w, float tau, float scale, float* loss,
                           void* dstudent, void* ws, hipStream_t s) {
-  const double c = 1.4426950408889634 / (double)tau;
-  float hi = (float)c;
-  if ((double)hi >= c) hi = std::nextafter(hi, 0.f);
-  DistillArgs a{T, V, K, ld, ids, t_logits, t_lse, token_w, 1.0 / (double)tau, hi,
-                (float)(c - (double)hi), scale, loss, 1, 0, nullptr};
+  DistillArgs a{T, V, K, ld, ids, t_logits, t_lse, token_w, 1.0 / (double)tau,
+                (float)(1.4426950408889634 / (double)tau), scale, loss, 1, 0, nullptr};
   if (is_bf16) return distill_t(a, (const bf16*)student, (bf16*)dstudent, ws, s);
   return distill_t(a, (const float*)student, (float*)dstudent, ws, s);
 }

@@ -266,7 +266,9 @@ DISTILL = [  # T, V, K, dtype, padded, tau
     (5, 64, 64, "f32", False, 2.0), (37, 65, 8, "bf16", True, 1.0), (9, 1000, 100, "bf16", False, 0.7),
     (17, 4099, 33, "bf16", False, 1.0), (17, 4099, 33, "f32", True, 3.0), (6, 32000, 64, "bf16", False, 2.0),
     (2, 131072, 1024, "bf16", False, 1.0), (3, 100003, 32, "f32", True, 1.5), (300, 2047, 5, "f32", False, 1.0),
-    (257, 20001, 7, "f32", False, 1.0), (256, 40003, 7, "bf16", False, 1.0),
+    (19, 4095, 20, "bf16", False, 1.0), (5, 4088, 20, "f32", True, 1.0), (7, 8185, 70, "bf16", False, 1.0),
+    (4, 16377, 3, "bf16", False, 1.0), (2, 12000, 3, "f32", True, 2.0), (130, 300, 17, "f32", False, 1.0),
+    (33, 500, 16, "bf16", False, 1.0), (257, 20001, 7, "f32", False, 1.0), (256, 40003, 7, "bf16", False, 1.0),
     (260, 66001, 9, "f32", False, 1.0), (64, 511, 65, "bf16", False, 1.0), (9, 512, 64, "f32", True, 1.0),
     (1, 262144, 1, "f32", False, 4.0), (1, 262144, 16, "bf16", False, 1.0), (700, 513, 3, "bf16", False, 1.0),
 ]

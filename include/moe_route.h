@@ -466,7 +466,10 @@ moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* 
  * must be given.  dlogits_add_opt may be dlogits itself, dx_add_opt dx itself.
  * dx_opt needs w_router, dw_router_opt needs x, and both need ws
  * (moe_route_backward_size); either may be NULL.  T = 0 clears dw_router
- * unless it accumulates, and enqueues nothing else.  E * hidden < 2^31. */
+ * unless it accumulates, and enqueues nothing else.  A bf16 layer's products
+ * take dlogits as a sum of bf16 parts (three for dw_router: all of it but
+ * 2^-24; two for dx: 2^-16): where dlogits is not finite they are NaN.
+ * E * hidden < 2^31. */
 moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x_opt,
                                 const void* w_router_opt, const int32_t* topk_ids_opt,
                                 const float* logits_opt, const float* dtopk_w_opt,

@@ -9,9 +9,9 @@
 //   (0 or 1 for moe_route's ids; an expert named twice counts twice).
 //   dx = dx_add + dl W_r,  dW_r = dl^T x.
 //
-// Three launches: the logits' gradient (route_dlogits_kernel), both products
-// in one grid (route_products_kernel), and the sum of dW's token ranges when
-// there is more than one.  The products read x once and write dx once, which
+// Launches: the logits' gradient (route_dlogits_kernel), then both products in
+// one grid (route_products_kernel), or, when dW is cut into ranges of tokens,
+// dW and then dx beside the sum of the ranges.  The products read x once and write dx once, which
 // bounds them (E <= 64: 4 E flops for four bytes of bf16).
 //
 // bf16 layers run v_mfma_f32_16x16x32_bf16 on x and W as they are; dl is fp32
@@ -25,6 +25,7 @@
 // c holding columns 4n + c, so nothing passes through LDS on the way in.
 // fp32 layers run v_mfma_f32_16x16x4_f32, whose operands are single values.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 
@@ -34,7 +35,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int RBWD_THREADS = 512;  // of the logits' gradient
-constexpr int RBWD_WAVES = RBWD_THREADS / MOE_WAVE;
 constexpr int PROD_THREADS = 256;  // of the products
 constexpr int PROD_WAVES = PROD_THREADS / MOE_WAVE;
 constexpr int RBWD_STEP = 32;   // tokens of one dW step (the K of one bf16 MFMA)
@@ -51,10 +51,13 @@ struct RouteBwdPlan {
   size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments, dW partials
 };
 
-// A dx wave takes enough token tiles that about RBWD_DX_WAVES waves run.
+// A dx wave takes as many token tiles as keep all waves to one round of two a
+// SIMD: a few waves more cost a second round (16384 x 3584: 35 us against 30).
 #ifndef RBWD_DX_WAVES
-#define RBWD_DX_WAVES 1024
+#define RBWD_DX_WAVES 2048
 #endif
+// One dW block a CU: more ranges cost more partials than they gain (the same
+// shape: 38 us with 9 ranges, 43 with 18).
 #ifndef RBWD_DW_BLOCKS
 #define RBWD_DW_BLOCKS 256
 #endif
@@ -71,7 +74,8 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   const int most = std::max(1, (p.steps + ways - 1) / ways);
   p.splits = std::min(most, std::max(1, RBWD_DW_BLOCKS / p.ncg));
   const int tiles = 2 * p.steps;
-  p.dx_tiles = std::min(16, std::max(1, (int)((int64_t)tiles * p.ncg / RBWD_DX_WAVES)));
+  const int ranges = std::max(1, RBWD_DX_WAVES / p.ncg);
+  p.dx_tiles = (tiles + ranges - 1) / ranges;
   size_t o = 0;
   auto take = [&](size_t n) {
     const size_t at = o;
@@ -87,93 +91,107 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   return p;
 }
 
-// v = hi + mid + lo with each part a bf16: v rounded, what is left rounded, and
-// so on.
-struct Parts3 {
-  uint16_t p[3];
-};
-__device__ __forceinline__ Parts3 bf16_parts(float v) {
-  Parts3 o;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    o.p[i] = f_to_bf16(v);
-    const float h = bf16_to_f(o.p[i]);
-    v = __builtin_isinf(h) ? 0.f : v - h;  // inf - inf would turn inf into NaN
-  }
-  return o;
+// Reductions and broadcasts within rows of 16 lanes (one token each).
+template <int CTRL> __device__ __forceinline__ float row_move(float v) {
+  const int x = __float_as_int(v);
+  return __int_as_float(dpp_move<CTRL, 0xf, false>(x, x));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += row_move<0xB1>(v);   // quad_perm 1,0,3,2
+  v += row_move<0x4E>(v);   // quad_perm 2,3,0,1
+  v += row_move<0x141>(v);  // row_half_mirror
+  return v + row_move<0x140>(v);  // row_mirror
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, row_move<0xB1>(v));
+  v = fmaxf(v, row_move<0x4E>(v));
+  v = fmaxf(v, row_move<0x141>(v));
+  return fmaxf(v, row_move<0x140>(v));
 }
 
-// One block per 32 tokens, lane = expert, four tokens a wave; dlogits_add may
-// be dlogits itself.  fx / fw (null for fp32 layers): the block's fragments,
+// One block per 32 tokens, 16 lanes a token: lane l holds experts l + 16 q and
+// slot l's id and gradient.  dlogits_add may be dlogits itself.  fx / fw (null
+// for fp32 layers): the block's fragments,
 //   fx [16-token tile][k step][part][lane]: token lane % 16, experts
 //     32 s + 8 (lane / 16) .. +7 (zero past T and E),
 //   fw [32-token step][expert tile][part][lane]: expert lane % 16, tokens
 //     8 (lane / 16) .. +7.
+// The parts of a value are it rounded to bf16, what is left rounded, and so on
+// (a value that is not finite leaves NaN).
 __global__ void __launch_bounds__(RBWD_THREADS)
 route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict__ ids,
                      const float* __restrict__ logits, const float* __restrict__ dtopk_w,
                      const float* dlogits_add, float* dlogits, int mt, int ks,
                      uint4* __restrict__ fx, uint4* __restrict__ fw) {
+  static_assert(RBWD_THREADS == 16 * RBWD_STEP, "16 lanes a token");
+  constexpr int Q = MOE_MAX_EXPERTS / 16;
   __shared__ float tile[RBWD_STEP][MOE_MAX_EXPERTS + 1];
-  constexpr int R = RBWD_STEP / RBWD_WAVES;  // tokens of one wave
-  const int lane = lane_id(), wv = threadIdx.x >> 6;
-  const bool in = lane < E;
-  // Every load of the wave's tokens first (tokens past T, lanes past E and
-  // slots past k read the last one): lane j holds slot j's id and gradient.
-  // Each stage then runs over all R tokens, whose chains are independent.
-  float l[R], dl[R], g[R];
-  int id[R];
-  const int t0 = blockIdx.x * RBWD_STEP + wv * R;
-  if (dtopk_w) {
+  const int tt = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const int t = blockIdx.x * RBWD_STEP + tt;
+  const int64_t tc = min(t, T - 1);  // tokens past T read the last one
+  float dl[Q];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t t = min(t0 + r, T - 1);
-      l[r] = logits[t * E + min(lane, E - 1)];
-      const int64_t o = t * k + min(lane, k - 1);
-      id[r] = ids[o];
-      g[r] = dtopk_w[o];
+  for (int q = 0; q < Q; ++q)
+    dl[q] = dlogits_add ? dlogits_add[tc * E + min(l + 16 * q, E - 1)] : 0.f;
+  if (dtopk_w) {
+    float v[Q], G[Q], n[Q];
+    bool part[Q];
+    const int64_t o = tc * k + min(l, k - 1);
+    const int id = l < k ? ids[o] : -1;  // slots past k match no expert
+    const float g = dtopk_w[o];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      v[q] = logits[tc * E + min(l + 16 * q, E - 1)];
+      G[q] = n[q] = 0.f;
     }
-  }
+    // slot J's id and gradient come from lane J of the token's row
+    auto slot = [&](auto J) {
+      constexpr int j = decltype(J)::value;
+      const int e = dpp_move<0x150 + j, 0xf, false>(id, id) - l;  // row_newbcast
+      const float gj = row_move<0x150 + j>(g);
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    dl[r] = dlogits_add ? dlogits_add[(int64_t)min(t0 + r, T - 1) * E + min(lane, E - 1)] : 0.f;
-  if (dtopk_w) {
-    float G[R], n[R], z[R], s[R], c[R];
-    bool part[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      G[r] = n[r] = 0.f;
-      for (int j = 0; j < k; ++j) {
-        const int e = __builtin_amdgcn_readlane(id[r], j);
-        const float gj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g[r]), j));
-        G[r] += e == lane ? gj : 0.f;
-        n[r] += e == lane ? 1.f : 0.f;
+      for (int q = 0; q < Q; ++q) {
+        G[q] += e == 16 * q ? gj : 0.f;
+        n[q] += e == 16 * q ? 1.f : 0.f;
       }
-      part[r] = in && (!renorm || n[r] > 0.f);
-      s[r] = part[r] ? l[r] : -__builtin_inff();
-    }
+    };
+    slot(std::integral_constant<int, 0>{});
+    slot(std::integral_constant<int, 1>{});
+    slot(std::integral_constant<int, 2>{});
+    slot(std::integral_constant<int, 3>{});
+    slot(std::integral_constant<int, 4>{});
+    slot(std::integral_constant<int, 5>{});
+    slot(std::integral_constant<int, 6>{});
+    slot(std::integral_constant<int, 7>{});
+    float m = -__builtin_inff(), s = 0.f, c = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      z[r] = part[r] ? expf(l[r] - wave_max(s[r])) : 0.f;
-      s[r] = renorm ? n[r] * z[r] : z[r];
+    for (int q = 0; q < Q; ++q) {
+      part[q] = l + 16 * q < E && (!renorm || n[q] > 0.f);
+      m = fmaxf(m, part[q] ? v[q] : -__builtin_inff());
     }
+    m = row_max(m);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float p = z[r] / wave_sum(s[r]);
-      z[r] = part[r] ? p : 0.f;
-      c[r] = in && n[r] > 0.f ? G[r] * p : 0.f;
+    for (int q = 0; q < Q; ++q) {
+      v[q] = part[q] ? expf(v[q] - m) : 0.f;
+      s += renorm ? n[q] * v[q] : v[q];
     }
+    s = row_sum(s);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float cr = wave_sum(c[r]);
-      dl[r] += part[r] ? z[r] * (G[r] - (renorm ? n[r] : 1.f) * cr) : 0.f;
+    for (int q = 0; q < Q; ++q) {
+      v[q] = part[q] ? v[q] / s : 0.f;
+      c += part[q] && n[q] > 0.f ? G[q] * v[q] : 0.f;
     }
+    c = row_sum(c);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      dl[q] += part[q] ? v[q] * (G[q] - (renorm ? n[q] : 1.f) * c) : 0.f;
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const bool on = in && t0 + r < T;
-    if (on) dlogits[(int64_t)(t0 + r) * E + lane] = dl[r];
-    tile[wv * R + r][lane] = on ? dl[r] : 0.f;
+  for (int q = 0; q < Q; ++q) {
+    const int e = l + 16 * q;
+    const bool on = e < E && t < T;
+    if (on) dlogits[(int64_t)t * E + e] = dl[q];
+    tile[tt][e] = on ? dl[q] : 0.f;
   }
   if (!fx && !fw) return;
   __syncthreads();
@@ -183,20 +201,25 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
     const bool to_x = i < nx;
     const int l16 = i & 15, g8 = 8 * ((i >> 4) & 3), f = (to_x ? i : i - nx) >> 6;
     const int half = ks == 2 ? f >> 1 : f, st = ks == 2 ? f & 1 : 0;
-    Parts3 v[8];
+    const float* src = to_x ? &tile[16 * half + l16][32 * st + g8] : &tile[g8][16 * f + l16];
+    const int step = to_x ? 1 : MOE_MAX_EXPERTS + 1;
+    float v[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      v[c] = bf16_parts(to_x ? tile[16 * half + l16][32 * st + g8 + c] : tile[g8 + c][16 * f + l16]);
+    for (int c = 0; c < 8; ++c) v[c] = src[c * step];
     const int parts = to_x ? RBWD_DX_PARTS : RBWD_DW_PARTS;
     uint4* dst = to_x ? fx + ((int64_t)blockIdx.x * 2 * ks + f) * RBWD_DX_PARTS * 64
                       : fw + ((int64_t)blockIdx.x * mt + f) * RBWD_DW_PARTS * 64;
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
-      if (p < parts)
-        dst[p * 64 + (i & 63)] = make_uint4(v[0].p[p] | ((uint32_t)v[1].p[p] << 16),
-                                            v[2].p[p] | ((uint32_t)v[3].p[p] << 16),
-                                            v[4].p[p] | ((uint32_t)v[5].p[p] << 16),
-                                            v[6].p[p] | ((uint32_t)v[7].p[p] << 16));
+    for (int p = 0; p < RBWD_DW_PARTS; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        w[c] = f2_to_bf16x2(v[2 * c], v[2 * c + 1]);
+        v[2 * c] -= bf16_lo(w[c]);
+        v[2 * c + 1] -= bf16_hi(w[c]);
+      }
+      if (p < parts) dst[p * 64 + (i & 63)] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -216,21 +239,28 @@ __device__ __forceinline__ bf16x8_t column_frag(const uint4 (&v)[8], int c) {
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
-// Rows r0 + 8 (lane / 16) .. +7 below n_rows (zero from there on), eight
-// columns each.
-__device__ __forceinline__ void load_rows8(const bf16* __restrict__ p, int r0, int n_rows, int H,
+// Rows r0 + 8 (lane / 16) .. +7, eight columns each, of a matrix whose row 0 is
+// at p: `off` is the lane's byte offset, 8 (lane / 16) rows and its column.  The
+// rest of the address is the same for the wave and stays in scalar registers.
+__device__ __forceinline__ void load_rows8(const bf16* __restrict__ p, int64_t r0, int H, uint32_t off,
                                            uint4 (&v)[8]) {
-  const int r = r0 + 8 * (lane_id() >> 4);
-  if (r0 + RBWD_STEP <= n_rows) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(r + i) * H);
-  } else {
+  for (int i = 0; i < 8; ++i)
+    v[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p + (r0 + i) * H) + off);
+}
+// The same where rows from n_rows on are zero.
+__device__ __forceinline__ void load_rows8_below(const bf16* __restrict__ p, int64_t r0, int n_rows,
+                                                 int H, uint32_t off, uint4 (&v)[8]) {
+  const int left = n_rows - (int)r0 - 8 * (lane_id() >> 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r + i < n_rows) v[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(r + i) * H);
-    }
+  for (int i = 0; i < 8; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < left)
+      v[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p + (r0 + i) * H) + off);
   }
+}
+__device__ __forceinline__ uint32_t rows8_off(int H, int col) {
+  return (uint32_t)(8 * (lane_id() >> 4) * H + col) * 2u;
 }
 
 struct RouteBwdArgs {
@@ -251,53 +281,85 @@ template <int MT> struct DwShape {
 };
 
 // acc[m][c] += the tokens of steps s0, s0 + WAYS, .. below s1: experts of tile
-// m0 + m by the lanes' column c.  Loads retire in order: a step's fragments are
-// asked for before the rows two steps on, so waiting for them leaves two
-// steps' rows in flight.
+// m0 + m by the lanes' column c.  Fragments are asked for one step ahead, rows
+// two, in this order, since loads retire in order: waiting for a step's
+// fragments leaves the rows after them in flight.  A last step that is not
+// whole runs by itself, so that the loop has one way to load its rows.
 template <int MT>
-__device__ __forceinline__ void dw_step(const RouteBwdArgs& a, const bf16* __restrict__ xc, int m0,
-                                        int s, int s1, uint4 (&v)[8],
+struct DwFrags {
+  uint4 f[DwShape<MT>::MW][RBWD_DW_PARTS];
+  __device__ __forceinline__ void load(const RouteBwdArgs& a, int m0, int s) {
+    const char* src = reinterpret_cast<const char*>(a.fw + ((int64_t)s * MT + m0) * RBWD_DW_PARTS * 64);
+    const uint32_t off = lane_id() * 16u;
+#pragma unroll
+    for (int m = 0; m < DwShape<MT>::MW; ++m)
+      if (m0 + m < MT) {
+#pragma unroll
+        for (int p = 0; p < RBWD_DW_PARTS; ++p)
+          f[m][p] = *reinterpret_cast<const uint4*>(src + (m * RBWD_DW_PARTS + p) * 1024 + off);
+      }
+  }
+};
+template <int MT>
+__device__ __forceinline__ void dw_mfma(int m0, const DwFrags<MT>& f, const bf16x8_t (&b)[8],
                                         f32x4_t (&acc)[DwShape<MT>::MW][8]) {
-  constexpr int MW = DwShape<MT>::MW, WAYS = DwShape<MT>::WAYS;
-  uint4 af[MW][RBWD_DW_PARTS];
-  const uint4* f = a.fw + ((int64_t)s * MT + m0) * RBWD_DW_PARTS * 64 + lane_id();
 #pragma unroll
-  for (int m = 0; m < MW; ++m)
-    if (m0 + m < MT) {
-#pragma unroll
-      for (int p = 0; p < RBWD_DW_PARTS; ++p) af[m][p] = f[(m * RBWD_DW_PARTS + p) * 64];
-    }
-  bf16x8_t b[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) b[c] = column_frag(v, c);
-  if (s + 2 * WAYS < s1) load_rows8(xc, (s + 2 * WAYS) * RBWD_STEP, a.T, a.H, v);
-#pragma unroll
-  for (int m = 0; m < MW; ++m)
+  for (int m = 0; m < DwShape<MT>::MW; ++m)
     if (m0 + m < MT) {
 #pragma unroll
       for (int p = RBWD_DW_PARTS - 1; p >= 0; --p)  // smallest part first
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8_t, af[m][p]), b[c], acc[m][c], 0, 0, 0);
+              __builtin_bit_cast(bf16x8_t, f.f[m][p]), b[c], acc[m][c], 0, 0, 0);
     }
 }
 template <int MT>
-__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ xc, int m0,
-                                         int s0, int s1, f32x4_t (&acc)[DwShape<MT>::MW][8]) {
+__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ x, int col,
+                                         int m0, int s0, int s1,
+                                         f32x4_t (&acc)[DwShape<MT>::MW][8]) {
   constexpr int WAYS = DwShape<MT>::WAYS;
-  if (s0 >= s1) return;
+  const uint32_t off = rows8_off(a.H, col);
+  const int whole = a.T / RBWD_STEP;  // steps with all their rows
+  const int e = min(s1, whole);
   uint4 v0[8], v1[8];
-  load_rows8(xc, s0 * RBWD_STEP, a.T, a.H, v0);
-  if (s0 + WAYS < s1) load_rows8(xc, (s0 + WAYS) * RBWD_STEP, a.T, a.H, v1);
-  for (int s = s0; s < s1; s += 2 * WAYS) {
-    dw_step<MT>(a, xc, m0, s, s1, v0, acc);
-    if (s + WAYS < s1) dw_step<MT>(a, xc, m0, s + WAYS, s1, v1, acc);
+  DwFrags<MT> f0, f1;
+  // loads past the end ask for the last step again, unused
+  auto rows = [&](int s, uint4 (&v)[8]) {
+    load_rows8(x, (int64_t)min(s, e - 1) * RBWD_STEP, a.H, off, v);
+  };
+  auto step = [&](int s, uint4 (&v)[8], const DwFrags<MT>& now, DwFrags<MT>& next) {
+    next.load(a, m0, min(s + WAYS, e - 1));
+    // the scheduler would move the loads down to their uses
+    __builtin_amdgcn_sched_barrier(0);
+    bf16x8_t b[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) b[c] = column_frag(v, c);
+    rows(s + 2 * WAYS, v);
+    __builtin_amdgcn_sched_barrier(0);
+    dw_mfma<MT>(m0, now, b, acc);
+  };
+  if (s0 < e) {
+    rows(s0, v0);
+    f0.load(a, m0, s0);
+    rows(s0 + WAYS, v1);
+    for (int s = s0; s < e; s += 2 * WAYS) {
+      step(s, v0, f0, f1);
+      if (s + WAYS < e) step(s + WAYS, v1, f1, f0);
+    }
+  }
+  if (whole < s1 && whole >= s0 && (whole - s0) % WAYS == 0) {
+    f0.load(a, m0, whole);
+    load_rows8_below(x, (int64_t)whole * RBWD_STEP, a.T, a.H, off, v0);
+    bf16x8_t b[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) b[c] = column_frag(v0, c);
+    dw_mfma<MT>(m0, f0, b, acc);
   }
 }
 template <int MT>
-__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ xc, int m0,
-                                         int s0, int s1, f32x4_t (&acc)[DwShape<MT>::MW][4]) {
+__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ x, int col,
+                                         int m0, int s0, int s1, f32x4_t (&acc)[DwShape<MT>::MW][4]) {
   constexpr int MW = DwShape<MT>::MW;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   for (int s = s0; s < s1; s += DwShape<MT>::WAYS) {
@@ -307,7 +369,7 @@ __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __r
     for (int q = 0; q < 8; ++q) {
       const int t = s * RBWD_STEP + 4 * q + g;
       v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < a.T) v[q] = *reinterpret_cast<const float4*>(xc + (int64_t)t * a.H);
+      if (t < a.T) v[q] = *reinterpret_cast<const float4*>(x + (int64_t)t * a.H + col);
 #pragma unroll
       for (int m = 0; m < MW; ++m) {
         const int e = 16 * (m0 + m) + n;
@@ -340,7 +402,8 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
   using S = DwShape<MT>;
   constexpr int NC = rbwd_nc<T>(), COLS = 16 * NC, MW = S::MW, TILE = 16 * MW * COLS;
   const int split = item / a.ncg, cg = item - split * a.ncg;
-  const int lane = lane_id(), wv = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = wv % S::MH, way = wv / S::MH, m0 = half * MW;
   const int per = (a.steps + a.splits - 1) / a.splits;
   const int s0 = split * per, s1 = min(a.steps, s0 + per);
@@ -350,7 +413,7 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // lanes past H read the row's last columns; their results are dropped below
-  dw_steps<MT>(a, x + min(cg * COLS + NC * n, a.H - NC), m0, s0 + way, s1, acc);
+  dw_steps<MT>(a, x, min(cg * COLS + NC * n, a.H - NC), m0, s0 + way, s1, acc);
   auto each = [&](auto f) {
 #pragma unroll
     for (int m = 0; m < MW; ++m)
@@ -399,43 +462,36 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   const int t0 = range * a.dx_tiles, t1 = min(2 * a.steps, t0 + a.dx_tiles);
   bf16x8_t wf[KS][8];
+  const uint32_t w_off = rows8_off(a.H, min(cg * 128 + 8 * (n >> 2) + 32 * (n & 3), a.H - 8));
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     uint4 v[8];
-    load_rows8(w + min(cg * 128 + 8 * (n >> 2) + 32 * (n & 3), a.H - 8), 32 * s, a.E, a.H, v);
+    load_rows8_below(w, 32 * s, a.E, a.H, w_off, v);
 #pragma unroll
     for (int c = 0; c < 8; ++c) wf[s][c] = column_frag(v, c);
   }
-  const int h = cg * 128 + 8 * g;                 // the lane's runs: h + 32 i
-  const int runs = min(4, (a.H - cg * 128) / 32); // 2 or 4 of them inside H
+  const uint32_t off = (uint32_t)(n * a.H + 8 * g) * 2u;  // the lane's runs: 64 i bytes on
+  const int runs = min(4, (a.H - cg * 128) / 32);         // 2 or 4 of them inside H
   // a tile's fragments and addend are asked for before the tile before it is
   // stored: loads and stores retire in one order
   uint4 f[NF], add[4];
   auto load = [&](int tl) {
-    const uint4* src = a.fx + (int64_t)tl * NF * 64 + lane;
+    const char* src = reinterpret_cast<const char*>(a.fx + (int64_t)tl * NF * 64);
+    const uint32_t l16 = lane * 16u;
 #pragma unroll
-    for (int i = 0; i < NF; ++i) f[i] = src[i * 64];
-    if (dx_add) {
-      const uint4* q = reinterpret_cast<const uint4*>(
-          dx_add + (int64_t)min(tl * 16 + n, a.T - 1) * a.H + h);
+    for (int i = 0; i < NF; ++i) f[i] = *reinterpret_cast<const uint4*>(src + i * 1024 + l16);
+    if (dx_add && tl * 16 + n < a.T) {
+      const char* q = reinterpret_cast<const char*>(dx_add + (int64_t)tl * 16 * a.H + cg * 128);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < runs) add[i] = q[4 * i];
+        if (i < runs) add[i] = *reinterpret_cast<const uint4*>(q + 64 * i + off);
     }
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) add[i] = make_uint4(0u, 0u, 0u, 0u);
   load(t0);
   for (int tl = t0; tl < t1; ++tl) {
-    const int t = tl * 16 + n;
     f32x4_t acc[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[2 * q][i] = bf16_lo(word_of(add[i], q));
-        acc[2 * q + 1][i] = bf16_hi(word_of(add[i], q));
-      }
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -443,15 +499,26 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              wf[s][c], __builtin_bit_cast(bf16x8_t, f[s * RBWD_DX_PARTS + p]), acc[c], 0, 0, 0);
+              wf[s][c], __builtin_bit_cast(bf16x8_t, f[s * RBWD_DX_PARTS + p]),
+              s == 0 && p == RBWD_DX_PARTS - 1 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[c], 0, 0, 0);
+    if (dx_add) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[2 * q][i] += bf16_lo(word_of(add[i], q));
+          acc[2 * q + 1][i] += bf16_hi(word_of(add[i], q));
+        }
+    }
     if (tl + 1 < t1) load(tl + 1);
-    if (t < a.T) {
-      uint4* q = reinterpret_cast<uint4*>(dx + (int64_t)t * a.H + h);
+    if (tl * 16 + n < a.T) {
+      char* q = reinterpret_cast<char*>(dx + (int64_t)tl * 16 * a.H + cg * 128);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i < runs)
-          q[4 * i] = make_uint4(f2_to_bf16x2(acc[0][i], acc[1][i]), f2_to_bf16x2(acc[2][i], acc[3][i]),
-                                f2_to_bf16x2(acc[4][i], acc[5][i]), f2_to_bf16x2(acc[6][i], acc[7][i]));
+          *reinterpret_cast<uint4*>(q + 64 * i + off) =
+              make_uint4(f2_to_bf16x2(acc[0][i], acc[1][i]), f2_to_bf16x2(acc[2][i], acc[3][i]),
+                         f2_to_bf16x2(acc[4][i], acc[5][i]), f2_to_bf16x2(acc[6][i], acc[7][i]));
     }
   }
 }
@@ -524,30 +591,35 @@ __device__ __forceinline__ int xcd_item(int b, int n) {
   return (b & 7) * per + (b >> 3);
 }
 
-// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx: both
-// fit a CU together, so one's loads and the other's stores overlap.
+// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the next sum_blocks
+// (a multiple of eight) add the ranges' partials of an earlier launch, the
+// others form dx.
+__device__ __forceinline__ void dw_sum(int i, int n4, int splits, const float4* __restrict__ part,
+                                       int accumulate, float4* __restrict__ dw);
+
 template <typename T, int MT>
 __global__ void __launch_bounds__(PROD_THREADS, 2)
-route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
+route_products_kernel(RouteBwdArgs a, int sum_blocks, int n4, int dx_items, const T* __restrict__ x,
                       const T* __restrict__ w, const T* dx_add, T* dx) {
   __shared__ __align__(16) float lds[dw_lds_floats<T, MT>()];
-  const int nw = (a.dw_blocks + 7) & ~7;
-  if ((int)blockIdx.x < nw) {
-    const int item = xcd_item(blockIdx.x, a.dw_blocks);
+  const int nw = (a.dw_blocks + 7) & ~7, b0 = blockIdx.x;
+  if (b0 < nw) {
+    const int item = xcd_item(b0, a.dw_blocks);
     if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
+  } else if (b0 < nw + sum_blocks) {
+    dw_sum((b0 - nw) * PROD_THREADS + threadIdx.x, n4, a.splits, (const float4*)a.part, a.accumulate,
+           (float4*)a.dw);
   } else {
     const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
-    const int b = xcd_item(blockIdx.x - nw, nx);
-    const int item = b * PROD_WAVES + (threadIdx.x >> 6);
+    const int b = xcd_item(b0 - nw - sum_blocks, nx);
+    const int item = b * PROD_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (b < nx && item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
   }
 }
 
 // dW = (dW +) the sum of the ranges' partials, in range order.
-__global__ void __launch_bounds__(PROD_THREADS)
-route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
-                    float4* __restrict__ dw) {
-  const int i = blockIdx.x * PROD_THREADS + threadIdx.x;
+__device__ __forceinline__ void dw_sum(int i, int n4, int splits, const float4* __restrict__ part,
+                                       int accumulate, float4* __restrict__ dw) {
   if (i >= n4) return;
   float4 s = accumulate ? dw[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -557,24 +629,44 @@ route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int acc
   }
   dw[i] = s;
 }
+// The sum alone; splits = 0 clears dW.
+__global__ void __launch_bounds__(PROD_THREADS)
+route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
+                    float4* __restrict__ dw) {
+  dw_sum(blockIdx.x * PROD_THREADS + threadIdx.x, n4, splits, part, accumulate, dw);
+}
 
 int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
   return T > 0 ? (int64_t)route_bwd_plan(d, T).total : 0;
 }
 
+// With one range of tokens both products go out in one launch.  With several,
+// dW goes first and its ranges are summed beside dx: run together, the two
+// streams cost more than one after the other (16384 x 3584, 64 experts: 77 us
+// against 37 + 28), and the sum needs all of dW.
 template <typename T, int MT>
-static hipError_t launch_products(const RouteBwdArgs& a, int dx_items, const void* x, const void* w,
+static hipError_t launch_products(RouteBwdArgs a, int dx_items, const void* x, const void* w,
                                   const void* dx_add, void* dx, hipStream_t s) {
-  const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
-  route_products_kernel<T, MT>
-      <<<((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7), PROD_THREADS, 0, s>>>(
-          a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.dw || a.splits == 1) return e;
+  const int nx = ((dx_items + PROD_WAVES - 1) / PROD_WAVES + 7) & ~7;
   const int n4 = (int)((int64_t)a.E * a.H / 4);
-  route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
-      n4, a.splits, (const float4*)a.part, a.accumulate, (float4*)a.dw);
-  return hipGetLastError();
+  int nw = (a.dw_blocks + 7) & ~7, sum_blocks = 0;
+  auto go = [&](int grid, int items) {
+    route_products_kernel<T, MT><<<grid, PROD_THREADS, 0, s>>>(
+        a, sum_blocks, n4, items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
+    return hipGetLastError();
+  };
+  if (nw > 0 && a.splits > 1) {
+    const hipError_t e = go(nw, 0);
+    if (e != hipSuccess) return e;
+    nw = a.dw_blocks = 0;
+    sum_blocks = ((n4 + PROD_THREADS - 1) / PROD_THREADS + 7) & ~7;
+    if (dx_items == 0) {
+      route_dw_sum_kernel<<<sum_blocks, PROD_THREADS, 0, s>>>(n4, a.splits, (const float4*)a.part,
+                                                              a.accumulate, (float4*)a.dw);
+      return hipGetLastError();
+    }
+  }
+  return go(nw + sum_blocks + nx, dx_items);
 }
 template <typename T>
 static hipError_t launch_products_t(int mt, const RouteBwdArgs& a, int dx_items, const void* x,

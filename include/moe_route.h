@@ -469,7 +469,7 @@ moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* 
  * unless it accumulates, and enqueues nothing else.  A bf16 layer's products
  * take dlogits as a sum of bf16 parts (three for dw_router: all of it but
  * 2^-24; two for dx: 2^-16): where dlogits is not finite they are NaN.
- * E * hidden < 2^31. */
+ * E * hidden < 2^31 and hidden <= 2^24. */
 moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x_opt,
                                 const void* w_router_opt, const int32_t* topk_ids_opt,
                                 const float* logits_opt, const float* dtopk_w_opt,

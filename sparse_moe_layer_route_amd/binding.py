@@ -162,6 +162,10 @@ class Dims:
     tie_margin: float = 1e-4
     weight_layout: str = "rows"      # "rows" or "mfma16" (see pack_weights)
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_struct", None)   # _dims' converted copy
+
     def c(self) -> MoeDims:
         return MoeDims(self.hidden, self.n_experts, self.top_k, self.inter, self.n_shared,
                        self.shared_inter, self.lore_rank, int(self.renormalize),
@@ -188,10 +192,10 @@ def _ptr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -208,7 +212,12 @@ def _mode(mode) -> int:
 
 
 def _dims(d) -> MoeDims:
-    return d.c() if isinstance(d, Dims) else d
+    if not isinstance(d, Dims):
+        return d
+    c = d.__dict__.get("_struct")    # converted once, until a field changes
+    if c is None:
+        c = d.__dict__["_struct"] = d.c()
+    return c
 
 
 # ------------------------------------------------------------- entry points --
@@ -429,7 +438,7 @@ def moe_dispatch(dims, T, x, inv, x_perm, stream=None):
     dt, P = _TORCH_DTYPES[d.dtype], T * d.top_k
     _check(_lib.moe_dispatch(ctypes.byref(d), T, _arg(dev, "x", x, T * d.hidden, dt),
                              _arg(dev, "inv", inv, P, torch.int32),
-                             _arg(dev, "x_perm", x_perm, P * d.hidden, dt), _stream(stream)),
+                             _arg(dev, "x_perm", x_perm, P * d.hidden, dt), _stream(stream, dev)),
            "moe_dispatch")
 
 
@@ -442,7 +451,7 @@ def moe_undispatch(dims, T, y_perm, inv, topk_w, out, add=None, stream=None):
                                _arg(dev, "inv", inv, P, torch.int32),
                                _arg(dev, "topk_w", topk_w, P, torch.float32, True),
                                _arg(dev, "add", add, T * H, dt, True), _arg(dev, "out", out, T * H, dt),
-                               _stream(stream)), "moe_undispatch")
+                               _stream(stream, dev)), "moe_undispatch")
 
 
 def moe_undispatch_backward(dims, T, dout, y_perm, inv, topk_w, dy_perm, dtopk_w, stream=None):
@@ -456,7 +465,7 @@ def moe_undispatch_backward(dims, T, dout, y_perm, inv, topk_w, dy_perm, dtopk_w
         _arg(dev, "y_perm", y_perm, P * H, rows.dtype, True), row, _arg(dev, "inv", inv, P, torch.int32),
         _arg(dev, "topk_w", topk_w, P, torch.float32, True),
         _arg(dev, "dy_perm", dy_perm, P * H, rows.dtype, True),
-        _arg(dev, "dtopk_w", dtopk_w, P, torch.float32, True), _stream(stream)),
+        _arg(dev, "dtopk_w", dtopk_w, P, torch.float32, True), _stream(stream, dev)),
         "moe_undispatch_backward")
 
 
@@ -479,7 +488,7 @@ def moe_route_backward(dims, T, x, w_router, topk_ids, logits, dtopk_w, dlogits,
         _arg(dev, "dtopk_w", dtopk_w, P, f32, True), _arg(dev, "dlogits_add", dlogits_add, T * E, f32, True),
         _arg(dev, "dlogits", dlogits, T * E, f32), _arg(dev, "dx_add", dx_add, T * H, dt, True),
         _arg(dev, "dx", dx, T * H, dt, True), _arg(dev, "dw_router", dw_router, E * H, f32, True),
-        int(accumulate_dw), ws_p, ws_n, _stream(stream)), "moe_route_backward")
+        int(accumulate_dw), ws_p, ws_n, _stream(stream, dev)), "moe_route_backward")
 
 
 def moe_distill_topk_size(T, V) -> int:
@@ -504,7 +513,7 @@ def moe_distill_topk(T, V, K, student, teacher_ids, teacher_logits, loss, dstude
         _arg(dev, "teacher_lse", teacher_lse, T, torch.float32, True),
         _arg(dev, "token_w", token_w, T, torch.float32, True), float(temperature), float(scale),
         _arg(dev, "loss", loss, T, torch.float32), _arg(dev, "dstudent", dstudent, n, student.dtype, True),
-        ws_p, ws_n, _stream(stream)), "moe_distill_topk")
+        ws_p, ws_n, _stream(stream, dev)), "moe_distill_topk")
 
 
 # ------------------------------------------------- exact miss execution --

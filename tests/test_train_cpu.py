@@ -136,6 +136,8 @@ def test_route_backward_refusals():
                                      ctypes.byref(n)) == B.MOE_EUNSUPPORTED
     assert L.moe_route_backward_size(ctypes.byref(dims(hidden=1 << 26, n_experts=32, inter=16).c()), 1,
                                      ctypes.byref(n)) == B.MOE_EUNSUPPORTED      # E * H = 2^31
+    assert L.moe_route_backward_size(ctypes.byref(dims(hidden=(1 << 24) + 64, inter=16).c()), 1,
+                                     ctypes.byref(n)) == B.MOE_EUNSUPPORTED
     for kw in [dict(dl=None), dict(dtopk_w=None), dict(ids=None), dict(logits=None), dict(w=None),
                dict(x=None), dict(acc=2), dict(ws=None), dict(dx=None, dx_add=at(7)),
                dict(dx=at(0)), dict(dl=at(3)), dict(dw=at(6)), dict(dl_add=at(6) + 16),

@@ -19,12 +19,13 @@ namespace moe {
 
 constexpr int DISPATCH_THREADS = 256;
 
-template <typename T> struct unit8;  // eight elements as loaded
-template <> struct unit8<bf16> {
+// N elements as loaded: 16 bytes of the layer's type (8 bf16, 4 fp32), and as
+// many elements of fp32 rows beside a bf16 layer (32 bytes).
+template <typename T, int N> struct unit;
+template <> struct unit<bf16, 8> {
   uint4 a;
   __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = a; }
-  __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
     v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
@@ -34,26 +35,29 @@ template <> struct unit8<bf16> {
                    f2_to_bf16x2(v[6], v[7]));
   }
 };
-template <> struct unit8<float> {
-  float4 a, b;
+template <int N> struct unit<float, N> {
+  float4 a[N / 4];
   __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) a[i] = reinterpret_cast<const float4*>(p)[i];
   }
   __device__ __forceinline__ void store(float* p) const {
-    *reinterpret_cast<float4*>(p) = a;
-    *reinterpret_cast<float4*>(p + 4) = b;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) reinterpret_cast<float4*>(p)[i] = a[i];
   }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void get(float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      v[4 * i] = a[i].x; v[4 * i + 1] = a[i].y; v[4 * i + 2] = a[i].z; v[4 * i + 3] = a[i].w;
+    }
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void set(const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      a[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   }
 };
+template <typename T> constexpr int unit_elems() { return 16 / (int)sizeof(T); }
 
 // One thread per (token, unit), flat over the batch.
 template <typename T>
@@ -63,11 +67,12 @@ dispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P, const T* _
   const uint32_t g = blockIdx.x * DISPATCH_THREADS + threadIdx.x;
   if (g >= n) return;
   const uint32_t t = g / units, u = g - t * units;
-  unit8<T> v;
-  v.load(x + (int64_t)g * 8);
+  constexpr int N = unit_elems<T>();
+  unit<T, N> v;
+  v.load(x + (int64_t)g * N);
   for (int j = 0; j < k; ++j) {
     const uint32_t row = (uint32_t)inv[(int64_t)t * k + j];
-    if (row < P) v.store(x_perm + (int64_t)row * H + u * 8);
+    if (row < P) v.store(x_perm + (int64_t)row * H + u * N);
   }
 }
 
@@ -82,13 +87,16 @@ undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
   const uint32_t g = blockIdx.x * DISPATCH_THREADS + threadIdx.x;
   if (g >= n) return;
   const uint32_t t = g / units, u = g - t * units;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int N = unit_elems<T>();
+  float acc[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) acc[c] = 0.f;
   if (add) {
-    unit8<T> a;
-    a.load(add + (int64_t)g * 8);
+    unit<T, N> a;
+    a.load(add + (int64_t)g * N);
     a.get(acc);
   }
-  unit8<Ty> v[MOE_MAX_TOPK];
+  unit<Ty, N> v[MOE_MAX_TOPK];
   float w[MOE_MAX_TOPK];
   bool live[MOE_MAX_TOPK];
 #pragma unroll
@@ -98,82 +106,106 @@ undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
     live[j] = row < P;
     w[j] = 1.f;
     if (live[j]) {
-      v[j].load(y_perm + (int64_t)row * H + u * 8);
+      v[j].load(y_perm + (int64_t)row * H + u * N);
       if (topk_w) w[j] = topk_w[o];
     }
   }
 #pragma unroll
   for (int j = 0; j < MOE_MAX_TOPK; ++j) {
     if (!live[j]) continue;
-    float f[8];
+    float f[N];
     v[j].get(f);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[j], f[c], acc[c]);
+    for (int c = 0; c < N; ++c) acc[c] = fmaf(w[j], f[c], acc[c]);
   }
-  unit8<T> o;
+  unit<T, N> o;
   o.set(acc);
-  o.store(out + (int64_t)g * 8);
+  o.store(out + (int64_t)g * N);
 }
 
-// One group of G lanes per token (G the power of two that covers the row's
-// units, at most a wave): each lane walks its units with all slots' rows in
-// flight, then the lanes' partial dots meet in a fixed tree.
-template <typename T, typename Ty, int G, bool DY, bool DW>
+// One group of G lanes per token (up to a wave: the power of two that covers the
+// row's units; 256: a block).  Each lane walks its units, U of them with up to
+// KM slots' rows in flight, then the lanes' partial dots meet in a fixed tree
+// (and a block's four waves in wave order).
+template <typename T, typename Ty, int G, int KM, bool DY, bool DW>
 __global__ void __launch_bounds__(DISPATCH_THREADS)
 undispatch_bwd_kernel(int T_, int units, int H, int k, uint32_t P, const T* __restrict__ dout,
                       const Ty* __restrict__ y_perm, const int32_t* __restrict__ inv,
                       const float* __restrict__ topk_w, Ty* __restrict__ dy_perm,
                       float* __restrict__ dtopk_w) {
+  constexpr int N = unit_elems<T>(), U = MOE_MAX_TOPK / KM;
   const int l = threadIdx.x % G;
   const int t = blockIdx.x * (DISPATCH_THREADS / G) + threadIdx.x / G;
   if (t >= T_) return;  // whole groups leave together
-  uint32_t row[MOE_MAX_TOPK];
-  float w[MOE_MAX_TOPK], dot[MOE_MAX_TOPK];
+  uint32_t row[KM];
+  float w[KM], dot[KM];
 #pragma unroll
-  for (int j = 0; j < MOE_MAX_TOPK; ++j) {
+  for (int j = 0; j < KM; ++j) {
     const int64_t o = (int64_t)t * k + j;
     row[j] = j < k ? (uint32_t)inv[o] : 0xFFFFFFFFu;
     w[j] = DY && j < k ? topk_w[o] : 0.f;
     dot[j] = 0.f;
   }
-  for (int u = l; u < units; u += G) {
-    unit8<T> d;
-    d.load(dout + (int64_t)t * H + u * 8);
-    unit8<Ty> y[MOE_MAX_TOPK];
-    if (DW) {
+  for (int u0 = l; u0 < units; u0 += U * G) {
+    unit<T, N> d[U];
+    unit<Ty, N> y[U][KM];
 #pragma unroll
-      for (int j = 0; j < MOE_MAX_TOPK; ++j)
-        if (row[j] < P) y[j].load(y_perm + (int64_t)row[j] * H + u * 8);
-    }
-    float df[8];
-    d.get(df);
-#pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      if (row[j] >= P) continue;
+    for (int q = 0; q < U; ++q) {
+      const int u = u0 + q * G;
+      if (q > 0 && u >= units) break;
+      d[q].load(dout + (int64_t)t * H + u * N);
       if (DW) {
-        float f[8];
-        y[j].get(f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) dot[j] = fmaf(df[c], f[c], dot[j]);
+        for (int j = 0; j < KM; ++j)
+          if (row[j] < P) y[q][j].load(y_perm + (int64_t)row[j] * H + u * N);
       }
-      if (DY) {
-        float o[8];
+    }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) o[c] = w[j] * df[c];
-        unit8<Ty> ov;
-        ov.set(o);
-        ov.store(dy_perm + (int64_t)row[j] * H + u * 8);
+    for (int q = 0; q < U; ++q) {
+      const int u = u0 + q * G;
+      if (q > 0 && u >= units) break;
+      float df[N];
+      d[q].get(df);
+#pragma unroll
+      for (int j = 0; j < KM; ++j) {
+        if (row[j] >= P) continue;
+        if (DW) {
+          float f[N];
+          y[q][j].get(f);
+#pragma unroll
+          for (int c = 0; c < N; ++c) dot[j] = fmaf(df[c], f[c], dot[j]);
+        }
+        if (DY) {
+          float o[N];
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[c] = w[j] * df[c];
+          unit<Ty, N> ov;
+          ov.set(o);
+          ov.store(dy_perm + (int64_t)row[j] * H + u * N);
+        }
       }
     }
   }
-  if (DW) {
+  if (!DW) return;
+  __shared__ float part[KM][DISPATCH_THREADS / MOE_WAVE];
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      if (j >= k) break;
-      float s = dot[j];
+  for (int j = 0; j < KM; ++j) {
+    float s = dot[j];
 #pragma unroll
-      for (int m = G / 2; m > 0; m >>= 1) s += __shfl_xor(s, m, G);
-      if (l == 0) dtopk_w[(int64_t)t * k + j] = s;
+    for (int m = (G < MOE_WAVE ? G : MOE_WAVE) / 2; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
+    if (G <= MOE_WAVE) {
+      if (l == 0 && j < k) dtopk_w[(int64_t)t * k + j] = s;
+    } else if (l % MOE_WAVE == 0) {
+      part[j][l / MOE_WAVE] = s;
+    }
+  }
+  if (G > MOE_WAVE) {
+    __syncthreads();
+    if (l < k) {
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < DISPATCH_THREADS / MOE_WAVE; ++v) s += part[l][v];
+      dtopk_w[(int64_t)t * k + l] = s;
     }
   }
 }
@@ -181,7 +213,7 @@ undispatch_bwd_kernel(int T_, int units, int H, int k, uint32_t P, const T* __re
 template <typename T>
 static void dispatch_t(const moe_dims_t& d, int T_, const void* x, const int32_t* inv, void* x_perm,
                        hipStream_t s) {
-  const uint32_t units = d.hidden / 8, n = (uint32_t)T_ * units;
+  const uint32_t units = d.hidden / unit_elems<T>(), n = (uint32_t)T_ * units;
   dispatch_kernel<T><<<(n + DISPATCH_THREADS - 1) / DISPATCH_THREADS, DISPATCH_THREADS, 0, s>>>(
       n, units, d.hidden, d.top_k, (uint32_t)T_ * d.top_k, (const T*)x, inv, (T*)x_perm);
 }
@@ -198,7 +230,7 @@ hipError_t launch_dispatch(const moe_dims_t& d, int T, const void* x, const int3
 template <typename T, typename Ty>
 static void undispatch_t(const moe_dims_t& d, int T_, const void* y, const int32_t* inv,
                          const float* w, const void* add, void* out, hipStream_t s) {
-  const uint32_t units = d.hidden / 8, n = (uint32_t)T_ * units;
+  const uint32_t units = d.hidden / unit_elems<T>(), n = (uint32_t)T_ * units;
   undispatch_kernel<T, Ty>
       <<<(n + DISPATCH_THREADS - 1) / DISPATCH_THREADS, DISPATCH_THREADS, 0, s>>>(
           n, units, d.hidden, d.top_k, (uint32_t)T_ * d.top_k, (const Ty*)y, inv, w, (const T*)add,
@@ -228,33 +260,46 @@ struct UndispatchBwd {
   hipStream_t s;
 };
 
-template <typename T, typename Ty, int G, bool DY, bool DW>
+template <typename T, typename Ty, int G, int KM, bool DY, bool DW>
 static void bwd_launch(const UndispatchBwd& a) {
   constexpr int per = DISPATCH_THREADS / G;
-  undispatch_bwd_kernel<T, Ty, G, DY, DW><<<(a.T + per - 1) / per, DISPATCH_THREADS, 0, a.s>>>(
-      a.T, a.d.hidden / 8, a.d.hidden, a.d.top_k, (uint32_t)a.T * a.d.top_k, (const T*)a.dout,
-      (const Ty*)a.y_perm, a.inv, a.w, (Ty*)a.dy, a.dw);
+  undispatch_bwd_kernel<T, Ty, G, KM, DY, DW><<<(a.T + per - 1) / per, DISPATCH_THREADS, 0, a.s>>>(
+      a.T, a.d.hidden / unit_elems<T>(), a.d.hidden, a.d.top_k, (uint32_t)a.T * a.d.top_k,
+      (const T*)a.dout, (const Ty*)a.y_perm, a.inv, a.w, (Ty*)a.dy, a.dw);
 }
-template <typename T, typename Ty, int G>
+template <typename T, typename Ty, int G, int KM>
 static void bwd_outputs(const UndispatchBwd& a) {
   if (a.dy && a.dw)
-    bwd_launch<T, Ty, G, true, true>(a);
+    bwd_launch<T, Ty, G, KM, true, true>(a);
   else if (a.dy)
-    bwd_launch<T, Ty, G, true, false>(a);
+    bwd_launch<T, Ty, G, KM, true, false>(a);
   else
-    bwd_launch<T, Ty, G, false, true>(a);
+    bwd_launch<T, Ty, G, KM, false, true>(a);
 }
-template <typename T, typename Ty>
+// A block per token for rows of more than a wave's units, when there are few
+// tokens (256 x 4096 top-8: 11.3 us against 14.6 with a wave per token) or its
+// waves are nearly always busy (2048 x 2048: 31 against 37); a row that leaves
+// many of them idle is better off with a wave (16384 x 1088, 136 units: 26
+// against 50).
+template <typename T, typename Ty, int KM>
 static void bwd_group(const UndispatchBwd& a) {
-  const int units = a.d.hidden / 8;
-  if (units <= 8)
-    bwd_outputs<T, Ty, 8>(a);
-  else if (units <= 16)
-    bwd_outputs<T, Ty, 16>(a);
-  else if (units <= 32)
-    bwd_outputs<T, Ty, 32>(a);
+  const int units = a.d.hidden / unit_elems<T>(), B = DISPATCH_THREADS;
+  const bool full = 8 * units >= 7 * ((units + B - 1) / B * B);
+  if (units <= 16)
+    bwd_outputs<T, Ty, 16, KM>(a);
+  else if (units > MOE_WAVE && (full || a.T <= 1024))
+    bwd_outputs<T, Ty, DISPATCH_THREADS, KM>(a);
   else
-    bwd_outputs<T, Ty, 64>(a);
+    bwd_outputs<T, Ty, MOE_WAVE, KM>(a);
+}
+// Up to two slots: four units of a lane at once, to have as many loads in
+// flight as eight slots have.
+template <typename T, typename Ty>
+static void bwd_slots(const UndispatchBwd& a) {
+  if (a.d.top_k <= 2)
+    bwd_group<T, Ty, 2>(a);
+  else
+    bwd_group<T, Ty, MOE_MAX_TOPK>(a);
 }
 
 // At least one of dy and dw is not null; y_perm is read only for dw, topk_w
@@ -264,11 +309,11 @@ hipError_t launch_undispatch_backward(const moe_dims_t& d, int T, const void* do
                                       const float* topk_w, void* dy, float* dw, hipStream_t s) {
   const UndispatchBwd a{d, T, dout, y_perm, inv, topk_w, dy, dw, s};
   if (d.dtype != MOE_BF16)
-    bwd_group<float, float>(a);
+    bwd_slots<float, float>(a);
   else if (rows_bf16)
-    bwd_group<bf16, bf16>(a);
+    bwd_slots<bf16, bf16>(a);
   else
-    bwd_group<bf16, float>(a);
+    bwd_slots<bf16, float>(a);
   return hipGetLastError();
 }
 

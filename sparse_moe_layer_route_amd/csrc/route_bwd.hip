@@ -48,7 +48,8 @@ struct RouteBwdPlan {
   int mt, ks, steps, ncg;
   int splits;              // token ranges of dW
   int dx_tiles;            // 16-token tiles of one dx wave
-  size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments, dW partials
+  size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments (fp32 layers: padded
+                               // dlogits at fx), dW partials
 };
 
 // A dx wave takes as many token tiles as keep all waves to one round of two a
@@ -85,6 +86,8 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   if (d.dtype == MOE_BF16) {
     p.fx = take((size_t)tiles * p.ks * RBWD_DX_PARTS * 1024);
     p.fw = take((size_t)p.steps * p.mt * RBWD_DW_PARTS * 1024);
+  } else {
+    p.fx = take((size_t)p.steps * RBWD_STEP * p.mt * 16 * 4);
   }
   if (p.splits > 1) p.part = take((size_t)p.splits * d.n_experts * d.hidden * 4);
   p.total = o;
@@ -110,8 +113,9 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // One block per 32 tokens, 16 lanes a token: lane l holds experts l + 16 q and
-// slot l's id and gradient.  dlogits_add may be dlogits itself.  fx / fw (null
-// for fp32 layers): the block's fragments,
+// slot l's id and gradient.  dlogits_add may be dlogits itself.  pad (fp32
+// layers, else null): dlogits again as [32 steps][16 mt], zero past T and E.
+// fx / fw (bf16 layers, else null): the block's fragments,
 //   fx [16-token tile][k step][part][lane]: token lane % 16, experts
 //     32 s + 8 (lane / 16) .. +7 (zero past T and E),
 //   fw [32-token step][expert tile][part][lane]: expert lane % 16, tokens
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(RBWD_THREADS)
 route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict__ ids,
                      const float* __restrict__ logits, const float* __restrict__ dtopk_w,
                      const float* dlogits_add, float* dlogits, int mt, int ks,
-                     uint4* __restrict__ fx, uint4* __restrict__ fw) {
+                     float* __restrict__ pad, uint4* __restrict__ fx, uint4* __restrict__ fw) {
   static_assert(RBWD_THREADS == 16 * RBWD_STEP, "16 lanes a token");
   constexpr int Q = MOE_MAX_EXPERTS / 16;
   __shared__ float tile[RBWD_STEP][MOE_MAX_EXPERTS + 1];
@@ -191,6 +195,7 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
     const int e = l + 16 * q;
     const bool on = e < E && t < T;
     if (on) dlogits[(int64_t)t * E + e] = dl[q];
+    if (pad && q < mt) pad[(int64_t)t * (16 * mt) + e] = on ? dl[q] : 0.f;
     tile[tt][e] = on ? dl[q] : 0.f;
   }
   if (!fx && !fw) return;
@@ -265,7 +270,7 @@ __device__ __forceinline__ uint32_t rows8_off(int H, int col) {
 
 struct RouteBwdArgs {
   int T, H, E, ncg, steps, splits, dx_tiles, dw_blocks;
-  const float* dl;
+  const float* pad;  // fp32 layers: dlogits [32 steps][16 MT]
   const uint4 *fx, *fw;
   float *part, *dw;
   int accumulate;
@@ -370,31 +375,48 @@ template <int MT>
 __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ x, int col,
                                          int m0, int r0, int way, int s1,
                                          f32x4_t (&acc)[DwShape<MT>::MW][4]) {
-  constexpr int MW = DwShape<MT>::MW;
+  constexpr int MW = DwShape<MT>::MW, WAYS = DwShape<MT>::WAYS;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
-  for (int s = r0 + way; s < s1; s += DwShape<MT>::WAYS) {
-    float4 v[8];
-    float d[8][MW];
+  struct Half {
+    float4 v[4];
+    float d[4][MW];
+  } h0, h1;
+  auto load = [&](Half& h, int s, int half) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int t = s * RBWD_STEP + 4 * q + g;
-      v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < a.T) v[q] = *reinterpret_cast<const float4*>(x + (int64_t)t * a.H + col);
+    for (int q = 0; q < 4; ++q) {
+      const int t = s * RBWD_STEP + 16 * half + 4 * q + g;
+      h.v[q] = *reinterpret_cast<const float4*>(x + (int64_t)min(t, a.T - 1) * a.H + col);
+#pragma unroll
+      for (int m = 0; m < MW; ++m)
+        h.d[q][m] = m0 + m < MT ? a.pad[(int64_t)t * (16 * MT) + 16 * (m0 + m) + n] : 0.f;
+    }
+  };
+  auto mfma = [&](Half& h, int s, int half) {
+    const bool whole = (s + 1) * RBWD_STEP <= a.T;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (!whole && s * RBWD_STEP + 16 * half + 4 * q + g >= a.T)
+        h.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);  // read the last row, times zero
 #pragma unroll
       for (int m = 0; m < MW; ++m) {
-        const int e = 16 * (m0 + m) + n;
-        d[q][m] = t < a.T && e < a.E ? a.dl[(int64_t)t * a.E + e] : 0.f;
+        acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].x, acc[m][0], 0, 0, 0);
+        acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].y, acc[m][1], 0, 0, 0);
+        acc[m][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].z, acc[m][2], 0, 0, 0);
+        acc[m][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].w, acc[m][3], 0, 0, 0);
       }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-#pragma unroll
-      for (int m = 0; m < MW; ++m) {
-        acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].x, acc[m][0], 0, 0, 0);
-        acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].y, acc[m][1], 0, 0, 0);
-        acc[m][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].z, acc[m][2], 0, 0, 0);
-        acc[m][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[q][m], v[q].w, acc[m][3], 0, 0, 0);
-      }
+  };
+  const int s0 = r0 + way;
+  if (s0 >= s1) return;
+  // half steps in turn, each asked for before the one before it is multiplied
+  load(h0, s0, 0);
+  for (int s = s0; s < s1; s += WAYS) {
+    load(h1, s, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    mfma(h0, s, 0);
+    load(h0, min(s + WAYS, s1 - 1), 0);
+    __builtin_amdgcn_sched_barrier(0);
+    mfma(h1, s, 1);
   }
 }
 
@@ -534,7 +556,9 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
 }
 // fp32: k step 4q + r holds experts 16 q + 4 (lane / 16) + r on both sides, so
 // a lane's four steps of one q are four consecutive experts of its token.
-// Operand row r takes columns 4 r + c: a lane ends with 16 consecutive ones.
+// Operand row r takes columns 4 (r / 4) + 16 (r % 4) + c: a lane ends with four
+// runs of four, 4 g + 16 i, and each store covers 64 contiguous bytes of a
+// token with four lanes.
 template <int MT>
 __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
                                          const float* __restrict__ w, const float* dx_add,
@@ -550,46 +574,52 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
       const int e = 16 * q + 4 * g + r;
       wf[q][r] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (e < a.E)
-        wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * 64 + 4 * n);
+        wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * 64 +
+                                                    4 * (n >> 2) + 16 * (n & 3));
     }
+  // a tile's loads go out before the tile before it is stored
+  float4 d[MT], add[4];
+  auto load = [&](int tl) {
+    const int64_t t = min(tl * 16 + n, a.T - 1);
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+      d[q] = *reinterpret_cast<const float4*>(a.pad + (int64_t)(tl * 16 + n) * (16 * MT) + 16 * q + 4 * g);
+    if (dx_add) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        add[i] = *reinterpret_cast<const float4*>(dx_add + t * a.H + cg * 64 + 4 * g + 16 * i);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  load(t0);
   for (int tl = t0; tl < t1; ++tl) {
     const int t = tl * 16 + n;
-    const int64_t o = (int64_t)t * a.H + cg * 64 + 16 * g;
     f32x4_t acc[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (dx_add && t < a.T) {
+    for (int q = 0; q < MT; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 d = *reinterpret_cast<const float4*>(dx_add + o + 4 * i);
-        acc[0][i] = d.x;
-        acc[1][i] = d.y;
-        acc[2][i] = d.z;
-        acc[3][i] = d.w;
+      for (int r = 0; r < 4; ++r) {
+        const float dv = r == 0 ? d[q].x : r == 1 ? d[q].y : r == 2 ? d[q].z : d[q].w;
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+        const bool first = q == 0 && r == 0;
+        acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].x, dv, first ? zero : acc[0], 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].y, dv, first ? zero : acc[1], 0, 0, 0);
+        acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].z, dv, first ? zero : acc[2], 0, 0, 0);
+        acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].w, dv, first ? zero : acc[3], 0, 0, 0);
       }
+    float4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
+      if (dx_add)
+        o[i] = make_float4(o[i].x + add[i].x, o[i].y + add[i].y, o[i].z + add[i].z, o[i].w + add[i].w);
     }
-    float d[MT][4];
-#pragma unroll
-    for (int q = 0; q < MT; ++q)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int e = 16 * q + 4 * g + r;
-        d[q][r] = t < a.T && e < a.E ? a.dl[(int64_t)t * a.E + e] : 0.f;
-      }
-#pragma unroll
-    for (int q = 0; q < MT; ++q)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].x, d[q][r], acc[0], 0, 0, 0);
-        acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].y, d[q][r], acc[1], 0, 0, 0);
-        acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].z, d[q][r], acc[2], 0, 0, 0);
-        acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].w, d[q][r], acc[3], 0, 0, 0);
-      }
+    if (tl + 1 < t1) load(tl + 1);
     if (t < a.T) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(dx + o + 4 * i) =
-            make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
+        *reinterpret_cast<float4*>(dx + (int64_t)t * a.H + cg * 64 + 4 * g + 16 * i) = o[i];
     }
   }
 }
@@ -706,15 +736,16 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
   const RouteBwdPlan p = route_bwd_plan(d, T);
   const bool packs = d.dtype == MOE_BF16;
   char* base = static_cast<char*>(ws);
+  float* pad = !packs && (dx || dw) ? reinterpret_cast<float*>(base + p.fx) : nullptr;
   uint4* fx = packs && dx ? reinterpret_cast<uint4*>(base + p.fx) : nullptr;
   uint4* fw = packs && dw ? reinterpret_cast<uint4*>(base + p.fw) : nullptr;
   route_dlogits_kernel<<<p.steps, RBWD_THREADS, 0, s>>>(T, d.n_experts, d.top_k, d.renormalize, ids,
                                                         logits, dtopk_w, dlogits_add, dlogits, p.mt,
-                                                        p.ks, fx, fw);
+                                                        p.ks, pad, fx, fw);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!dx && !dw)) return e;
   const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles, dw ? p.splits * p.ncg : 0,
-                       dlogits, fx, fw,
+                       pad, fx, fw,
                        p.splits > 1 ? reinterpret_cast<float*>(base + p.part) : nullptr, dw, accumulate};
   const int dx_items = dx ? (2 * p.steps + p.dx_tiles - 1) / p.dx_tiles * p.ncg : 0;
   if (packs) return launch_products_t<bf16>(p.mt, a, dx_items, x, w_router, dx_add, dx, s);

@@ -419,8 +419,8 @@ moe_status_t moe_layer_forward_noalloc(const moe_dims_t* dims, int32_t T, const 
  * enqueues nothing (but see moe_route_backward), and no buffer is looked at. */
 
 /* Rows sorted by expert: x_perm[inv[t*k+j]] = x[t] for every slot with inv in
- * 0..T*k-1 (moe_permute; other slots are skipped).  x [T][H], x_perm [T*k][H]
- * dtype.  Rows that no slot names are left as they were.  The gradient is
+ * 0..T*k-1 (moe_permute's; other slots are skipped; no two slots may name one
+ * row, or either's value may stand there).  x [T][H], x_perm [T*k][H] dtype.  Rows that no slot names are left as they were.  The gradient is
  * moe_undispatch with topk_w_opt = NULL. */
 moe_status_t moe_dispatch(const moe_dims_t* dims, int32_t T, const void* x, const int32_t* inv,
                           void* x_perm, void* stream);

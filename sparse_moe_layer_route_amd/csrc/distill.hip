@@ -266,7 +266,8 @@ distill_group_kernel(DistillArgs a, const T* student, T* dstudent) {
   }
   const double S = (double)group_sum<G>(sum);
   const double top = fmax((double)m * a.inv_tau, zm);
-  const double A = group_sum_d<G>(has_p ? p * (lp - (z - top)) : 0.0);
+  // an entry whose p underflows counts nothing, whatever the student says (0 * inf)
+  const double A = group_sum_d<G>(has_p && p != 0.0 ? p * (lp - (z - top)) : 0.0);
   const RowResult r = finish_row(a, c, mass, m, S, zm, hs, A, top, cnt < a.V);
   if (l == 0) a.loss[t] = r.loss;
   if (!drow) return;
@@ -493,7 +494,7 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
       if (PHASE == DISTILL_GRAD) continue;
       cnt += __popcll(__ballot(first));
       if (first && s_z[i] != NEG_INF) hs += exp(s_z[i] - zm);
-      if (in && lp != NEG_INF) {
+      if (in && p != 0.0) {  // p may underflow where the student is -inf
         P += p;
         A += p * (lp - (s_z[i] - zr));
       }

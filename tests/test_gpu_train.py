@@ -250,6 +250,30 @@ def test_route_backward(T, H, E, k, dtype, renorm, form):
     assert torch.equal(dw3, dw)
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_with_masked_experts(renorm):
+    """Experts masked by -inf or the type's lowest value, a token whose chosen
+    logits are all the lowest, one without slots."""
+    T, H, E, k = 5, 64, 20, 3
+    g = gen(51)
+    logits = torch.randn(T, E, generator=g)
+    ids = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+    mask = torch.ones(T, E, dtype=torch.bool).scatter_(1, ids.long(), False)
+    low = torch.finfo(torch.float32).min
+    logits[0][mask[0]] = -float("inf")
+    logits[1][mask[1]] = low
+    logits[2] = low
+    ids[3] = -1
+    dtw = torch.randn(T, k, generator=g)
+    d = make_dims(H, E, k, "f32", renorm)
+    dl = torch.empty(T, E, device="cuda")
+    M.moe_route_backward(d, T, None, None, ids.cuda(), logits.cuda(), dtw.cuda(), dl, None, None, None)
+    want = TO.route_dlogits(f64(logits), ids.numpy(), f64(dtw), renorm)
+    assert torch.isfinite(dl).all() and not dl[3].any()
+    # p off by at most (4 + E + 16) u where |l - m| counts (below it p is 0)
+    near(dl, want, 2 * 64 * U * np.abs(f64(dtw)).sum(1, keepdims=True), "dlogits")
+
+
 def test_route_backward_of_an_empty_batch():
     d = make_dims(128, 8, 2, "bf16")
     dw = torch.full((8, 128), 3.0, device="cuda")
@@ -368,6 +392,27 @@ def test_distill_skipped_doubled_and_masked(V, tail):
         assert loss[0] == 0 and not ds[0].any() and loss[5] == 0 and not ds[5].any()
 
 
+@pytest.mark.parametrize("V,T", [(40, 5), (400, 5), (5000, 5), (300000 // 2, 2)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_lowest_teacher_logits_on_masked_classes(V, T, tail):
+    """A teacher entry of the type's lowest value has p = 0 (it underflows): a
+    student that masks the class with -inf loses nothing by it."""
+    K, low = 7, torch.finfo(torch.float32).min
+    s, ids, u, lse = distill_case(21 + V, T, V, K, "f32", False, 1.0, tail)
+    u[:, 3:] = low
+    rows = torch.arange(T)[:, None]
+    s[rows.cuda(), ids[:, 3:].long().cuda()] = -float("inf")
+    u[1, 1] = -1e4                                     # and one that underflows by itself
+    s[1, ids[1, 1].item()] = -float("inf")
+    ids, u = ids.cuda(), u.cuda()
+    lse = None if lse is None else lse.cuda()
+    loss, ds = torch.empty(T, device="cuda"), torch.empty_like(s)
+    ws = torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")
+    M.moe_distill_topk(T, V, K, s, ids, u, loss, ds, ws, teacher_lse=lse)
+    assert torch.isfinite(loss).all() and torch.isfinite(ds).all()
+    distill_check(s, ids, u, lse, V, 1.0, None, 1.0, "f32", loss, ds)
+
+
 def test_distill_infinite_and_nan_rows():
     T, V, K = 4, 300, 3
     s, ids, u, _ = distill_case(5, T, V, K, "f32", False, 1.0, False)
@@ -382,6 +427,108 @@ def test_distill_infinite_and_nan_rows():
     assert torch.isnan(loss[2])
     rl, rg = TO.distill(f64(s)[3:], ids[3:].numpy(), f64(u)[3:], 1.0)
     assert abs(float(loss[3]) - rl[0]) < 1e-5 and np.abs(f64(ds)[3] - rg[0]).max() < 1e-6
+
+
+def test_distill_rows_past_2_31_elements():
+    """A row stride that puts the last rows behind 2^31 elements, onto the student."""
+    T, V, K, ld = 3, 5001, 9, (1 << 30) + 5001
+    s, ids, u, _ = distill_case(31, T, V, K, "bf16", False, 1.0, False)
+    far = torch.empty((T - 1) * ld + V, dtype=torch.bfloat16, device="cuda")
+    for t in range(T):
+        far[t * ld:t * ld + V] = s[t]
+    loss = torch.empty(T, device="cuda")
+    ws = torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")
+    M.moe_distill_topk(T, V, K, far, ids.cuda(), u.cuda(), loss, far, ws, ld=ld)
+    ds = torch.stack([far[t * ld:t * ld + V] for t in range(T)])
+    distill_check(s, ids, u, None, V, 1.0, None, 1.0, "bf16", loss, ds)
+
+
+def test_distill_many_rows_in_segments():
+    """More rows than one launch of segments takes; the rows repeat, so each
+    must equal its first copy."""
+    R, T, V, K = 48, 32768 + 48, 66000, 2
+    s, ids, u, lse = distill_case(33, R, V, K, "f32", False, 1.0, True)
+    n = -(-T // R)
+    big = s.repeat(n, 1)[:T].contiguous()
+    ids, u, lse = ids.repeat(n, 1)[:T].cuda(), u.repeat(n, 1)[:T].cuda(), lse.repeat(n)[:T].cuda()
+    loss = torch.empty(T, device="cuda")
+    ws = torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")
+    M.moe_distill_topk(T, V, K, big, ids, u, loss, big, ws, teacher_lse=lse)
+    distill_check(s[:3], ids[:3], u[:3], lse[:3], V, 1.0, None, 1.0, "f32", loss[:3], big[:3])
+    at = torch.arange(T, device="cuda") % R
+    assert torch.equal(loss, loss[:R][at])
+    for t0 in range(0, T, 4096):
+        assert torch.equal(big[t0:t0 + 4096], big[:R][at[t0:t0 + 4096]])
+
+
+def test_distill_segments_in_a_graph():
+    T, V, K = 5, 100003, 12
+    s, ids, u, lse = distill_case(35, T, V, K, "f32", False, 1.0, True)
+    ids, u, lse = ids.cuda(), u.cuda(), lse.cuda()
+    bufs = [(torch.empty(T, device="cuda"), torch.empty_like(s),
+             torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")) for _ in range(2)]
+    run = lambda b: M.moe_distill_topk(T, V, K, s, ids, u, b[0], b[1], b[2], teacher_lse=lse)
+    run(bufs[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(bufs[0])
+    for i in range(4):
+        s.copy_(randn(gen(90 + i), T, V, std=2.0))
+        run(bufs[1])
+        torch.cuda.synchronize()
+        bufs[0][0].fill_(float("nan"))
+        bufs[0][1].fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[0][0], bufs[1][0]) and torch.equal(bufs[0][1], bufs[1][1])
+
+
+def test_sorted_rows_near_the_element_limit():
+    """T * k * hidden just below 2^31: 4 GiB of sorted rows."""
+    T, H, k = 65528, 4096, 8
+    assert (1 << 31) - (1 << 19) < T * k * H < 1 << 31
+    d = make_dims(H, 8, k, "bf16")
+    g = gen(77)
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    inv = torch.randperm(T * k, generator=g).to(torch.int32).cuda()
+    rows = torch.empty(T * k, H, dtype=torch.bfloat16, device="cuda")
+    M.moe_dispatch(d, T, x, inv, rows)
+    iv = inv.view(T, k).long()
+    for j in range(k):
+        for t0 in range(0, T, 8192):
+            assert torch.equal(rows[iv[t0:t0 + 8192, j]], x[t0:t0 + 8192])
+    w = torch.rand(T, k, device="cuda")
+    w[:, 4:] = 0.0
+    out = torch.empty_like(x)
+    M.moe_undispatch(d, T, rows, inv, None, out)
+    assert torch.equal(out, (x.float() * 8).to(torch.bfloat16))      # eight times itself: exact
+    dw = torch.empty(T, k, device="cuda")
+    M.moe_undispatch_backward(d, T, x, rows, inv, None, None, dw)
+    some = torch.tensor([0, 1, T // 2, T - 1], device="cuda")
+    want = (x[some].double() ** 2).sum(1, keepdim=True).expand(-1, k)
+    assert torch.allclose(dw[some].double(), want, rtol=(H / 8 + 17) * U, atol=0)
+    M.moe_undispatch_backward(d, T, x, None, inv, w, rows, None)
+    some_rows = (w[some][..., None] * x[some].float()[:, None]).to(torch.bfloat16)
+    assert torch.equal(rows[iv[some]], some_rows)
+
+
+def test_route_backward_of_many_tokens():
+    """A long batch of a narrow layer: many token ranges and long ones."""
+    T, H, E, k = 300007, 64, 5, 2
+    g = gen(41)
+    d = make_dims(H, E, k, "bf16", True)
+    x, w = randn(g, T, H, dtype="bf16"), randn(g, E, H, dtype="bf16")
+    add = randn(g, T, E)
+    dl, dx, dw = torch.empty_like(add), torch.empty_like(x), torch.empty(E, H, device="cuda")
+    ws = torch.empty(M.moe_route_backward_size(d, T), dtype=torch.uint8, device="cuda")
+    M.moe_route_backward(d, T, x, w, None, None, None, dl, dx, dw, ws, dlogits_add=add)
+    assert torch.equal(dl, add)
+    rdx, rdw = TO.router_linear_backward(f64(add), f64(x), f64(w))
+    mx, mw = TO.router_linear_backward(np.abs(f64(add)), np.abs(f64(x)), np.abs(f64(w)))
+    near(dx, rdx, ((2 * E + 2) * U + 2.0 ** -16) * mx + HALF["bf16"] * 1.01 * np.abs(rdx), "dx")
+    # a wave sums at most T / 256 tokens before the ranges meet
+    near(dw, rdw, (T / 256 + 300) * U * mw, "dw_router")
 
 
 # ------------------------------------------------------ the operators as one --

@@ -619,25 +619,19 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   }
 }
 
-// Segments of a call's rows: 1 when a block holds a row and the rows fill the
-// GPU, or a row is too short to be worth two launches.
-constexpr int SEG_NT = 256, SEG_NU = 8;
-constexpr int ROW_UNITS = 1024 * 16;  // of the largest one-block kernel
-#ifndef DISTILL_FILL
-#define DISTILL_FILL 256
-#endif
-#ifndef DISTILL_SEG_BLOCKS
-#define DISTILL_SEG_BLOCKS 512
-#endif
-#ifndef DISTILL_SPLIT_UNITS
-#define DISTILL_SPLIT_UNITS 4096
-#endif
+// Segments of a call's rows.  One block holds rows of up to ROW_UNITS units;
+// longer ones are cut.  Below that, rows that need the 1024-thread block are cut
+// as well while they are few (8 x 65000 bf16: 11 us cut, 14 whole; 32 x 128000:
+// 15 and 22; 64 x 65000: 15.4 both; 255 x 32800: 22 and 15), into about
+// SEG_BLOCKS segments in all.
+constexpr int SEG_NT = 256, SEG_NU = 8, SEG_BLOCKS = 512, SEG_TOKENS = 64;
+constexpr int ROW_UNITS = 1024 * 16, HALF_ROW_UNITS = 512 * 8;
 
 static void distill_segments(int T, int units, int* segs, int* seg_units) {
   *segs = 1;
   *seg_units = units;
-  if (units <= ROW_UNITS && (T >= DISTILL_FILL || units < DISTILL_SPLIT_UNITS)) return;
-  const int64_t want = ((int64_t)T * units + DISTILL_SEG_BLOCKS - 1) / DISTILL_SEG_BLOCKS;
+  if (units <= HALF_ROW_UNITS || (units <= ROW_UNITS && T >= SEG_TOKENS)) return;
+  const int64_t want = ((int64_t)T * units + SEG_BLOCKS - 1) / SEG_BLOCKS;
   const int64_t per = (want + SEG_NT - 1) / SEG_NT * SEG_NT;
   *seg_units = (int)std::min<int64_t>(std::max<int64_t>(per, SEG_NT), SEG_NT * SEG_NU);
   *segs = (units + *seg_units - 1) / *seg_units;
@@ -671,6 +665,9 @@ static hipError_t distill_t(DistillArgs a, const T* student, T* dstudent, void* 
     kernel<<<(a.T + rows - 1) / rows, GROUP_THREADS, 0, s>>>(a, student, dstudent);
     return hipGetLastError();
   };
+  // 16 lanes a row where they hold its entries (4096 x 40 fp32: 4.7 us, 8.0
+  // with 64 lanes, 10.7 with a block; 16384 x 500 bf16: 24, 29 and 41), else a
+  // wave (40 entries: 29 against 41 with a block)
   if (a.K <= 16 && a.V <= 64) return group(distill_group_kernel<T, 16, 4>, GROUP_THREADS / 16);
   if (a.K <= 16 && a.V <= 512) return group(distill_group_kernel<T, 16, 32>, GROUP_THREADS / 16);
   if (a.K <= 64 && a.V <= 512) return group(distill_group_kernel<T, 64, 8>, GROUP_THREADS / 64);
@@ -709,7 +706,7 @@ static hipError_t distill_t(DistillArgs a, const T* student, T* dstudent, void* 
     block_launch<T, 128, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
   else if (units <= 256 * 8)
     block_launch<T, 256, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
-  else if (units <= 512 * 8)
+  else if (units <= HALF_ROW_UNITS)
     block_launch<T, 512, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
   else
     block_launch<T, 1024, 16, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);

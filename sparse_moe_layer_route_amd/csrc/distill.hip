@@ -177,7 +177,8 @@ template <int G> __device__ __forceinline__ float group_sum(float v) {
 
 constexpr int GROUP_THREADS = 256;
 
-// Rows of at most G * NE classes and G teacher entries, G lanes each.
+// Rows of at most G * NE classes and G teacher entries, G lanes each.  4096 x 40
+// fp32, 8 entries (1.6 MB): 5.1 us, a launch and one chain of a row's steps.
 template <typename T, int G, int NE>
 __global__ void __launch_bounds__(GROUP_THREADS)
 distill_group_kernel(DistillArgs a, const T* student, T* dstudent) {
@@ -347,6 +348,10 @@ template <int NU> __device__ __forceinline__ float units_max(const uint4 (&x)[NU
 
 // Segment blockIdx.x of row blockIdx.y (DISTILL_ROW: row blockIdx.x), NT
 // threads of at most NU units each.  OCC: waves a SIMD should hold.
+// 2048 x 32000 bf16, 64 entries, a tenth of the rows masked (250 MB): 54 to 60
+// us, 4.2 to 4.6 TB/s; what is above a copy's time is the 32-bit exponentials,
+// one an element, kept for the gradient, beside the loads of other rows.  Cut
+// rows, 7 x 100003 fp32: 5.4 us for the sums and 6.8 for the gradient, two launches.
 template <typename T, int NT, int NU, int PHASE, int OCC>
 __global__ void __launch_bounds__(NT, OCC)
 distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {

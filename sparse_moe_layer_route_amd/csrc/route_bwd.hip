@@ -24,6 +24,12 @@
 // interleaves them in registers into the fragments of four column tiles, tile
 // c holding columns 4n + c, so nothing passes through LDS on the way in.
 // fp32 layers run v_mfma_f32_16x16x4_f32, whose operands are single values.
+//
+// bf16, 16384 x 3584, 64 experts (246 MB, 45.5 us at the rate of a large copy):
+// 73 us, of which 8 the logits' gradient, 62 the products, 5 the sum of the
+// ranges.  What bounds the products is the rate at which a CU takes lines from
+// its L2 (about 30 bytes a clock): dW reads x and its fragments, dx writes as
+// much again, and the two run side by side.
 #include <algorithm>
 #include <type_traits>
 
@@ -122,6 +128,9 @@ __device__ __forceinline__ float row_max(float v) {
 //     8 (lane / 16) .. +7.
 // The parts of a value are it rounded to bf16, what is left rounded, and so on
 // (a value that is not finite leaves NaN).
+// No branch on a lane's expert or slot: selects only, so that all loads of a
+// token go out together (64 x 64: 8.7 us with branches, 3.9 without, a launch and
+// a chain of short steps; 16384 x 64: 7.9, of 8 MB read and 14 written).
 __global__ void __launch_bounds__(RBWD_THREADS)
 route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict__ ids,
                      const float* __restrict__ logits, const float* __restrict__ dtopk_w,
@@ -286,10 +295,11 @@ template <int MT> struct DwShape {
 };
 
 // acc[m][c] += the tokens of steps r0 + way, then every WAYS-th, below s1 (r0
-// and s1 the same for the block): experts of tile m0 + m by the lanes' column c.  Fragments are asked for one step ahead, rows
-// two, in this order, since loads retire in order: waiting for a step's
-// fragments leaves the rows after them in flight.  A last step that is not
-// whole runs by itself, so that the loop has one way to load its rows.
+// and s1 the same for the block): experts of tile m0 + m by the lanes' column
+// c.  Fragments are asked for one step ahead, rows two, in this order, since
+// loads retire in order: waiting for a step's fragments leaves the rows after
+// them in flight.  A last step that is not whole runs by itself, so that the
+// loop has one way to load its rows.
 template <int MT>
 struct DwFrags {
   uint4 f[DwShape<MT>::MW][RBWD_DW_PARTS];
@@ -346,7 +356,8 @@ __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __re
   };
   // The block's waves go through their steps together, so the second wave of a
   // pair finds the rows of the first in L1 (dW of 16384 x 3584: 38 us without
-  // the barriers, 34 with them); every wave passes every barrier, whether or not it has a step.
+  // the barriers, 34 with them).  Every wave passes every barrier, whether or
+  // not it has a step.
   const int trips = (e - r0 + WAYS - 1) / WAYS;
   if (trips > 0) {
     rows(s0, v0);

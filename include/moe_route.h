@@ -419,8 +419,9 @@ moe_status_t moe_layer_forward_noalloc(const moe_dims_t* dims, int32_t T, const 
  * enqueues nothing (but see moe_route_backward), and no buffer is looked at. */
 
 /* Rows sorted by expert: x_perm[inv[t*k+j]] = x[t] for every slot with inv in
- * 0..T*k-1 (moe_permute's; other slots are skipped; no two slots may name one
- * row, or either's value may stand there).  x [T][H], x_perm [T*k][H] dtype.  Rows that no slot names are left as they were.  The gradient is
+ * 0..T*k-1 (moe_permute's; other slots are skipped).  No two slots may name
+ * one row: it would hold parts of either's.  x [T][H], x_perm [T*k][H] dtype.
+ * Rows that no slot names are left as they were.  The gradient is
  * moe_undispatch with topk_w_opt = NULL. */
 moe_status_t moe_dispatch(const moe_dims_t* dims, int32_t T, const void* x, const int32_t* inv,
                           void* x_perm, void* stream);
@@ -438,7 +439,7 @@ moe_status_t moe_undispatch(const moe_dims_t* dims, int32_t T, const void* y_per
 
 /* Gradient of moe_undispatch with weights, dout [T][H] dtype:
  *   dy_perm[inv[t*k+j]] = w_tj dout[t] (row_dtype; rows that no slot names are
- *     left as they were); needs topk_w.
+ *     left as they were; no two slots may name one row); needs topk_w.
  *   dtopk_w[t*k+j] = <dout[t], y_perm[inv[t*k+j]]> in fp32, 0 for a slot
  *     without a row; needs y_perm.
  * Either output may be NULL, not both (MOE_EINVAL).  The gradient of add is
@@ -493,7 +494,7 @@ moe_status_t moe_distill_topk_size(int32_t T, int32_t V, size_t* bytes /* host *
  *   loss [T] fp32 = scale * token_w[t] * KL (token_w_opt NULL: 1).
  *   dstudent_opt [T][ld] of the student's dtype = d loss[t] / d student[t],
  *     rounded once; NULL: the loss alone; the student's buffer itself is
- *     allowed.  Columns V..ld-1 are neither read nor written.
+ *     allowed.  Columns V..ld-1 play no part and are left as they were.
  * student [T][ld] dtype, ld >= V (rows need not be aligned); teacher_ids and
  * teacher_logits [T][K].  Entries with an id outside 0..V-1 are skipped; a
  * class named twice has both entries' mass.  A row with token_w = 0 is not

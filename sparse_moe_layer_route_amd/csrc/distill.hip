@@ -55,11 +55,13 @@ struct DistillArgs {
   struct SegStat* stats;  // [T][segs]
 };
 
-// What a segment of a row brings to the row's sums.
+// What a segment of a row brings to the row's sums.  e = exp(d) is a teacher's
+// entry before it is normalised: d = u / tau minus the entries' largest (minus
+// lse_teacher where that is given, and e is p).
 struct SegStat {
   float m, s;  // tail: maximum logit, sum of exp((logit - m) / tau)
   double zm, hs;  // teacher's classes: maximum z, sum of exp(z - zm), each class once
-  double A, P;  // sum of p (log p - (z - ref)) with ref = zm (0 if that is -inf), sum of p
+  double A, P;  // sum of e (d - (z - ref)) with ref = zm (0 if that is -inf), sum of e
   int cnt;      // number of the teacher's classes
 };
 
@@ -103,38 +105,53 @@ __device__ __forceinline__ float distill_exp(float s, float m, const DistillArgs
 // Everything the gradient needs of a row, and its loss.
 struct RowResult {
   double zm, qh;  // a teacher's class: q = exp(z - zm) qh
-  double M;
+  double M, norm;  // p = e norm
   float m, f;  // a tail class's gradient is f exp((logit - m) / tau)
   float loss;
 };
 
-// From the joined sums of a row: m, S of the tail; zm, hs of the teacher's
-// classes; A = sum of p (log p - (z - top)), top = max(m / tau, zm).  All is
-// taken relative to top: beside a maximum of the type's lowest value a
-// logarithm would be lost.  All -inf: NaN from here on.
-__device__ __forceinline__ RowResult finish_row(const DistillArgs& a, double c, double mass, float m,
+// From the joined sums of a row: sum of e; m, S of the tail; zm, hs of the
+// teacher's classes; A = sum of e (d - (z - top)), top = max(m / tau, zm).  All is
+// taken relative to top, and log p = d - log(sum) in this order: beside a
+// maximum of the type's lowest value a logarithm would be lost.  All -inf: NaN
+// from here on.
+// The row's values are in every lane; of two exponentials, three quotients and
+// two logarithms each lane of four takes one: one call of each in the chain that
+// the row's other waves wait for.
+__device__ __forceinline__ RowResult finish_row(const DistillArgs& a, double c, double sum, float m,
                                                 double S, double zm, double hs, double A, double top,
                                                 bool has_tail) {
   RowResult r;
+  const int l = threadIdx.x & 3;
+  auto lane0 = [](double v) { return dpp_move_d<0x00, 0xf, false>(v, v); };  // quad_perm 0,0,0,0
+  auto lane1 = [](double v) { return dpp_move_d<0x55, 0xf, false>(v, v); };  // quad_perm 1,1,1,1
+  auto lane2 = [](double v) { return dpp_move_d<0xAA, 0xf, false>(v, v); };  // quad_perm 2,2,2,2
   const double dt = (double)m * a.inv_tau - top;
-  const double et = exp(dt), eh = exp(zm - top), W = S * et + hs * eh, iW = 1.0 / W;
+  const double ev = exp(l == 0 ? dt : zm - top);
+  const double et = lane0(ev), eh = lane1(ev), W = S * et + hs * eh;
+  const double iv = 1.0 / (l == 0 ? W : l == 1 ? S : sum);
+  const double iW = lane0(iv), iS = lane1(iv);
+  r.norm = a.t_lse ? 1.0 : lane2(iv);
+  const double mass = sum * r.norm;
   const double pt = a.t_lse && has_tail ? fmax(0.0, 1.0 - mass) : 0.0;
-  double kl = A + mass * log(W);
-  if (pt > 0.0) kl += pt * (log(pt * W / S) - dt);
+  const double lv = log(l == 0 ? W : a.t_lse ? pt * W * iS : sum);
+  const double lW = lane0(lv), l1 = lane1(lv);
+  double kl = A * r.norm + mass * lW;
+  if (!a.t_lse) kl -= mass * l1;
+  if (pt > 0.0) kl += pt * (l1 - dt);
   const double g = c * a.inv_tau;
   r.zm = zm;
   r.qh = eh * iW;
   r.M = mass + pt;
   r.m = m == -__builtin_inff() ? 0.f : m;
-  r.f = (float)(S == 0.0 ? 0.0 * W : g * (r.M * et * iW - pt / S));
+  r.f = (float)(S == 0.0 ? 0.0 * W : g * (r.M * et * iW - pt * iS));
   r.loss = (float)(c * kl);
   return r;
 }
-// Gradient of a teacher's class of value z and joined mass p.
-__device__ __forceinline__ float head_grad(const DistillArgs& a, double c, const RowResult& r, double z,
+// Gradient of a teacher's class: ez = exp(z - zm), p its entries' mass.
+__device__ __forceinline__ float head_grad(const DistillArgs& a, double c, const RowResult& r, double ez,
                                            double p) {
-  const double e = z == NEG_INF ? 0.0 : exp(z - r.zm);
-  return (float)(c * a.inv_tau * (e * r.qh * r.M - p));
+  return (float)(c * a.inv_tau * (ez * r.qh * r.M - p));
 }
 
 // --------------------------------------------- a group of lanes per row ---
@@ -178,7 +195,9 @@ template <int G> __device__ __forceinline__ float group_sum(float v) {
 constexpr int GROUP_THREADS = 256;
 
 // Rows of at most G * NE classes and G teacher entries, G lanes each.  4096 x 40
-// fp32, 8 entries (1.6 MB): 5.1 us, a launch and one chain of a row's steps.
+// fp32, 8 entries (1.6 MB): 4.5 us, a launch and one chain of a row's steps;
+// 16384 x 500 bf16, 40 entries: 25 us, bound by some 800 vector instructions a
+// row, half of them the entries' 64-bit steps.
 template <typename T, int G, int NE>
 __global__ void __launch_bounds__(GROUP_THREADS)
 distill_group_kernel(DistillArgs a, const T* student, T* dstudent) {
@@ -223,27 +242,16 @@ distill_group_kernel(DistillArgs a, const T* student, T* dstudent) {
       const int idj = __shfl(id, base + j);  // by the whole group
       if (j < l && idj == id) own = false;
     }
-  // teacher: log p = (u - ref) - log_sum, in this order (beside a maximum of
-  // the type's lowest value the logarithm would be lost)
   const bool has_p = ok && u != NEG_INF;
-  double p, lp;
-  if (a.t_lse) {
-    lp = u - t_lse;
-    p = has_p ? exp(lp) : 0.0;
-  } else {
-    const double um = group_max_d<G>(ok ? u : NEG_INF);
-    const double e = has_p ? exp(u - um) : 0.0, sum = group_sum_d<G>(e);
-    lp = (u - um) - log(sum);
-    p = e / sum;
-    if (sum == 0.0) return clear();  // no entry to learn from
-  }
-  const double mass = group_sum_d<G>(p);
-  double p_class = p;
+  const double d = u - (a.t_lse ? t_lse : group_max_d<G>(ok ? u : NEG_INF));
+  const double e = has_p ? exp(d) : 0.0, psum = group_sum_d<G>(e);
+  if (!a.t_lse && psum == 0.0) return clear();  // no entry to learn from
+  double e_class = e;
   if (dup)
     for (int j = 0; j < a.K; ++j) {
-      const double pj = __shfl(p, base + j);
+      const double ej = __shfl(e, base + j);
       const int idj = __shfl(id, base + j);
-      if (j != l && idj == id) p_class += pj;
+      if (j != l && idj == id) e_class += ej;
     }
   const double zm = group_max_d<G>(z);
   const double ez = z != NEG_INF ? exp(z - zm) : 0.0;
@@ -268,14 +276,14 @@ distill_group_kernel(DistillArgs a, const T* student, T* dstudent) {
   const double S = (double)group_sum<G>(sum);
   const double top = fmax((double)m * a.inv_tau, zm);
   // an entry whose p underflows counts nothing, whatever the student says (0 * inf)
-  const double A = group_sum_d<G>(has_p && p != 0.0 ? p * (lp - (z - top)) : 0.0);
-  const RowResult r = finish_row(a, c, mass, m, S, zm, hs, A, top, cnt < a.V);
+  const double A = group_sum_d<G>(e != 0.0 ? e * (d - (z - top)) : 0.0);
+  const RowResult r = finish_row(a, c, psum, m, S, zm, hs, A, top, cnt < a.V);
   if (l == 0) a.loss[t] = r.loss;
   if (!drow) return;
 #pragma unroll
   for (int i = 0; i < NE; ++i)
     if (tail[i]) elem<T>::store(drow, l + G * i, r.f * s[i]);
-  if (own) elem<T>::store(drow, id, (float)(c * a.inv_tau * (ez * r.qh * r.M - p_class)));
+  if (own) elem<T>::store(drow, id, head_grad(a, c, r, ez, e_class * r.norm));
 }
 
 // ------------------------------------------------- one block per segment ---
@@ -348,10 +356,9 @@ template <int NU> __device__ __forceinline__ float units_max(const uint4 (&x)[NU
 
 // Segment blockIdx.x of row blockIdx.y (DISTILL_ROW: row blockIdx.x), NT
 // threads of at most NU units each.  OCC: waves a SIMD should hold.
-// 2048 x 32000 bf16, 64 entries, a tenth of the rows masked (250 MB): 54 to 60
-// us, 4.2 to 4.6 TB/s; what is above a copy's time is the 32-bit exponentials,
-// one an element, kept for the gradient, beside the loads of other rows.  Cut
-// rows, 7 x 100003 fp32: 5.4 us for the sums and 6.8 for the gradient, two launches.
+// 2048 x 32000 bf16, 64 entries, a tenth of the rows masked (250 MB): 54 us, 4.6
+// TB/s; vector instructions (15 an element) fill 56% of the time beside the
+// loads and stores of other rows.  Cut rows, 7 x 100003 fp32: 11.2 us, two launches.
 template <typename T, int NT, int NU, int PHASE, int OCC>
 __global__ void __launch_bounds__(NT, OCC)
 distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
@@ -361,13 +368,13 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   constexpr bool KEEP = PHASE == DISTILL_ROW && NU * EPU <= 64;
   extern __shared__ double smem[];
   const int K = a.K, V = a.V, tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
-  double* s_lp = smem;                   // [K] log p
-  double* s_z = s_lp + K;                // [K] z of this segment's entries
+  double* s_e = smem;                    // [K] the teacher's u / tau, then e
+  double* s_z = s_e + K;                 // [K] this segment's entries: z, then exp(z - zm)
   int32_t* s_id = (int32_t*)(s_z + K);   // [K] class, -1 where skipped
   uint32_t* bits = (uint32_t*)(s_id + K);  // this segment's marked elements
   __shared__ int s_dup;
   __shared__ float s_max[NW], s_sum[NW];
-  __shared__ double s_mass;
+  __shared__ double s_psum;
   __shared__ SegStat s_stat;
   __shared__ RowResult s_row;
   const int64_t t = PHASE == DISTILL_ROW ? blockIdx.x : blockIdx.y;
@@ -404,28 +411,30 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   // the first NT entries before the row: loads retire in order
   const int id0 = tid < K ? a.ids[t * K + tid] : -1;
   const float t0 = tid < K ? a.t_logits[t * K + tid] : 0.f;
+  // whole units, with what they hold of other rows (masked below); threads past
+  // the segment load its last one.  The last unit of the last row may pass the
+  // buffer's end and is put together from its elements.
+  const bool end = t == a.T - 1 && edge1 >= u0 && edge1 < u1;
+  const int n_whole = n_units - end;
   uint4 x[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int u = u0 + i * NT + tid;
-    // units past the segment count as -inf
-    x[i] = mask_unit<T>(make_uint4(0u, 0u, 0u, 0u), ALL);
-    if (u >= u1) continue;
-    if (u != edge0 && u != edge1) {
+    if (i * NT < n_whole) {
+      const int u = u0 + min(i * NT + tid, n_whole - 1);
       x[i] = *reinterpret_cast<const uint4*>(row + (u * EPU - ph));
     } else {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int e = 0; e < EPU; ++e) {
-        const int v = u * EPU - ph + e;
-        if ((unsigned)v >= (unsigned)V) continue;  // marked below
-        if (sizeof(T) == 2)
-          w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[v] << (16 * (e & 1));
-        else
-          w[e % 4] = reinterpret_cast<const uint32_t*>(row)[v];
-      }
-      x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      x[i] = mask_unit<T>(make_uint4(0u, 0u, 0u, 0u), ALL);
     }
+  }
+  if (end) {
+    T el[EPU];
+#pragma unroll
+    for (int e = 0; e < EPU; ++e) el[e] = row[min(max(edge1 * EPU - ph + e, 0), V - 1)];
+    uint4 last;
+    __builtin_memcpy(&last, el, 16);
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+      if (i * NT + tid == n_whole) x[i] = last;
   }
   if (tid == 0) s_dup = 0;
   for (int i = tid; i < (n_units * EPU + 31) / 32; i += NT) bits[i] = 0u;
@@ -436,7 +445,7 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
     const int id = i < NT ? id0 : a.ids[t * K + i];
     const bool ok = (unsigned)id < (unsigned)V;
     s_id[i] = ok ? id : -1;
-    s_lp[i] = (double)(i < NT ? t0 : a.t_logits[t * K + i]) * a.inv_tau;
+    s_e[i] = (double)(i < NT ? t0 : a.t_logits[t * K + i]) * a.inv_tau;
     const int b = id - b0;
     if (ok && b >= 0 && b < nb) {
       const uint32_t bit = 1u << (b & 31);
@@ -460,56 +469,55 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   };
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int q = (i * NT + tid) * EPU;
-    if (u0 + i * NT + tid >= u1) continue;
-    const uint32_t k = (bits[q >> 5] >> (q & 31)) & ALL;
+    if (i * NT >= n_units) continue;
+    const int u = i * NT + tid, q = min(u, n_units - 1) * EPU;
+    const uint32_t k = u < n_units ? (bits[q >> 5] >> (q & 31)) & ALL : ALL;
     if (k) x[i] = mask_unit<T>(x[i], k);
   }
-  if (wv == 0) {
-    // log p = (u - ref) - log_sum, in this order: beside a maximum of the
-    // type's lowest value the logarithm would be lost
-    double ref, log_sum = 0.0;
+  // The teacher's entries, by the block's last wave while the others form the
+  // tail's sum: one exponential an entry for p and one for its class.
+  auto teacher = [&] {
+    double ref, zm = NEG_INF;
     if (a.t_lse) {
       ref = (double)a.t_lse[t];
     } else {
-      double um = NEG_INF, e = 0.0;
+      double um = NEG_INF;
       for (int i = lane; i < K; i += 64)
-        if (s_id[i] >= 0) um = fmax(um, s_lp[i]);
+        if (s_id[i] >= 0) um = fmax(um, s_e[i]);
       ref = wave_max_d(um);
-      for (int i = lane; i < K; i += 64)
-        if (s_id[i] >= 0 && s_lp[i] != NEG_INF) e += exp(s_lp[i] - ref);
-      log_sum = log(wave_sum_d(e));
     }
-    double zm = NEG_INF;
     if (PHASE != DISTILL_GRAD) {
       for (int i = lane; i < K; i += 64)
         if (here(i)) zm = fmax(zm, s_z[i]);
       zm = wave_max_d(zm);
     }
     const double zr = zm == NEG_INF ? 0.0 : zm;
-    double mass = 0.0, hs = 0.0, A = 0.0, P = 0.0;
+    double psum = 0.0, hs = 0.0, A = 0.0, P = 0.0;
     int cnt = 0;
     for (int i0 = 0; i0 < K; i0 += 64) {
       const int i = i0 + lane;
       const bool ok = i < K && s_id[i] >= 0, in = ok && here(i), first = in && own(i);
-      const double lp = ok && s_lp[i] != NEG_INF ? (s_lp[i] - ref) - log_sum : NEG_INF;
-      const double p = exp(lp);
-      if (ok) s_lp[i] = lp;
-      mass += p;
+      const double d = ok && s_e[i] != NEG_INF ? s_e[i] - ref : NEG_INF;
+      const double e = exp(d);
+      if (ok) s_e[i] = e;
+      psum += e;
       if (PHASE == DISTILL_GRAD) continue;
       cnt += __popcll(__ballot(first));
-      if (first && s_z[i] != NEG_INF) hs += exp(s_z[i] - zm);
-      if (in && p != 0.0) {  // p may underflow where the student is -inf
-        P += p;
-        A += p * (lp - (s_z[i] - zr));
+      const double z = in ? s_z[i] : NEG_INF;
+      const double ez = z == NEG_INF ? 0.0 : exp(z - zm);
+      if (first) hs += ez;
+      if (in && e != 0.0) {  // e may underflow where the student is -inf
+        P += e;
+        A += e * (d - (z - zr));
       }
+      if (PHASE == DISTILL_ROW && in) s_z[i] = ez;
     }
-    mass = wave_sum_d(mass);
-    if (lane == 0) s_mass = mass;
+    psum = wave_sum_d(psum);
+    if (lane == 0) s_psum = psum;
     if (PHASE != DISTILL_GRAD) {
       hs = wave_sum_d(hs);
       A = wave_sum_d(A);
-      P = PHASE == DISTILL_ROW ? mass : wave_sum_d(P);
+      P = PHASE == DISTILL_ROW ? psum : wave_sum_d(P);
       if (lane == 0) {
         s_stat.zm = zm;
         s_stat.hs = hs;
@@ -518,12 +526,15 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
         s_stat.cnt = cnt;
       }
     }
-  }
+  };
   float ex[KEEP ? NU : 1][EPU];
+  float m;
+  double S = 0.0;
   if (PHASE != DISTILL_GRAD) {
-    float m = wave_max(units_max(x, T{}));
+    m = wave_max(units_max(x, T{}));
     if (lane == 0) s_max[wv] = m;
     __syncthreads();
+    if (wv == NW - 1) teacher();
     m = s_max[0];
 #pragma unroll
     for (int w = 1; w < NW; ++w) m = fmaxf(m, s_max[w]);
@@ -542,59 +553,63 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
     }
     sum = wave_sum(sum);
     if (lane == 0) s_sum[wv] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      double S = 0.0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) S += (double)s_sum[w];
-      s_stat.m = m;
-      s_stat.s = (float)S;
-      if (PHASE == DISTILL_STATS) a.stats[t * a.segs + seg] = s_stat;
+  } else if (wv == NW - 1) {
+    teacher();
+  }
+  // meanwhile, the second launch: the first wave joins the segments
+  double zm, top, hs, A;
+  int cnt;
+  if (PHASE == DISTILL_GRAD && wv == 0) {
+    const SegStat* st = a.stats + t * a.segs;
+    m = -__builtin_inff();
+    zm = NEG_INF;
+    for (int i = lane; i < a.segs; i += 64) {
+      m = fmaxf(m, st[i].m);
+      zm = fmax(zm, st[i].zm);
     }
-    if (PHASE == DISTILL_STATS) return;
+    m = wave_max(m);
+    zm = wave_max_d(zm);
+    top = fmax((double)m * a.inv_tau, zm);
+    hs = A = 0.0;
+    cnt = 0;
+    for (int i = lane; i < a.segs; i += 64) {
+      const SegStat q = st[i];
+      if (q.s != 0.f) S += (double)q.s * exp(((double)q.m - (double)m) * a.inv_tau);
+      if (q.hs != 0.0) hs += q.hs * exp(q.zm - zm);
+      if (q.P != 0.0) A += q.A - q.P * ((q.zm == NEG_INF ? 0.0 : q.zm) - top);
+      cnt += q.cnt;
+    }
+    S = wave_sum_d(S);
+    hs = wave_sum_d(hs);
+    A = wave_sum_d(A);
+    cnt = __builtin_amdgcn_readlane(wave_incl_scan_i(cnt), 63);
   }
   __syncthreads();
-  const double mass = s_mass;
-  if (!a.t_lse && mass == 0.0) return clear();  // no entry to learn from
+  if (PHASE != DISTILL_GRAD && wv == 0) {
+#pragma unroll
+    for (int w = 0; w < NW; ++w) S += (double)s_sum[w];
+    S = (double)(float)S;
+  }
+  if (PHASE == DISTILL_STATS) {
+    if (tid == 0) {
+      SegStat q = s_stat;
+      q.m = m;
+      q.s = (float)S;
+      a.stats[t * a.segs + seg] = q;
+    }
+    return;
+  }
+  const double psum = s_psum;
+  if (!a.t_lse && psum == 0.0) return clear();  // no entry to learn from
   if (wv == 0) {
-    // join the segments (one: the block's own)
-    float m;
-    double zm, top, S, hs, A;
-    int cnt;
     if (PHASE == DISTILL_ROW) {
-      m = s_stat.m;
       zm = s_stat.zm;
       top = fmax((double)m * a.inv_tau, zm);
-      S = (double)s_stat.s;
       hs = s_stat.hs;
-      A = mass == 0.0 ? 0.0 : s_stat.A - mass * ((zm == NEG_INF ? 0.0 : zm) - top);
+      A = psum == 0.0 ? 0.0 : s_stat.A - psum * ((zm == NEG_INF ? 0.0 : zm) - top);
       cnt = s_stat.cnt;
-    } else {
-      const SegStat* st = a.stats + t * a.segs;
-      m = -__builtin_inff();
-      zm = NEG_INF;
-      for (int i = lane; i < a.segs; i += 64) {
-        m = fmaxf(m, st[i].m);
-        zm = fmax(zm, st[i].zm);
-      }
-      m = wave_max(m);
-      zm = wave_max_d(zm);
-      top = fmax((double)m * a.inv_tau, zm);
-      S = hs = A = 0.0;
-      cnt = 0;
-      for (int i = lane; i < a.segs; i += 64) {
-        const SegStat q = st[i];
-        if (q.s != 0.f) S += (double)q.s * exp(((double)q.m - (double)m) * a.inv_tau);
-        if (q.hs != 0.0) hs += q.hs * exp(q.zm - zm);
-        if (q.P != 0.0) A += q.A - q.P * ((q.zm == NEG_INF ? 0.0 : q.zm) - top);
-        cnt += q.cnt;
-      }
-      S = wave_sum_d(S);
-      hs = wave_sum_d(hs);
-      A = wave_sum_d(A);
-      cnt = __builtin_amdgcn_readlane(wave_incl_scan_i(cnt), 63);
     }
-    const RowResult r = finish_row(a, c, mass, m, S, zm, hs, A, top, cnt < V);
+    const RowResult r = finish_row(a, c, psum, m, S, zm, hs, A, top, cnt < V);
     if (lane == 0) {
       s_row = r;
       if (seg == 0) a.loss[t] = r.loss;
@@ -616,19 +631,22 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   __syncthreads();  // the teacher's classes over what the units wrote there
   for (int i = tid; i < K; i += NT) {
     if (!here(i) || !own(i)) continue;
-    double p = exp(s_lp[i]);
+    double e = s_e[i];
     if (s_dup)
       for (int j = i + 1; j < K; ++j)
-        if (s_id[j] == s_id[i]) p += exp(s_lp[j]);
-    elem<T>::store(drow, s_id[i], head_grad(a, c, r, s_z[i], p));
+        if (s_id[j] == s_id[i]) e += s_e[j];
+    const double z = s_z[i];
+    const double ez = PHASE == DISTILL_ROW ? z : z == NEG_INF ? 0.0 : exp(z - r.zm);
+    elem<T>::store(drow, s_id[i], head_grad(a, c, r, ez, e * r.norm));
   }
 }
 
 // Segments of a call's rows.  One block holds rows of up to ROW_UNITS units;
-// longer ones are cut.  Below that, rows that need the 1024-thread block are cut
-// as well while they are few (8 x 65000 bf16: 11 us cut, 14 whole; 32 x 128000:
-// 15 and 22; 64 x 65000: 15.4 both; 255 x 32800: 22 and 15), into about
+// longer ones are cut.  Below that, rows of more than HALF_ROW_UNITS are cut as
+// well while they are few (8 x 65000 bf16: 10.3 us cut, 14.0 whole; 32 x 128000:
+// 14.0 and 21.7; 80 x 65000: 16.6 and 16.0; 240 x 128000: 49 and 38), into about
 // SEG_BLOCKS segments in all.
+constexpr int FEW_WAVES = 4 * 1024;  // waves that four a SIMD hold
 constexpr int SEG_NT = 256, SEG_NU = 8, SEG_BLOCKS = 512, SEG_TOKENS = 64;
 constexpr int ROW_UNITS = 1024 * 16, HALF_ROW_UNITS = 512 * 8;
 
@@ -664,17 +682,25 @@ static void block_launch(const DistillArgs& a, dim3 grid, const T* student, T* d
   distill_block_kernel<T, NT, NU, PHASE, OCC><<<grid, NT, lds, s>>>(a, student, dstudent);
 }
 
+template <typename T, int NT, int NU>
+static hipError_t row_launch(const DistillArgs& a, const T* student, T* dstudent, hipStream_t s) {
+  block_launch<T, NT, NU, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
+  return hipGetLastError();
+}
+
 template <typename T>
 static hipError_t distill_t(DistillArgs a, const T* student, T* dstudent, void* ws, hipStream_t s) {
   auto group = [&](auto kernel, int rows) {
     kernel<<<(a.T + rows - 1) / rows, GROUP_THREADS, 0, s>>>(a, student, dstudent);
     return hipGetLastError();
   };
-  // 16 lanes a row where they hold its entries (4096 x 40 fp32: 4.7 us, 8.0
-  // with 64 lanes, 10.7 with a block; 16384 x 500 bf16: 24, 29 and 41), else a
-  // wave (40 entries: 29 against 41 with a block)
+  // 16 lanes a row where they hold its entries (4096 x 40 fp32: 4.5 us, 7.3 with
+  // 64 lanes, 8.8 with a block), and longer rows when there are many (16384 x 500
+  // bf16: 23, 25 and 29; 5000 x 500 fp32: 10.8, 10.9 and 12.2; 300 x 500 bf16:
+  // 10.2, 5.7 and 6.2), else a wave
   if (a.K <= 16 && a.V <= 64) return group(distill_group_kernel<T, 16, 4>, GROUP_THREADS / 16);
-  if (a.K <= 16 && a.V <= 512) return group(distill_group_kernel<T, 16, 32>, GROUP_THREADS / 16);
+  if (a.K <= 16 && a.V <= 512 && a.T > FEW_WAVES)
+    return group(distill_group_kernel<T, 16, 32>, GROUP_THREADS / 16);
   if (a.K <= 64 && a.V <= 512) return group(distill_group_kernel<T, 64, 8>, GROUP_THREADS / 64);
   const int units = row_units(a.V, sizeof(T));
   distill_segments(a.T, units, &a.segs, &a.seg_units);
@@ -702,20 +728,36 @@ static hipError_t distill_t(DistillArgs a, const T* student, T* dstudent, void* 
     }
     return hipSuccess;
   }
-  // the smallest block that holds the row: a row's chain of small steps (its
+  // A small block of eight units a thread: a row's chain of small steps (its
   // entries, joins, barriers) then overlaps that of more other rows on the CU
-  // (8192 x 2000 fp32: 33 us with 64 threads, 37 with 128, 45 with 256)
-  if (units <= 64 * 8)
-    block_launch<T, 64, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
-  else if (units <= 128 * 8)
-    block_launch<T, 128, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
-  else if (units <= 256 * 8)
-    block_launch<T, 256, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
-  else if (units <= HALF_ROW_UNITS)
-    block_launch<T, 512, 8, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
-  else
-    block_launch<T, 1024, 16, DISTILL_ROW, 4>(a, a.T, student, dstudent, s);
-  return hipGetLastError();
+  // (8192 x 2000 fp32: 33 us with 64 threads, 37 with 128, 45 with 256).  As
+  // long as all rows are on the GPU at once anyway (four waves a SIMD), four
+  // units and twice the threads shorten the chain (10 x 15000 bf16: 8.1 us with
+  // eight, 6.9 with four; 500 x 15001: 13.8, 13.0; 1000 x 15001: 19.4, 21.2).
+  // Rows of up to 256 units have a wave either way (16384 x 2000 bf16: 51, 48).
+  const bool few = (int64_t)a.T * ((units + 255) / 256) <= FEW_WAVES;
+  if (units <= 256) return row_launch<T, 64, 4>(a, student, dstudent, s);
+  if (units <= 512)
+    return few ? row_launch<T, 128, 4>(a, student, dstudent, s)
+               : row_launch<T, 64, 8>(a, student, dstudent, s);
+  if (units <= 1024)
+    return few ? row_launch<T, 256, 4>(a, student, dstudent, s)
+               : row_launch<T, 128, 8>(a, student, dstudent, s);
+  if (units <= 2048)
+    return few ? row_launch<T, 512, 4>(a, student, dstudent, s)
+               : row_launch<T, 256, 8>(a, student, dstudent, s);
+  if (units <= 4096) {
+    if (few) return row_launch<T, 1024, 4>(a, student, dstudent, s);
+    // fp32 rows keep sixteen units' exponentials in registers as well (2000 x
+    // 16000: 55 us, 61 with eight); bf16 rows hold twice as many a unit (2048 x
+    // 32000: 66 us, 61 with eight)
+    if constexpr (sizeof(T) == 4) return row_launch<T, 256, 16>(a, student, dstudent, s);
+    return row_launch<T, 512, 8>(a, student, dstudent, s);
+  }
+  // two blocks a CU, so that one reads while the other sums and writes (1000 x
+  // 65000 bf16: 65 us, 83 with 1024 threads of half the units)
+  if (units <= 8192) return row_launch<T, 512, 16>(a, student, dstudent, s);
+  return row_launch<T, 1024, 16>(a, student, dstudent, s);
 }
 
 hipError_t launch_distill(int T, int V, int64_t ld, int K, const void* student, bool is_bf16,

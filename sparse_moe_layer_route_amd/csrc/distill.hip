@@ -412,9 +412,10 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   const int id0 = tid < K ? a.ids[t * K + tid] : -1;
   const float t0 = tid < K ? a.t_logits[t * K + tid] : 0.f;
   // whole units, with what they hold of other rows (masked below); threads past
-  // the segment load its last one.  The last unit of the last row may pass the
-  // buffer's end and is put together from its elements.
-  const bool end = t == a.T - 1 && edge1 >= u0 && edge1 < u1;
+  // the segment load its last one.  A unit that passes the buffer's end (the last
+  // one of the last row) is put together from its elements.
+  const bool end = u1 == all_units && u1 > u0 &&
+                   t * a.ld - ph + (int64_t)all_units * EPU > (a.T - 1) * a.ld + V;
   const int n_whole = n_units - end;
   uint4 x[NU];
 #pragma unroll
@@ -429,7 +430,7 @@ distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {
   if (end) {
     T el[EPU];
 #pragma unroll
-    for (int e = 0; e < EPU; ++e) el[e] = row[min(max(edge1 * EPU - ph + e, 0), V - 1)];
+    for (int e = 0; e < EPU; ++e) el[e] = row[min(max((u1 - 1) * EPU - ph + e, 0), V - 1)];
     uint4 last;
     __builtin_memcpy(&last, el, 16);
 #pragma unroll

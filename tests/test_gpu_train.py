@@ -363,6 +363,46 @@ def test_distill(T, V, K, dtype, pad, tau, tail):
     assert torch.equal(l3, loss) and torch.equal(s2[:, :V], ds[:, :V])
 
 
+MANY = [  # T, V, K, dtype: more rows than the GPU holds at once, odd row lengths
+    (2101, 2401, 20, "bf16"), (4103, 1201, 3, "f32"), (1101, 6001, 70, "bf16"), (521, 12001, 9, "bf16"),
+    (1030, 3001, 5, "f32"), (301, 30001, 65, "bf16"), (353, 12001, 30, "f32"), (71, 50001, 17, "bf16"),
+    (70, 32001, 17, "f32"), (4200, 301, 16, "bf16"),
+]
+
+
+@pytest.mark.parametrize("T,V,K,dtype", MANY)
+def test_distill_many_rows(T, V, K, dtype):
+    say(f"[distill] T={T} V={V} K={K} {dtype}")
+    s, ids, u, lse = distill_case(T + V, T, V, K, dtype, False, 1.5, True)
+    ids, u, lse = ids.cuda(), u.cuda(), lse.cuda()
+    loss, ds = torch.full((T,), 3.0, device="cuda"), torch.full_like(s, 3.0)
+    ws = torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")
+    M.moe_distill_topk(T, V, K, s, ids, u, loss, ds, ws, teacher_lse=lse, temperature=1.5)
+    distill_check(s, ids, u, lse, V, 1.5, None, 1.0, dtype, loss, ds)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,ld", [(1, 1, 1), (2, 1, 1), (5, 3, 3), (4, 7, 9), (3, 9, 9)])
+def test_distill_more_entries_than_classes(T, V, ld, dtype):
+    """Each class named by many entries, rows shorter than a 16-byte load."""
+    K = 150
+    g = gen(37 * V + T)
+    flat = randn(g, (T - 1) * ld + V, dtype=dtype)
+    s = flat.as_strided((T, V), (ld, 1)).contiguous()
+    ids = torch.randint(-1, V + 1, (T, K), generator=g).to(torch.int32)
+    ids[:, :V] = torch.arange(V)
+    u = torch.randn(T, K, generator=g)
+    # of the mass, nine tenths are the entries'
+    lse = torch.stack([torch.logsumexp(u[t][(ids[t] >= 0) & (ids[t] < V)], 0) for t in range(T)]) + 0.1
+    for l in (None, lse.cuda()):
+        loss, ds = torch.empty(T, device="cuda"), torch.full_like(flat, 3.0)
+        M.moe_distill_topk(T, V, K, flat, ids.cuda(), u.cuda(), loss, ds, None, teacher_lse=l, ld=ld)
+        got = ds.as_strided((T, V), (ld, 1)).contiguous()
+        distill_check(s, ids, u, None if l is None else lse, V, 1.0, None, 1.0, dtype, loss, got)
+        for t in range(T - 1):
+            assert torch.all(ds[t * ld + V:(t + 1) * ld] == 3.0)
+
+
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("V", [40, 5000])
 def test_distill_skipped_doubled_and_masked(V, tail):

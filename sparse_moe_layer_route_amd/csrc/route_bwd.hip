@@ -9,9 +9,9 @@
 //   (0 or 1 for moe_route's ids; an expert named twice counts twice).
 //   dx = dx_add + dl W_r,  dW_r = dl^T x.
 //
-// Launches: the logits' gradient (route_dlogits_kernel), both products in one
-// grid (route_products_kernel), and, when dW is cut into ranges of tokens, the
-// sum of the ranges.  The products read x once and write dx once, which
+// Launches: up to 64 tokens one (route_few_kernel); else the logits' gradient
+// (route_dlogits_kernel), both products in one grid (route_products_kernel), and,
+// when dW is cut into ranges of tokens, the sum of the ranges.  The products read x once and write dx once, which
 // bounds them (E <= 64: 4 E flops for four bytes of bf16).
 //
 // bf16 layers run v_mfma_f32_16x16x32_bf16 on x and W as they are; dl is fp32
@@ -118,43 +118,36 @@ __device__ __forceinline__ float row_max(float v) {
   return fmaxf(v, row_move<0x140>(v));
 }
 
-// One block per 32 tokens, 16 lanes a token: lane l holds experts l + 16 q and
-// slot l's id and gradient.  dlogits_add may be dlogits itself.  pad (fp32
-// layers, else null): dlogits again as [32 steps][16 mt], zero past T and E.
-// fx / fw (bf16 layers, else null): the block's fragments,
-//   fx [16-token tile][k step][part][lane]: token lane % 16, experts
-//     32 s + 8 (lane / 16) .. +7 (zero past T and E),
-//   fw [32-token step][expert tile][part][lane]: expert lane % 16, tokens
-//     8 (lane / 16) .. +7.
-// The parts of a value are it rounded to bf16, what is left rounded, and so on
-// (a value that is not finite leaves NaN).
-// No branch on a lane's expert or slot: selects only, so that all loads of a
-// token go out together (64 x 64: 8.7 us with branches, 3.9 without, a launch and
-// a chain of short steps; 16384 x 64: 7.9, of 8 MB read and 14 written).
-__global__ void __launch_bounds__(RBWD_THREADS)
-route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict__ ids,
-                     const float* __restrict__ logits, const float* __restrict__ dtopk_w,
-                     const float* dlogits_add, float* dlogits, int mt, int ks,
-                     float* __restrict__ pad, uint4* __restrict__ fx, uint4* __restrict__ fw) {
-  static_assert(RBWD_THREADS == 16 * RBWD_STEP, "16 lanes a token");
-  constexpr int Q = MOE_MAX_EXPERTS / 16;
-  __shared__ float tile[RBWD_STEP][MOE_MAX_EXPERTS + 1];
-  const int tt = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int t = blockIdx.x * RBWD_STEP + tt;
-  const int64_t tc = min(t, T - 1);  // tokens past T read the last one
-  float dl[Q];
+struct DlogitsArgs {
+  int T, E, k, renorm;
+  const int32_t* ids;
+  const float *logits, *dtopk_w;
+  const float* add;  // may be dlogits itself
+  float* dlogits;
+};
+constexpr int RBWD_Q = MOE_MAX_EXPERTS / 16;
+typedef float rbwd_tile_t[RBWD_STEP][MOE_MAX_EXPERTS + 1];
+
+// dl of token t by 16 lanes: lane l holds experts l + 16 q and slot l's id and
+// gradient.  Tokens past T get the last one's.  No branch on a lane's expert or
+// slot: selects only, so that all loads of a token go out together (64 x 64: 8.7
+// us with branches, 3.9 without, a launch and a chain of short steps).
+__device__ __forceinline__ void token_dlogits(const DlogitsArgs& a, int t, float (&dl)[RBWD_Q]) {
+  constexpr int Q = RBWD_Q;
+  const int l = threadIdx.x & 15, E = a.E, k = a.k;
+  const bool renorm = a.renorm;
+  const int64_t tc = min(t, a.T - 1);
 #pragma unroll
-  for (int q = 0; q < Q; ++q)
-    dl[q] = dlogits_add ? dlogits_add[tc * E + min(l + 16 * q, E - 1)] : 0.f;
-  if (dtopk_w) {
+  for (int q = 0; q < Q; ++q) dl[q] = a.add ? a.add[tc * E + min(l + 16 * q, E - 1)] : 0.f;
+  if (a.dtopk_w) {
     float v[Q], G[Q], n[Q];
     bool part[Q];
     const int64_t o = tc * k + min(l, k - 1);
-    const int id = l < k ? ids[o] : -1;  // slots past k match no expert
-    const float g = dtopk_w[o];
+    const int id = l < k ? a.ids[o] : -1;  // slots past k match no expert
+    const float g = a.dtopk_w[o];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      v[q] = logits[tc * E + min(l + 16 * q, E - 1)];
+      v[q] = a.logits[tc * E + min(l + 16 * q, E - 1)];
       G[q] = n[q] = 0.f;
     }
     // slot J's id and gradient come from lane J of the token's row
@@ -199,19 +192,31 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
     for (int q = 0; q < Q; ++q)
       dl[q] += part[q] ? v[q] * (G[q] - (renorm ? n[q] : 1.f) * c) : 0.f;
   }
+}
+// Token t's row of dlogits (store), of a tile of 32 tokens and of pad (or null).
+__device__ __forceinline__ void put_dlogits(const DlogitsArgs& a, int t, const float (&dl)[RBWD_Q],
+                                            bool store, rbwd_tile_t& tile, int mt, float* pad) {
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const int e = l + 16 * q;
-    const bool on = e < E && t < T;
-    if (on) dlogits[(int64_t)t * E + e] = dl[q];
+  for (int q = 0; q < RBWD_Q; ++q) {
+    const int e = (threadIdx.x & 15) + 16 * q;
+    const bool on = e < a.E && t < a.T;
+    if (on && store) a.dlogits[(int64_t)t * a.E + e] = dl[q];
     if (pad && q < mt) pad[(int64_t)t * (16 * mt) + e] = on ? dl[q] : 0.f;
-    tile[tt][e] = on ? dl[q] : 0.f;
+    tile[t % RBWD_STEP][e] = on ? dl[q] : 0.f;
   }
-  if (!fx && !fw) return;
-  __syncthreads();
+}
+// The fragments of a tile, fx and fw each where not null:
+//   fx [16-token tile][k step][part][lane]: token lane % 16, experts
+//     32 s + 8 (lane / 16) .. +7 (zero past T and E),
+//   fw [expert tile][part][lane]: expert lane % 16, tokens 8 (lane / 16) .. +7.
+// The parts of a value are it rounded to bf16, what is left rounded, and so on
+// (a value that is not finite leaves NaN).
+template <int NT>
+__device__ __forceinline__ void pack_dlogits(const rbwd_tile_t& tile, int mt, int ks, uint4* fx,
+                                             uint4* fw) {
   // one thread per fragment slot, all of its parts
   const int nx = fx ? 2 * ks * 64 : 0, nw = fw ? mt * 64 : 0;
-  for (int i = threadIdx.x; i < nx + nw; i += RBWD_THREADS) {
+  for (int i = threadIdx.x; i < nx + nw; i += NT) {
     const bool to_x = i < nx;
     const int l16 = i & 15, g8 = 8 * ((i >> 4) & 3), f = (to_x ? i : i - nx) >> 6;
     const int half = ks == 2 ? f >> 1 : f, st = ks == 2 ? f & 1 : 0;
@@ -221,8 +226,7 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] = src[c * step];
     const int parts = to_x ? RBWD_DX_PARTS : RBWD_DW_PARTS;
-    uint4* dst = to_x ? fx + ((int64_t)blockIdx.x * 2 * ks + f) * RBWD_DX_PARTS * 64
-                      : fw + ((int64_t)blockIdx.x * mt + f) * RBWD_DW_PARTS * 64;
+    uint4* dst = to_x ? fx + f * RBWD_DX_PARTS * 64 : fw + f * RBWD_DW_PARTS * 64;
 #pragma unroll
     for (int p = 0; p < RBWD_DW_PARTS; ++p) {
       uint32_t w[4];
@@ -235,6 +239,25 @@ route_dlogits_kernel(int T, int E, int k, int renorm, const int32_t* __restrict_
       if (p < parts) dst[p * 64 + (i & 63)] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// One block per 32 tokens.  pad (fp32 layers, else null): dlogits again as [32
+// steps][16 mt], zero past T and E.  fx / fw (bf16 layers, else null): the
+// fragments of all steps in turn.  16384 x 64: 7.9 us, of 8 MB read and 14 written.
+__global__ void __launch_bounds__(RBWD_THREADS)
+route_dlogits_kernel(DlogitsArgs a, int mt, int ks, float* __restrict__ pad,
+                     uint4* __restrict__ fx, uint4* __restrict__ fw) {
+  static_assert(RBWD_THREADS == 16 * RBWD_STEP, "16 lanes a token");
+  __shared__ rbwd_tile_t tile;
+  const int t = blockIdx.x * RBWD_STEP + (threadIdx.x >> 4);
+  float dl[RBWD_Q];
+  token_dlogits(a, t, dl);
+  put_dlogits(a, t, dl, true, tile, mt, pad);
+  if (!fx && !fw) return;
+  __syncthreads();
+  pack_dlogits<RBWD_THREADS>(
+      tile, mt, ks, fx ? fx + (int64_t)blockIdx.x * 2 * ks * RBWD_DX_PARTS * 64 : nullptr,
+      fw ? fw + (int64_t)blockIdx.x * mt * RBWD_DW_PARTS * 64 : nullptr);
 }
 
 // Eight columns of eight rows -> fragment c: column c, the eight rows in k
@@ -644,7 +667,7 @@ __device__ __forceinline__ int xcd_item(int b, int n) {
 
 // Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx: one
 // launch, and a CU may hold a block of each (8192 x 2048, 64 experts: 29.0 us for
-// the whole call, 30.6 with a launch each; 64 x 2048: 9.1 and 12.3).
+// the whole call, 30.6 with a launch each).
 template <typename T, int MT>
 __global__ void __launch_bounds__(PROD_THREADS, 2)
 route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
@@ -659,6 +682,52 @@ route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
     const int b = xcd_item(b0 - nw, nx);
     const int item = b * PROD_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (b < nx && item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
+  }
+}
+
+// One or two steps of tokens: the products' blocks each form the gradient of all
+// logits for themselves, in LDS, and the first one stores it, so that the call is
+// one launch.  Not where dlogits is the addend too: other blocks read it.  bf16,
+// 2048 columns, 64 experts: 32 tokens 7.0 us, 8.5 with the logits' gradient in a
+// launch of its own; 64 tokens 9.0 both ways, and 2.6 us less of the caller's time.
+template <typename T, int MT, int STEPS>
+__global__ void __launch_bounds__(RBWD_THREADS, 2)
+route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restrict__ x,
+                 const T* __restrict__ w, const T* dx_add, T* dx) {
+  constexpr int KS = (MT + 1) / 2;
+  constexpr int TILES = STEPS * (int)sizeof(rbwd_tile_t) / 4;
+  constexpr int SUMS = dw_lds_floats<T, MT>();
+  constexpr int FX = 2 * KS * RBWD_DX_PARTS * 64, FW = MT * RBWD_DW_PARTS * 64;  // a step's
+  constexpr int PACK = sizeof(T) == 2 ? (FX > FW ? FX : FW) : RBWD_STEP * 16 * MT / 4;
+  __shared__ __align__(16) float lds[TILES > SUMS ? TILES : SUMS];  // the tiles, then dW's sums
+  __shared__ uint4 packed[STEPS * PACK];
+  rbwd_tile_t* tile = reinterpret_cast<rbwd_tile_t*>(lds);
+  float* pad = sizeof(T) == 4 ? reinterpret_cast<float*>(packed) : nullptr;
+  const bool for_dw = (int)blockIdx.x < a.dw_blocks;
+  // the loads of all steps go out together
+  const int t = threadIdx.x >> 4;
+  float dl[STEPS][RBWD_Q];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) token_dlogits(g, t + s * RBWD_STEP, dl[s]);
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+    put_dlogits(g, t + s * RBWD_STEP, dl[s], blockIdx.x == 0, tile[s], MT, pad);
+  __syncthreads();
+  if (sizeof(T) == 2) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+      pack_dlogits<RBWD_THREADS>(tile[s], MT, KS, for_dw ? nullptr : packed + s * FX,
+                                 for_dw ? packed + s * FW : nullptr);
+    __syncthreads();
+  }
+  a.pad = pad;
+  a.fx = a.fw = packed;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (for_dw) {
+    if (wv < PROD_WAVES) route_dw<T, MT>(a, blockIdx.x, x, lds);  // its barriers wait for these
+  } else {
+    const int item = (blockIdx.x - a.dw_blocks) * (RBWD_THREADS / MOE_WAVE) + wv;
+    if (item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
   }
 }
 
@@ -683,8 +752,16 @@ int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
 }
 
 template <typename T, int MT>
-static hipError_t launch_products(const RouteBwdArgs& a, int dx_items, const void* x, const void* w,
-                                  const void* dx_add, void* dx, hipStream_t s) {
+static hipError_t launch_products(const DlogitsArgs* few, const RouteBwdArgs& a, int dx_items,
+                                  const void* x, const void* w, const void* dx_add, void* dx,
+                                  hipStream_t s) {
+  if (few) {
+    constexpr int waves = RBWD_THREADS / MOE_WAVE;
+    const auto kernel = a.steps == 1 ? route_few_kernel<T, MT, 1> : route_few_kernel<T, MT, 2>;
+    kernel<<<a.dw_blocks + (dx_items + waves - 1) / waves, RBWD_THREADS, 0, s>>>(
+        *few, a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
+    return hipGetLastError();
+  }
   const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
   route_products_kernel<T, MT>
       <<<((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7), PROD_THREADS, 0, s>>>(
@@ -697,14 +774,14 @@ static hipError_t launch_products(const RouteBwdArgs& a, int dx_items, const voi
   return hipGetLastError();
 }
 template <typename T>
-static hipError_t launch_products_t(int mt, const RouteBwdArgs& a, int dx_items, const void* x,
-                                    const void* w, const void* dx_add, void* dx,
-                                    hipStream_t s) {
+static hipError_t launch_products_t(int mt, const DlogitsArgs* few, const RouteBwdArgs& a,
+                                    int dx_items, const void* x, const void* w,
+                                    const void* dx_add, void* dx, hipStream_t s) {
   switch (mt) {
-    case 1: return launch_products<T, 1>(a, dx_items, x, w, dx_add, dx, s);
-    case 2: return launch_products<T, 2>(a, dx_items, x, w, dx_add, dx, s);
-    case 3: return launch_products<T, 3>(a, dx_items, x, w, dx_add, dx, s);
-    default: return launch_products<T, 4>(a, dx_items, x, w, dx_add, dx, s);
+    case 1: return launch_products<T, 1>(few, a, dx_items, x, w, dx_add, dx, s);
+    case 2: return launch_products<T, 2>(few, a, dx_items, x, w, dx_add, dx, s);
+    case 3: return launch_products<T, 3>(few, a, dx_items, x, w, dx_add, dx, s);
+    default: return launch_products<T, 4>(few, a, dx_items, x, w, dx_add, dx, s);
   }
 }
 
@@ -727,17 +804,20 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
   float* pad = !packs && (dx || dw) ? reinterpret_cast<float*>(base + p.fx) : nullptr;
   uint4* fx = packs && dx ? reinterpret_cast<uint4*>(base + p.fx) : nullptr;
   uint4* fw = packs && dw ? reinterpret_cast<uint4*>(base + p.fw) : nullptr;
-  route_dlogits_kernel<<<p.steps, RBWD_THREADS, 0, s>>>(T, d.n_experts, d.top_k, d.renormalize, ids,
-                                                        logits, dtopk_w, dlogits_add, dlogits, p.mt,
-                                                        p.ks, pad, fx, fw);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (!dx && !dw)) return e;
+  const DlogitsArgs g{T, d.n_experts, d.top_k, d.renormalize, ids, logits, dtopk_w, dlogits_add,
+                      dlogits};
+  const bool few = (dx || dw) && p.steps <= 2 && p.splits == 1 && dlogits_add != dlogits;
+  if (!few) {
+    route_dlogits_kernel<<<p.steps, RBWD_THREADS, 0, s>>>(g, p.mt, p.ks, pad, fx, fw);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!dx && !dw)) return e;
+  }
   const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles, dw ? p.splits * p.ncg : 0,
                        pad, fx, fw,
                        p.splits > 1 ? reinterpret_cast<float*>(base + p.part) : nullptr, dw, accumulate};
   const int dx_items = dx ? (2 * p.steps + p.dx_tiles - 1) / p.dx_tiles * p.ncg : 0;
-  if (packs) return launch_products_t<bf16>(p.mt, a, dx_items, x, w_router, dx_add, dx, s);
-  return launch_products_t<float>(p.mt, a, dx_items, x, w_router, dx_add, dx, s);
+  if (packs) return launch_products_t<bf16>(p.mt, few ? &g : nullptr, a, dx_items, x, w_router, dx_add, dx, s);
+  return launch_products_t<float>(p.mt, few ? &g : nullptr, a, dx_items, x, w_router, dx_add, dx, s);
 }
 
 }  // namespace moe

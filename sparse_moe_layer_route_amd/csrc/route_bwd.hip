@@ -11,8 +11,9 @@
 //
 // Launches: up to 64 tokens one (route_few_kernel); else the logits' gradient
 // (route_dlogits_kernel), both products in one grid (route_products_kernel), and,
-// when dW is cut into ranges of tokens, the sum of the ranges.  The products read x once and write dx once, which
-// bounds them (E <= 64: 4 E flops for four bytes of bf16).
+// when dW is cut into ranges of tokens, the sum of the ranges.  The products read
+// x once and write dx once, which bounds them (E <= 64: 4 E flops for four bytes
+// of bf16).
 //
 // bf16 layers run v_mfma_f32_16x16x32_bf16 on x and W as they are; dl is fp32
 // and goes in as bf16 parts whose sum it is: three for dW (fp32 out, what is
@@ -54,6 +55,7 @@ struct RouteBwdPlan {
   int mt, ks, steps, ncg;
   int splits;              // token ranges of dW
   int dx_tiles;            // 16-token tiles of one dx wave
+  bool apart;              // dW and dx in launches of their own
   size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments (fp32 layers: padded
                                // dlogits at fx), dW partials
 };
@@ -64,6 +66,11 @@ constexpr int RBWD_DX_WAVES = 2048;
 // One dW block a CU: more ranges cost more partials than they gain (the same
 // shape: 38 us with 9 ranges, 43 with 18).
 constexpr int RBWD_DW_BLOCKS = 256;
+// fp32 products are bound by the matrix units.  From this many on dW and dx have a
+// launch each (8192 x 3584, 64 experts: 96 us for the call, 119 in one launch; 2048
+// x 2048, 64 experts: 25.6, 26.8, 40 experts: 23.1, 22.4) and dx one wave a SIMD: two
+// take longer than one with the work of both (8192 x 3584: 50 us against 58).
+constexpr int64_t RBWD_APART = 1 << 28;
 
 static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   RouteBwdPlan p{};
@@ -81,7 +88,8 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   const int most = std::max(1, (p.steps + least - 1) / least);
   p.splits = std::min(most, std::max(1, RBWD_DW_BLOCKS / p.ncg));
   const int tiles = 2 * p.steps;
-  const int ranges = std::max(1, RBWD_DX_WAVES / p.ncg);
+  p.apart = d.dtype == MOE_F32 && (int64_t)T * d.hidden * (16 * p.mt) >= RBWD_APART;
+  const int ranges = std::max(1, (p.apart ? RBWD_DX_WAVES / 2 : RBWD_DX_WAVES) / p.ncg);
   p.dx_tiles = (tiles + ranges - 1) / ranges;
   size_t o = 0;
   auto take = [&](size_t n) {
@@ -411,26 +419,28 @@ __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __r
                                          f32x4_t (&acc)[DwShape<MT>::MW][4]) {
   constexpr int MW = DwShape<MT>::MW, WAYS = DwShape<MT>::WAYS;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+  // the lane's byte offsets; the rest of an address is the same for the wave
+  const uint32_t x_off = (uint32_t)(g * a.H + col) * 4u, p_off = (uint32_t)(g * 16 * MT + n) * 4u;
   struct Half {
     float4 v[4];
     float d[4][MW];
   } h0, h1;
   auto load = [&](Half& h, int s, int half) {
+    const int t = s * RBWD_STEP + 16 * half;
+    const char* px = reinterpret_cast<const char*>(x + (int64_t)t * a.H);
+    const char* pp = reinterpret_cast<const char*>(a.pad + (int64_t)t * (16 * MT));
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int t = s * RBWD_STEP + 16 * half + 4 * q + g;
-      h.v[q] = *reinterpret_cast<const float4*>(x + (int64_t)min(t, a.T - 1) * a.H + col);
+      h.v[q] = *reinterpret_cast<const float4*>(px + (int64_t)q * 16 * a.H + x_off);
 #pragma unroll
-      for (int m = 0; m < MW; ++m)
-        h.d[q][m] = m0 + m < MT ? a.pad[(int64_t)t * (16 * MT) + 16 * (m0 + m) + n] : 0.f;
+      for (int m = 0; m < MW; ++m)  // past the last tile the first one's, dropped at the end
+        h.d[q][m] = *reinterpret_cast<const float*>(
+            pp + (4 * q * MT + (m0 + m < MT ? m0 + m : 0)) * 64 + p_off);
     }
   };
-  auto mfma = [&](Half& h, int s, int half) {
-    const bool whole = (s + 1) * RBWD_STEP <= a.T;
+  auto mfma = [&](const Half& h) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (!whole && s * RBWD_STEP + 16 * half + 4 * q + g >= a.T)
-        h.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);  // read the last row, times zero
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int m = 0; m < MW; ++m) {
         acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].x, acc[m][0], 0, 0, 0);
@@ -438,19 +448,35 @@ __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __r
         acc[m][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].z, acc[m][2], 0, 0, 0);
         acc[m][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(h.d[q][m], h.v[q].w, acc[m][3], 0, 0, 0);
       }
-    }
   };
-  const int s0 = r0 + way;
-  if (s0 >= s1) return;
-  // half steps in turn, each asked for before the one before it is multiplied
-  load(h0, s0, 0);
-  for (int s = s0; s < s1; s += WAYS) {
-    load(h1, s, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    mfma(h0, s, 0);
-    load(h0, min(s + WAYS, s1 - 1), 0);
-    __builtin_amdgcn_sched_barrier(0);
-    mfma(h1, s, 1);
+  const int whole = a.T / RBWD_STEP;  // steps with all their rows
+  const int e = min(s1, whole), s0 = r0 + way;
+  if (s0 < e) {
+    // half steps in turn, each asked for before the one before it is multiplied
+    load(h0, s0, 0);
+    for (int s = s0; s < e; s += WAYS) {
+      load(h1, s, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      mfma(h0);
+      load(h0, min(s + WAYS, e - 1), 0);
+      __builtin_amdgcn_sched_barrier(0);
+      mfma(h1);
+    }
+  }
+  if (whole < s1 && whole >= s0 && (whole - s0) % WAYS == 0) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int t = whole * RBWD_STEP + 16 * half + 4 * q + g;
+        h0.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < a.T) h0.v[q] = *reinterpret_cast<const float4*>(x + (int64_t)t * a.H + col);
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+          h0.d[q][m] = a.pad[(int64_t)t * (16 * MT) + 16 * (m0 + m < MT ? m0 + m : 0) + n];
+      }
+      mfma(h0);
+    }
   }
 }
 
@@ -611,50 +637,59 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
         wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * 64 +
                                                     4 * (n >> 2) + 16 * (n & 3));
     }
-  // a tile's loads go out before the tile before it is stored
-  float4 d[MT], add[4];
-  auto load = [&](int tl) {
+  // a tile's loads go out before the products of the tile before it: loads and
+  // stores retire in one order, so they wait for the stores of the one before that
+  struct Tile {
+    float4 d[MT], add[4];
+  } b0, b1;
+  auto load = [&](Tile& b, int tl) {
     const int64_t t = min(tl * 16 + n, a.T - 1);
 #pragma unroll
     for (int q = 0; q < MT; ++q)
-      d[q] = *reinterpret_cast<const float4*>(a.pad + (int64_t)(tl * 16 + n) * (16 * MT) + 16 * q + 4 * g);
+      b.d[q] = *reinterpret_cast<const float4*>(a.pad + (int64_t)(tl * 16 + n) * (16 * MT) +
+                                                16 * q + 4 * g);
     if (dx_add) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        add[i] = *reinterpret_cast<const float4*>(dx_add + t * a.H + cg * 64 + 4 * g + 16 * i);
+        b.add[i] = *reinterpret_cast<const float4*>(dx_add + t * a.H + cg * 64 + 4 * g + 16 * i);
     }
   };
-#pragma unroll
-  for (int i = 0; i < 4; ++i) add[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  load(t0);
-  for (int tl = t0; tl < t1; ++tl) {
+  auto products = [&](const Tile& b, int tl) {
     const int t = tl * 16 + n;
     f32x4_t acc[4];
 #pragma unroll
     for (int q = 0; q < MT; ++q)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float dv = r == 0 ? d[q].x : r == 1 ? d[q].y : r == 2 ? d[q].z : d[q].w;
+        const float4 d = b.d[q], v = wf[q][r];
+        const float dv = r == 0 ? d.x : r == 1 ? d.y : r == 2 ? d.z : d.w;
         const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
         const bool first = q == 0 && r == 0;
-        acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].x, dv, first ? zero : acc[0], 0, 0, 0);
-        acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].y, dv, first ? zero : acc[1], 0, 0, 0);
-        acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].z, dv, first ? zero : acc[2], 0, 0, 0);
-        acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[q][r].w, dv, first ? zero : acc[3], 0, 0, 0);
+        acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.x, dv, first ? zero : acc[0], 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.y, dv, first ? zero : acc[1], 0, 0, 0);
+        acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.z, dv, first ? zero : acc[2], 0, 0, 0);
+        acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(v.w, dv, first ? zero : acc[3], 0, 0, 0);
       }
-    float4 o[4];
+    if (t >= a.T) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o[i] = make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
-      if (dx_add)
-        o[i] = make_float4(o[i].x + add[i].x, o[i].y + add[i].y, o[i].z + add[i].z, o[i].w + add[i].w);
+      float4 o = make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
+      if (dx_add) {
+        const float4 e = b.add[i];
+        o = make_float4(o.x + e.x, o.y + e.y, o.z + e.z, o.w + e.w);
+      }
+      *reinterpret_cast<float4*>(dx + (int64_t)t * a.H + cg * 64 + 4 * g + 16 * i) = o;
     }
-    if (tl + 1 < t1) load(tl + 1);
-    if (t < a.T) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(dx + (int64_t)t * a.H + cg * 64 + 4 * g + 16 * i) = o[i];
-    }
+  };
+  load(b0, t0);
+  for (int tl = t0; tl < t1; tl += 2) {
+    if (tl + 1 < t1) load(b1, tl + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    products(b0, tl);
+    if (tl + 1 >= t1) break;
+    if (tl + 2 < t1) load(b0, tl + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    products(b1, tl + 1);
   }
 }
 
@@ -678,6 +713,10 @@ route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
     const int item = xcd_item(b0, a.dw_blocks);
     if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
   } else {
+    // fp32: dx first, so that dW's long waves have a SIMD to themselves early (2048
+    // x 2048, 40 experts: 21.1 us for the call, 24.8 at one priority; a bf16 call
+    // loses by it: 16384 x 3584 83, 74)
+    if (sizeof(T) == 4) __builtin_amdgcn_s_setprio(3);
     const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
     const int b = xcd_item(b0 - nw, nx);
     const int item = b * PROD_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -752,7 +791,8 @@ int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
 }
 
 template <typename T, int MT>
-static hipError_t launch_products(const DlogitsArgs* few, const RouteBwdArgs& a, int dx_items,
+static hipError_t launch_products(const RouteBwdPlan& p, const DlogitsArgs* few,
+                                  const RouteBwdArgs& a, int dx_items,
                                   const void* x, const void* w, const void* dx_add, void* dx,
                                   hipStream_t s) {
   if (few) {
@@ -762,11 +802,16 @@ static hipError_t launch_products(const DlogitsArgs* few, const RouteBwdArgs& a,
         *few, a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
     return hipGetLastError();
   }
-  const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;
-  route_products_kernel<T, MT>
-      <<<((a.dw_blocks + 7) & ~7) + ((nx + 7) & ~7), PROD_THREADS, 0, s>>>(
-          a, dx_items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
-  const hipError_t e = hipGetLastError();
+  auto run = [&](RouteBwdArgs b, int dw_blocks, int items) {
+    b.dw_blocks = dw_blocks;
+    const int nx = (items + PROD_WAVES - 1) / PROD_WAVES;
+    route_products_kernel<T, MT><<<((dw_blocks + 7) & ~7) + ((nx + 7) & ~7), PROD_THREADS, 0, s>>>(
+        b, items, (const T*)x, (const T*)w, (const T*)dx_add, (T*)dx);
+    return hipGetLastError();
+  };
+  const bool apart = p.apart && a.dw_blocks > 0 && dx_items > 0;
+  hipError_t e = run(a, a.dw_blocks, apart ? 0 : dx_items);
+  if (e == hipSuccess && apart) e = run(a, 0, dx_items);
   if (e != hipSuccess || !a.dw || a.splits == 1) return e;
   const int n4 = (int)((int64_t)a.E * a.H / 4);
   route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
@@ -774,14 +819,14 @@ static hipError_t launch_products(const DlogitsArgs* few, const RouteBwdArgs& a,
   return hipGetLastError();
 }
 template <typename T>
-static hipError_t launch_products_t(int mt, const DlogitsArgs* few, const RouteBwdArgs& a,
-                                    int dx_items, const void* x, const void* w,
-                                    const void* dx_add, void* dx, hipStream_t s) {
-  switch (mt) {
-    case 1: return launch_products<T, 1>(few, a, dx_items, x, w, dx_add, dx, s);
-    case 2: return launch_products<T, 2>(few, a, dx_items, x, w, dx_add, dx, s);
-    case 3: return launch_products<T, 3>(few, a, dx_items, x, w, dx_add, dx, s);
-    default: return launch_products<T, 4>(few, a, dx_items, x, w, dx_add, dx, s);
+static hipError_t launch_products_t(const RouteBwdPlan& p, const DlogitsArgs* few,
+                                    const RouteBwdArgs& a, int dx_items, const void* x,
+                                    const void* w, const void* dx_add, void* dx, hipStream_t s) {
+  switch (p.mt) {
+    case 1: return launch_products<T, 1>(p, few, a, dx_items, x, w, dx_add, dx, s);
+    case 2: return launch_products<T, 2>(p, few, a, dx_items, x, w, dx_add, dx, s);
+    case 3: return launch_products<T, 3>(p, few, a, dx_items, x, w, dx_add, dx, s);
+    default: return launch_products<T, 4>(p, few, a, dx_items, x, w, dx_add, dx, s);
   }
 }
 
@@ -812,12 +857,13 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!dx && !dw)) return e;
   }
-  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles, dw ? p.splits * p.ncg : 0,
-                       pad, fx, fw,
+  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles,
+                       dw ? p.splits * p.ncg : 0, pad, fx, fw,
                        p.splits > 1 ? reinterpret_cast<float*>(base + p.part) : nullptr, dw, accumulate};
   const int dx_items = dx ? (2 * p.steps + p.dx_tiles - 1) / p.dx_tiles * p.ncg : 0;
-  if (packs) return launch_products_t<bf16>(p.mt, few ? &g : nullptr, a, dx_items, x, w_router, dx_add, dx, s);
-  return launch_products_t<float>(p.mt, few ? &g : nullptr, a, dx_items, x, w_router, dx_add, dx, s);
+  const DlogitsArgs* in_one = few ? &g : nullptr;
+  if (packs) return launch_products_t<bf16>(p, in_one, a, dx_items, x, w_router, dx_add, dx, s);
+  return launch_products_t<float>(p, in_one, a, dx_items, x, w_router, dx_add, dx, s);
 }
 
 }  // namespace moe

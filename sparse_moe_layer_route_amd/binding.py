@@ -188,8 +188,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 # The current stream's handle without building a torch.cuda.Stream for it (0.3
-# against 3 us a call); not every torch build has it.
+# against 3 us a call) and the current device's number; not every torch build has
+# them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream, dev=None):
@@ -395,7 +397,10 @@ _MOE_DTYPES = {v: k for k, v in _TORCH_DTYPES.items()}
 def _device(stream):
     """The current GPU, which the stream has to belong to; -2, no tensor's
     device, before torch has touched one."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    if not torch.cuda.is_initialized():
+        dev = -2
+    else:
+        dev = _raw_device() if _raw_device is not None else torch.cuda.current_device()
     if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the current GPU is {dev}")
     return dev
@@ -404,13 +409,15 @@ def _device(stream):
 def _arg(dev, name, t, n, dtype, optional=False):
     """Address of a contiguous tensor of at least n elements of `dtype` on
     GPU `dev`; None where optional."""
-    if isinstance(t, torch.Tensor):
+    if t is None and optional:
+        return None
+    try:
         if (t.dtype is dtype and t.numel() >= n and t.get_device() == dev
                 and t.is_contiguous()):
             return t.data_ptr()
-    elif t is None and optional:
-        return None
-    else:
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")

@@ -82,7 +82,7 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   // each range gives every set of its block's waves four steps at least, fp32
   // layers (twice the matrix time a step) two: fewer cost more in partials than
   // the blocks gain (4096 x 1536, 40 experts: 18.2 us with four, 20.8 with two,
-  // 21.0 with one; fp32 1024 x 2048, 64 experts: 22.1, 18.6 and 18.8)
+  // 21.0 with one; fp32 1024 x 2048, 64 experts: 20.8, 19.5 and 19.6)
   const int ways = p.mt > 1 ? PROD_WAVES / 2 : PROD_WAVES;
   const int least = ways * (d.dtype == MOE_BF16 ? 4 : 2);
   const int most = std::max(1, (p.steps + least - 1) / least);
@@ -714,7 +714,7 @@ route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
     if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
   } else {
     // fp32: dx first, so that dW's long waves have a SIMD to themselves early (2048
-    // x 2048, 40 experts: 21.1 us for the call, 24.8 at one priority; a bf16 call
+    // x 2048, 40 experts: 22.1 us for the call, 25.3 at one priority; a bf16 call
     // loses by it: 16384 x 3584 83, 74)
     if (sizeof(T) == 4) __builtin_amdgcn_s_setprio(3);
     const int nx = (dx_items + PROD_WAVES - 1) / PROD_WAVES;

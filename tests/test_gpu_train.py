@@ -159,7 +159,8 @@ ROUTE = [  # T, H, E, k, dtype, renorm
     (1, 64, 2, 1, "bf16", True), (1, 2048, 64, 6, "bf16", False), (5, 64, 64, 8, "f32", True),
     (37, 192, 40, 8, "bf16", True), (300, 576, 17, 3, "f32", False), (129, 1536, 40, 8, "bf16", False),
     (1030, 320, 64, 8, "bf16", True), (64, 4160, 33, 5, "bf16", True), (257, 256, 8, 2, "f32", True),
-    (2200, 128, 1, 1, "bf16", False),
+    (2200, 128, 1, 1, "bf16", False), (32, 640, 24, 4, "bf16", True), (33, 192, 48, 2, "f32", False),
+    (64, 128, 64, 8, "f32", True), (65, 2048, 50, 4, "bf16", False), (4200, 1024, 60, 4, "f32", True),
 ]
 
 
@@ -282,6 +283,46 @@ def test_route_backward_of_an_empty_batch():
     assert torch.all(dw == 3.0)
     M.moe_route_backward(d, 0, None, None, None, None, e, e, None, dw, None)
     assert torch.all(dw == 0.0)
+
+
+@pytest.mark.parametrize("T,H,E,dtype", [(20, 256, 40, "bf16"), (64, 2048, 64, "bf16"), (900, 192, 20, "bf16"),
+                                         (41, 320, 9, "f32"), (4200, 1024, 64, "f32")])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_route_backward_in_a_graph(T, H, E, dtype, in_place):
+    """Replayed over new logits and a workspace full of what was there; the
+    eager call goes to a stream of its own."""
+    g, k = gen(T + E), 3
+    x, w = randn(g, T, H, dtype=dtype), randn(g, E, H, dtype=dtype, std=0.05)
+    logits, dtw = randn(g, T, E), randn(g, T, k)
+    ids = torch.topk(logits, k, dim=1).indices.to(torch.int32).contiguous()
+    d = make_dims(H, E, k, dtype, True)
+    side = torch.cuda.Stream()
+
+    def bufs():
+        return dict(dl=torch.zeros(T, E, device="cuda"), dx=torch.zeros(T, H, dtype=TT[dtype], device="cuda"),
+                    dw=torch.zeros(E, H, device="cuda"),
+                    ws=torch.empty(M.moe_route_backward_size(d, T), dtype=torch.uint8, device="cuda"))
+
+    def run(b, stream=None):
+        M.moe_route_backward(d, T, x, w, ids, logits, dtw, b["dl"], b["dx"], b["dw"], b["ws"],
+                             dlogits_add=b["dl"] if in_place else None,
+                             dx_add=b["dx"] if in_place else None, accumulate_dw=in_place, stream=stream)
+
+    got, want = bufs(), bufs()
+    run(bufs())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got)
+    for i in range(4):
+        logits.copy_(randn(gen(i), T, E))
+        got["ws"].fill_(255)
+        torch.cuda.synchronize()
+        run(want, side)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ("dl", "dx", "dw"):
+            assert torch.equal(got[n], want[n]) and torch.isfinite(got[n]).all(), (i, n)
 
 
 # ------------------------------------------------------------ distillation --
@@ -499,6 +540,34 @@ def test_distill_many_rows_in_segments():
     assert torch.equal(loss, loss[:R][at])
     for t0 in range(0, T, 4096):
         assert torch.equal(big[t0:t0 + 4096], big[:R][at[t0:t0 + 4096]])
+
+
+@pytest.mark.parametrize("T,V,K,dtype", [(5, 40, 8, "f32"), (300, 500, 12, "bf16"), (7, 5001, 70, "bf16"),
+                                         (2100, 2401, 5, "bf16"), (66, 40001, 20, "f32"),
+                                         (1100, 12001, 3, "f32")])
+def test_distill_in_a_graph(T, V, K, dtype):
+    """Onto the student, replayed over new students."""
+    s, ids, u, lse = distill_case(T + K, T, V, K, dtype, False, 1.0, True)
+    ids, u, lse = ids.cuda(), u.cuda(), lse.cuda()
+    loss, eager, l0, side = torch.empty(T, device="cuda"), s.clone(), torch.empty(T, device="cuda"), torch.cuda.Stream()
+    ws = torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")
+    run = lambda st, lo, stream=None: M.moe_distill_topk(T, V, K, st, ids, u, lo, st, ws, teacher_lse=lse,
+                                                         scale=0.5, stream=stream)
+    run(s.clone(), l0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(s, loss)
+    for i in range(4):
+        new = randn(gen(i), T, V, dtype=dtype)
+        s.copy_(new)
+        eager.copy_(new)
+        torch.cuda.synchronize()
+        run(eager, l0, side)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s, eager) and torch.equal(loss, l0) and torch.isfinite(s).all(), i
 
 
 def test_distill_segments_in_a_graph():

@@ -20,12 +20,19 @@ namespace moe {
 
 constexpr int DISPATCH_THREADS = 256;
 
+// 16 bytes that are read once (load_once below): they do not stay in the caches.
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  typedef uint32_t v4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const v4*>(p)));
+}
+
 // N elements as loaded: 16 bytes of the layer's type (8 bf16, 4 fp32), and as
 // many elements of fp32 rows beside a bf16 layer (32 bytes).
 template <typename T, int N> struct unit;
 template <> struct unit<bf16, 8> {
   uint4 a;
   __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_once(const bf16* p) { a = load_stream(p); }
   __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = a; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
@@ -41,6 +48,10 @@ template <int N> struct unit<float, N> {
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) a[i] = reinterpret_cast<const float4*>(p)[i];
+  }
+  __device__ __forceinline__ void load_once(const float* p) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) a[i] = __builtin_bit_cast(float4, load_stream(p + 4 * i));
   }
   __device__ __forceinline__ void store(float* p) const {
 #pragma unroll
@@ -83,9 +94,10 @@ dispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P, const T* _
 // One thread per (token, unit): the loads of all slots' rows go out together,
 // then the sum runs in slot order in fp32 and is rounded once.  add may be
 // out itself (a thread reads its unit before it writes it).
-// 6007 x 2048 bf16 top-6, a tenth of the pairs missing (182 MB): 36.7 us, 5.0
+// ONCE: the rows are read past the caches.
+// 6007 x 2048 bf16 top-6, a tenth of the pairs missing (182 MB): 32.2 us, 5.7
 // TB/s; 256 x 3584 top-8 on fp32 rows (33 MB): 7.0 us.
-template <typename T, typename Ty>
+template <typename T, typename Ty, bool ONCE>
 __global__ void __launch_bounds__(DISPATCH_THREADS)
 undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
                   const Ty* __restrict__ y_perm, const int32_t* __restrict__ inv,
@@ -112,7 +124,11 @@ undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
     live[j] = row < P;
     w[j] = 1.f;
     if (live[j]) {
-      v[j].load(y_perm + (int64_t)row * H + u * N);
+      const Ty* p = y_perm + (int64_t)row * H + u * N;
+      if (ONCE)
+        v[j].load_once(p);
+      else
+        v[j].load(p);
       if (topk_w) w[j] = topk_w[o];
     }
   }
@@ -235,14 +251,24 @@ hipError_t launch_dispatch(const moe_dims_t& d, int T, const void* x, const int3
   return hipGetLastError();
 }
 
+// Bytes of sorted rows from which reading them past the caches gains, also right
+// after the kernel that wrote them, whose last rows the caches still hold (with
+// that kernel, bf16 rows: 67 MB 33.0 us without, 34.8 with; 101 MB 51.5, 49.9; 147 MB
+// 79, 72; fp32 rows beside a bf16 layer, two loads a unit: 101 MB 50.0, 53.7; 134
+// MB 75, 69).  Stores are not treated so: their reader loses more than they gain.
+template <typename T, typename Ty> constexpr size_t once_bytes() {
+  return (size_t)(sizeof(T) == sizeof(Ty) ? 80 : 128) << 20;
+}
 template <typename T, typename Ty>
 static void undispatch_t(const moe_dims_t& d, int T_, const void* y, const int32_t* inv,
                          const float* w, const void* add, void* out, hipStream_t s) {
   const uint32_t units = d.hidden / unit_elems<T>(), n = (uint32_t)T_ * units;
-  undispatch_kernel<T, Ty>
-      <<<(n + DISPATCH_THREADS - 1) / DISPATCH_THREADS, DISPATCH_THREADS, 0, s>>>(
-          n, units, d.hidden, d.top_k, (uint32_t)T_ * d.top_k, (const Ty*)y, inv, w, (const T*)add,
-          (T*)out);
+  const size_t bytes = (size_t)T_ * d.top_k * d.hidden * sizeof(Ty);
+  const auto kernel = bytes >= once_bytes<T, Ty>() ? undispatch_kernel<T, Ty, true>
+                                                   : undispatch_kernel<T, Ty, false>;
+  kernel<<<(n + DISPATCH_THREADS - 1) / DISPATCH_THREADS, DISPATCH_THREADS, 0, s>>>(
+      n, units, d.hidden, d.top_k, (uint32_t)T_ * d.top_k, (const Ty*)y, inv, w, (const T*)add,
+      (T*)out);
 }
 
 hipError_t launch_undispatch(const moe_dims_t& d, int T, const void* y_perm, bool rows_bf16,

@@ -117,6 +117,23 @@ def test_undispatch(T, H, k, dtype, rows, miss, weighted, added):
         assert torch.equal(add, out)
 
 
+@pytest.mark.parametrize("T,H,k,dtype,rows", [(6001, 1024, 8, "bf16", "bf16"), (4501, 1024, 8, "bf16", "f32"),
+                                              (4501, 640, 8, "f32", "f32")])
+def test_undispatch_many_rows(T, H, k, dtype, rows):
+    """More bytes than the rows that stay in the caches; in 64 bits on the GPU."""
+    g = gen(T + H)
+    inv, y, w = random_inv(g, T, k, 0.2), randn(g, T * k, H, dtype=rows), torch.rand(T, k, generator=g).cuda()
+    add, out = randn(g, T, H, dtype=dtype), torch.full((T, H), 3.0, dtype=TT[dtype], device="cuda")
+    M.moe_undispatch(make_dims(H, 16, k, dtype), T, y, inv, w, out, add=add)
+    at, want, size = inv.view(T, k).long(), add.double(), add.double().abs()
+    for j in range(k):
+        p = torch.where(at[:, j:j + 1] >= 0, w[:, j:j + 1].double() * y[at[:, j].clamp(min=0)].double(), 0.0)
+        want += p
+        size += p.abs()
+    tol = (k + 1) * U * size + HALF[dtype] * 1.01 * want.abs()
+    assert bool(((out.double() - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("want_dy,want_dw", [(True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("T,H,k,dtype,rows,miss", ROWS)
 def test_undispatch_backward(T, H, k, dtype, rows, miss, want_dy, want_dw):

@@ -149,9 +149,10 @@ undispatch_kernel(uint32_t n, uint32_t units, int H, int k, uint32_t P,
 // row's units; 256: a block).  Each lane walks its units, U of them with up to
 // KM slots' rows in flight, then the lanes' partial dots meet in a fixed tree
 // (and a block's four waves in wave order).
-// 4096 x 1536 bf16 top-8, both gradients (214 MB): 45.4 us, 4.7 TB/s, as much
+// ONCE: y_perm is read past the caches.
+// 4096 x 1536 bf16 top-8, both gradients (214 MB): 45.0 us, 4.8 TB/s, as much
 // read as written; 333 x 256 fp32 top-2: 3.4 us, a launch.
-template <typename T, typename Ty, int G, int KM, bool DY, bool DW>
+template <typename T, typename Ty, int G, int KM, bool DY, bool DW, bool ONCE>
 __global__ void __launch_bounds__(DISPATCH_THREADS)
 undispatch_bwd_kernel(int T_, int units, int H, int k, uint32_t P, const T* __restrict__ dout,
                       const Ty* __restrict__ y_perm, const int32_t* __restrict__ inv,
@@ -181,7 +182,13 @@ undispatch_bwd_kernel(int T_, int units, int H, int k, uint32_t P, const T* __re
       if (DW) {
 #pragma unroll
         for (int j = 0; j < KM; ++j)
-          if (row[j] < P) y[q][j].load(y_perm + (int64_t)row[j] * H + u * N);
+          if (row[j] < P) {
+            const Ty* p = y_perm + (int64_t)row[j] * H + u * N;
+            if (ONCE)
+              y[q][j].load_once(p);
+            else
+              y[q][j].load(p);
+          }
       }
     }
 #pragma unroll
@@ -294,10 +301,20 @@ struct UndispatchBwd {
   hipStream_t s;
 };
 
+// Reading y_perm past the caches gains from less on here, since dy_perm is as much
+// again (with the kernel that wrote the rows, bf16: 34 MB 25.2 us without, 25.9 with;
+// 49 MB 37.3, 35.8; 67 MB 52.4, 50.7; 246 MB 189, 170).  fp32 rows beside a bf16 layer
+// lose at every size (201 MB 149, 160); rows below a wave of units keep the plain
+// loads.
+constexpr size_t BWD_ONCE_BYTES = (size_t)40 << 20;
 template <typename T, typename Ty, int G, int KM, bool DY, bool DW>
 static void bwd_launch(const UndispatchBwd& a) {
   constexpr int per = DISPATCH_THREADS / G;
-  undispatch_bwd_kernel<T, Ty, G, KM, DY, DW><<<(a.T + per - 1) / per, DISPATCH_THREADS, 0, a.s>>>(
+  constexpr bool MAY = DW && G >= MOE_WAVE && sizeof(T) == sizeof(Ty);
+  const bool once = MAY && (size_t)a.T * a.d.top_k * a.d.hidden * sizeof(Ty) >= BWD_ONCE_BYTES;
+  const auto kernel = once ? undispatch_bwd_kernel<T, Ty, G, KM, DY, DW, MAY>
+                           : undispatch_bwd_kernel<T, Ty, G, KM, DY, DW, false>;
+  kernel<<<(a.T + per - 1) / per, DISPATCH_THREADS, 0, a.s>>>(
       a.T, a.d.hidden / unit_elems<T>(), a.d.hidden, a.d.top_k, (uint32_t)a.T * a.d.top_k,
       (const T*)a.dout, (const Ty*)a.y_perm, a.inv, a.w, (Ty*)a.dy, a.dw);
 }

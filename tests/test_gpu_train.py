@@ -132,6 +132,17 @@ def test_undispatch_many_rows(T, H, k, dtype, rows):
         size += p.abs()
     tol = (k + 1) * U * size + HALF[dtype] * 1.01 * want.abs()
     assert bool(((out.double() - want).abs() <= tol).all())
+    # and back
+    dy, dw = torch.zeros_like(y), torch.empty(T, k, device="cuda")
+    M.moe_undispatch_backward(make_dims(H, 16, k, dtype), T, out, y, inv, w, dy, dw)
+    for j in range(k):
+        on, row = at[:, j] >= 0, at[:, j].clamp(min=0)
+        p = out.double() * y[row].double()
+        want, tol = p.sum(1), (H + 1) * U * p.abs().sum(1)
+        assert bool(torch.where(on, (dw[:, j].double() - want).abs() <= tol, dw[:, j] == 0).all())
+        want = w[:, j:j + 1].double() * out.double()
+        ok = (dy[row].double() - want).abs() <= HALF[rows] * 1.01 * want.abs()
+        assert bool((ok | ~on[:, None]).all())
 
 
 @pytest.mark.parametrize("want_dy,want_dw", [(True, True), (True, False), (False, True)])

@@ -20,17 +20,15 @@
 // left out is 2^-24 of dl), two for dx (2^-16, against an output step of
 // 2^-8).  The parts are written by the first launch as whole operand
 // fragments.  Both operands want eight consecutive k (tokens for dW, experts
-// for dx) in a lane, while x and W are contiguous along H: a lane loads four
-// columns of eight rows (8 bytes each; 16 lanes cover a 128-byte line) and
-// interleaves them in registers into the fragments of four column tiles, tile
-// c holding columns 4n + c, so nothing passes through LDS on the way in.
+// for dx) in a lane, while x and W are contiguous along H: a lane loads eight
+// columns of eight rows (16 bytes each; 16 lanes cover two 128-byte lines) and
+// interleaves them in registers into the fragments of as many column tiles.
 // fp32 layers run v_mfma_f32_16x16x4_f32, whose operands are single values.
 //
 // bf16, 16384 x 3584, 64 experts (246 MB, 45.5 us at the rate of a large copy):
-// 73 us, of which 8 the logits' gradient, 62 the products, 5 the sum of the
-// ranges.  What bounds the products is the rate at which a CU takes lines from
-// its L2 (about 30 bytes a clock): dW reads x and its fragments, dx writes as
-// much again, and the two run side by side.
+// 75 us, of which 8 the logits' gradient, 61 the products, 5 the sum of the
+// ranges.  dW alone reads its 117 MB at about 4 TB/s, dx alone writes as much at
+// 4.5, and side by side they do not gain on one another.
 #include <algorithm>
 #include <type_traits>
 
@@ -48,28 +46,29 @@ constexpr int RBWD_STEP = 32;   // tokens of one dW step (the K of one bf16 MFMA
 // Column tiles of 16 a wave owns (H % 64 == 0: the last wave of a bf16 row may
 // own 64 columns past the end, which it neither keeps nor stores).
 template <typename T> constexpr int rbwd_nc() { return sizeof(T) == 2 ? 8 : 4; }
+constexpr int DW_GROUP = PROD_WAVES;  // steps a bf16 dW block takes at once: each wave loads one
 constexpr int RBWD_DW_PARTS = 3, RBWD_DX_PARTS = 2;
 
 // Shapes of one call.  mt: 16-expert tiles, ks: 32-expert k steps of dx.
 struct RouteBwdPlan {
   int mt, ks, steps, ncg;
-  int splits;              // token ranges of dW
+  int per, splits;         // steps of a token range of dW, ranges
   int dx_tiles;            // 16-token tiles of one dx wave
   bool apart;              // dW and dx in launches of their own
   size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments (fp32 layers: padded
                                // dlogits at fx), dW partials
 };
 
-// A dx wave takes as many token tiles as keep all waves to one round of two a
-// SIMD: a few waves more cost a second round (16384 x 3584: 35 us against 30).
-constexpr int RBWD_DX_WAVES = 2048;
-// One dW block a CU: more ranges cost more partials than they gain (the same
-// shape: 38 us with 9 ranges, 43 with 18).
+// A dx wave takes as many token tiles as leave all waves a place beside dW's at
+// once, one a SIMD (bf16, 4096 x 1536, 40 experts: 20.3 us for the call, 21.4 with
+// twice the waves; 16384 x 3584: 74.7, 75.2; fp32 dx alone, 1024 x 2048: 9.7, 11.3).
+constexpr int RBWD_DX_WAVES = 1024;
+// One dW block a CU: more ranges cost more partials than they gain (bf16 dW of
+// 16384 x 3584: 45 us with 9 ranges, 48 with 18).
 constexpr int RBWD_DW_BLOCKS = 256;
 // fp32 products are bound by the matrix units.  From this many on dW and dx have a
 // launch each (8192 x 3584, 64 experts: 96 us for the call, 119 in one launch; 2048
-// x 2048, 64 experts: 25.6, 26.8, 40 experts: 23.1, 22.4) and dx one wave a SIMD: two
-// take longer than one with the work of both (8192 x 3584: 50 us against 58).
+// x 2048, 64 experts: 25.6, 26.8, 40 experts: 23.1, 22.4).
 constexpr int64_t RBWD_APART = 1 << 28;
 
 static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
@@ -79,17 +78,19 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   p.steps = (T + RBWD_STEP - 1) / RBWD_STEP;
   const int cols = d.dtype == MOE_BF16 ? 16 * rbwd_nc<bf16>() : 16 * rbwd_nc<float>();
   p.ncg = (d.hidden + cols - 1) / cols;
-  // each range gives every set of its block's waves four steps at least, fp32
-  // layers (twice the matrix time a step) two: fewer cost more in partials than
-  // the blocks gain (4096 x 1536, 40 experts: 18.2 us with four, 20.8 with two,
-  // 21.0 with one; fp32 1024 x 2048, 64 experts: 20.8, 19.5 and 19.6)
-  const int ways = p.mt > 1 ? PROD_WAVES / 2 : PROD_WAVES;
-  const int least = ways * (d.dtype == MOE_BF16 ? 4 : 2);
-  const int most = std::max(1, (p.steps + least - 1) / least);
-  p.splits = std::min(most, std::max(1, RBWD_DW_BLOCKS / p.ncg));
+  // Ranges of whole groups of steps (fp32: two steps for each set of its block's
+  // waves at least), and one range where there are two groups: it spares the launch
+  // that adds the ranges (256 x 2048, 64 experts: 9.4 us, 10.2 with two; 902 x 64, 27
+  // experts: 9.0 with ranges of one group, 10.4 with two).
+  const int most = std::max(1, RBWD_DW_BLOCKS / p.ncg);
+  const int unit = d.dtype == MOE_BF16 ? DW_GROUP : p.mt > 1 ? PROD_WAVES : 2 * PROD_WAVES;
+  const int even = (p.steps + most - 1) / most;
+  const bool one = d.dtype == MOE_BF16 && p.steps <= 2 * DW_GROUP;
+  p.per = one ? p.steps : (even + unit - 1) / unit * unit;
+  p.splits = (p.steps + p.per - 1) / p.per;
   const int tiles = 2 * p.steps;
   p.apart = d.dtype == MOE_F32 && (int64_t)T * d.hidden * (16 * p.mt) >= RBWD_APART;
-  const int ranges = std::max(1, (p.apart ? RBWD_DX_WAVES / 2 : RBWD_DX_WAVES) / p.ncg);
+  const int ranges = std::max(1, RBWD_DX_WAVES / p.ncg);
   p.dx_tiles = (tiles + ranges - 1) / ranges;
   size_t o = 0;
   auto take = [&](size_t n) {
@@ -309,110 +310,19 @@ __device__ __forceinline__ uint32_t rows8_off(int H, int col) {
 }
 
 struct RouteBwdArgs {
-  int T, H, E, ncg, steps, splits, dx_tiles, dw_blocks;
+  int T, H, E, ncg, steps, per, splits, dx_tiles, dw_blocks;
   const float* pad;  // fp32 layers: dlogits [32 steps][16 MT]
   const uint4 *fx, *fw;
   float *part, *dw;
   int accumulate;
 };
 
-// How the four waves of a dW block share a range of tokens: MH halves of the
-// expert tiles (MW each) by WAYS interleaved sets of steps.  Halving the tiles
-// holds a wave to 256 registers (one wave's 64 experts by 128 columns are 128
-// accumulators alone), so a dx block runs beside it on the CU; the two waves
-// of a pair read the same rows of x, the second time from near caches.
+// How the four waves of an fp32 dW block share a range of tokens: MH halves of the
+// expert tiles (MW each) by WAYS interleaved sets of steps.
 template <int MT> struct DwShape {
   static constexpr int MH = MT > 1 ? 2 : 1, MW = (MT + MH - 1) / MH, WAYS = PROD_WAVES / MH;
 };
 
-// acc[m][c] += the tokens of steps r0 + way, then every WAYS-th, below s1 (r0
-// and s1 the same for the block): experts of tile m0 + m by the lanes' column
-// c.  Fragments are asked for one step ahead, rows two, in this order, since
-// loads retire in order: waiting for a step's fragments leaves the rows after
-// them in flight.  A last step that is not whole runs by itself, so that the
-// loop has one way to load its rows.
-template <int MT>
-struct DwFrags {
-  uint4 f[DwShape<MT>::MW][RBWD_DW_PARTS];
-  __device__ __forceinline__ void load(const RouteBwdArgs& a, int m0, int s) {
-    const char* src = reinterpret_cast<const char*>(a.fw + ((int64_t)s * MT + m0) * RBWD_DW_PARTS * 64);
-    const uint32_t off = lane_id() * 16u;
-#pragma unroll
-    for (int m = 0; m < DwShape<MT>::MW; ++m)
-      if (m0 + m < MT) {
-#pragma unroll
-        for (int p = 0; p < RBWD_DW_PARTS; ++p)
-          f[m][p] = *reinterpret_cast<const uint4*>(src + (m * RBWD_DW_PARTS + p) * 1024 + off);
-      }
-  }
-};
-template <int MT>
-__device__ __forceinline__ void dw_mfma(int m0, const DwFrags<MT>& f, const bf16x8_t (&b)[8],
-                                        f32x4_t (&acc)[DwShape<MT>::MW][8]) {
-#pragma unroll
-  for (int m = 0; m < DwShape<MT>::MW; ++m)
-    if (m0 + m < MT) {
-#pragma unroll
-      for (int p = RBWD_DW_PARTS - 1; p >= 0; --p)  // smallest part first
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8_t, f.f[m][p]), b[c], acc[m][c], 0, 0, 0);
-    }
-}
-template <int MT>
-__device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const bf16* __restrict__ x, int col,
-                                         int m0, int r0, int way, int s1,
-                                         f32x4_t (&acc)[DwShape<MT>::MW][8]) {
-  constexpr int WAYS = DwShape<MT>::WAYS;
-  const uint32_t off = rows8_off(a.H, col);
-  const int whole = a.T / RBWD_STEP;  // steps with all their rows
-  const int e = min(s1, whole), s0 = r0 + way;
-  uint4 v0[8], v1[8];
-  DwFrags<MT> f0, f1;
-  // loads past the end ask for the last step again, unused
-  auto rows = [&](int s, uint4 (&v)[8]) {
-    load_rows8(x, (int64_t)min(s, e - 1) * RBWD_STEP, a.H, off, v);
-  };
-  auto step = [&](int s, uint4 (&v)[8], const DwFrags<MT>& now, DwFrags<MT>& next) {
-    next.load(a, m0, min(s + WAYS, e - 1));
-    // the scheduler would move the loads down to their uses
-    __builtin_amdgcn_sched_barrier(0);
-    bf16x8_t b[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) b[c] = column_frag(v, c);
-    rows(s + 2 * WAYS, v);
-    __builtin_amdgcn_sched_barrier(0);
-    dw_mfma<MT>(m0, now, b, acc);
-  };
-  // The block's waves go through their steps together, so the second wave of a
-  // pair finds the rows of the first in L1 (dW of 16384 x 3584: 38 us without
-  // the barriers, 34 with them).  Every wave passes every barrier, whether or
-  // not it has a step.
-  const int trips = (e - r0 + WAYS - 1) / WAYS;
-  if (trips > 0) {
-    rows(s0, v0);
-    f0.load(a, m0, min(s0, e - 1));
-    rows(s0 + WAYS, v1);
-    for (int i = 0; i < trips; i += 2) {
-      const int s = s0 + i * WAYS;
-      __builtin_amdgcn_s_barrier();
-      if (s < e) step(s, v0, f0, f1);
-      if (i + 1 < trips) {
-        __builtin_amdgcn_s_barrier();
-        if (s + WAYS < e) step(s + WAYS, v1, f1, f0);
-      }
-    }
-  }
-  if (whole < s1 && whole >= s0 && (whole - s0) % WAYS == 0) {
-    f0.load(a, m0, whole);
-    load_rows8_below(x, (int64_t)whole * RBWD_STEP, a.T, a.H, off, v0);
-    bf16x8_t b[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) b[c] = column_frag(v0, c);
-    dw_mfma<MT>(m0, f0, b, acc);
-  }
-}
 template <int MT>
 __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __restrict__ x, int col,
                                          int m0, int r0, int way, int s1,
@@ -480,25 +390,135 @@ __device__ __forceinline__ void dw_steps(const RouteBwdArgs& a, const float* __r
   }
 }
 
+constexpr int DW_STEP_FLOATS = 8 * 64 * 4;  // of LDS: the fragments of a step's x
 template <typename T, int MT>
 constexpr int dw_lds_floats() {
   using S = DwShape<MT>;
+  if (sizeof(T) == 2) return DW_GROUP * DW_STEP_FLOATS;
   return (S::WAYS - 1) * S::MH * 16 * S::MW * 16 * rbwd_nc<T>();
 }
 
-// dW of a wave's columns over one range of tokens.  The waves of way 1 and up
-// leave their tiles in LDS, those of way 0 add them in way order and store.
-template <typename T, int MT>
+// dW of 128 columns over one range of tokens, bf16: the block's waves load a step
+// of x each, interleave it into fragments and leave them in LDS for all four, which
+// own an expert tile each (of fewer than three tiles a part of the columns), so no
+// row is read or interleaved twice and a wave holds 32 accumulators.  Rows are asked
+// for two groups of steps ahead, a step's fragments of dlogits as soon as the group
+// before is through with theirs.  The last step, if it is not whole, runs by itself, so
+// that the loop has one way to load its rows.  1024 x 2048, 64 experts: 12.7 us for the
+// call, 14.3 with the waves of a pair each loading and interleaving what both need;
+// 16384 x 3584: 74.7, 74.0.  A second buffer, which spares one of the two barriers a
+// group, gains nothing (12.7, 75) and halves the blocks that a CU has LDS for.
+template <int MT>
 __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
-                                         const T* __restrict__ x, float* lds) {
+                                         const bf16* __restrict__ x, float* lds) {
+  constexpr int TILES = MT == 3 ? 4 : MT, NC = 8 * TILES / PROD_WAVES;
+  const int split = item / a.ncg, cg = item - split * a.ncg;
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = wv % TILES, c0 = wv / TILES * NC;
+  const int s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
+  const int whole = a.T / RBWD_STEP, e = min(s1, whole);  // steps with all their rows
+  const int groups = (e - s0 + DW_GROUP - 1) / DW_GROUP;
+  uint4* frags = reinterpret_cast<uint4*>(lds);
+  // lanes past H read the row's last columns; their results are dropped below
+  const uint32_t off = rows8_off(a.H, min(cg * 128 + 8 * n, a.H - 8));
+  // loads past the end ask for the last step again, unused
+  auto rows = [&](int gi, uint4 (&v)[8]) {
+    load_rows8(x, (int64_t)min(s0 + gi * DW_GROUP + wv, e - 1) * RBWD_STEP, a.H, off, v);
+  };
+  uint4 d[DW_GROUP][RBWD_DW_PARTS];
+  auto parts = [&](int s, int q) {
+    const uint4* at = a.fw + ((int64_t)s * MT + min(m, MT - 1)) * RBWD_DW_PARTS * 64;
+    const char* src = reinterpret_cast<const char*>(at);
+#pragma unroll
+    for (int p = 0; p < RBWD_DW_PARTS; ++p)
+      d[q][p] = *reinterpret_cast<const uint4*>(src + p * 1024 + lane * 16u);
+  };
+  f32x4_t acc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto put = [&](uint4* buf, const uint4 (&v)[8]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) buf[c * 64 + lane] = __builtin_bit_cast(uint4, column_frag(v, c));
+  };
+  auto mfma = [&](const uint4* buf, int q) {
+    bf16x8_t b[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) b[c] = __builtin_bit_cast(bf16x8_t, buf[(c0 + c) * 64 + lane]);
+#pragma unroll
+    for (int p = RBWD_DW_PARTS - 1; p >= 0; --p)  // smallest part first
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, d[q][p]), b[c],
+                                                         acc[c], 0, 0, 0);
+  };
+  uint4 v0[8], v1[8];
+  auto group = [&](int gi, uint4 (&v)[8]) {
+    const int s = s0 + gi * DW_GROUP;
+    if (gi > 0) __syncthreads();  // all are through with the group before
+    if (s + wv < e) put(frags + wv * 512, v);
+    rows(gi + 2, v);
+    // the scheduler would move the loads down to their uses
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < DW_GROUP; ++q) {
+      if (s + q < e && m < MT) mfma(frags + q * 512, q);
+      parts(min(s + DW_GROUP + q, e - 1), q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (groups > 0) {
+    rows(0, v0);
+#pragma unroll
+    for (int q = 0; q < DW_GROUP; ++q) parts(min(s0 + q, e - 1), q);
+    rows(1, v1);
+    for (int gi = 0; gi < groups; gi += 2) {
+      group(gi, v0);
+      if (gi + 1 < groups) group(gi + 1, v1);
+    }
+  }
+  if (s0 <= whole && whole < s1) {  // the last step, not whole
+    __syncthreads();
+    parts(whole, 0);
+    if (wv == 0) {
+      load_rows8_below(x, (int64_t)whole * RBWD_STEP, a.T, a.H, off, v0);
+      put(frags, v0);
+    }
+    __syncthreads();
+    if (m < MT) mfma(frags, 0);
+  }
+  if (m >= MT) return;
+  const bool direct = a.splits == 1;
+  float* out = direct ? a.dw : a.part + (int64_t)split * a.E * a.H;
+  typedef float vec_t __attribute__((ext_vector_type(NC < 4 ? NC : 4)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 16 * m + 4 * g + i, h = cg * 128 + 8 * n + c0;
+    if (e >= a.E || h >= a.H) continue;
+#pragma unroll
+    for (int c = 0; c < NC; c += 4) {
+      vec_t* dst = reinterpret_cast<vec_t*>(out + (int64_t)e * a.H + h + c);
+      vec_t v;
+#pragma unroll
+      for (int r = 0; r < (NC < 4 ? NC : 4); ++r) v[r] = acc[c + r][i];
+      if (direct && a.accumulate) v = *dst + v;
+      *dst = v;
+    }
+  }
+}
+// dW of a wave's columns over one range of tokens, fp32.  The waves of way 1 and up
+// leave their tiles in LDS, those of way 0 add them in way order and store.
+template <int MT>
+__device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
+                                         const float* __restrict__ x, float* lds) {
   using S = DwShape<MT>;
-  constexpr int NC = rbwd_nc<T>(), COLS = 16 * NC, MW = S::MW, TILE = 16 * MW * COLS;
+  constexpr int NC = rbwd_nc<float>(), COLS = 16 * NC, MW = S::MW, TILE = 16 * MW * COLS;
   const int split = item / a.ncg, cg = item - split * a.ncg;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = wv % S::MH, way = wv / S::MH, m0 = half * MW;
-  const int per = (a.steps + a.splits - 1) / a.splits;
-  const int s0 = split * per, s1 = min(a.steps, s0 + per);
+  const int s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
   f32x4_t acc[MW][NC];
 #pragma unroll
   for (int m = 0; m < MW; ++m)
@@ -711,7 +731,7 @@ route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
   const int nw = (a.dw_blocks + 7) & ~7, b0 = blockIdx.x;
   if (b0 < nw) {
     const int item = xcd_item(b0, a.dw_blocks);
-    if (item < a.dw_blocks) route_dw<T, MT>(a, item, x, lds);
+    if (item < a.dw_blocks) route_dw<MT>(a, item, x, lds);
   } else {
     // fp32: dx first, so that dW's long waves have a SIMD to themselves early (2048
     // x 2048, 40 experts: 22.1 us for the call, 25.3 at one priority; a bf16 call
@@ -735,7 +755,7 @@ route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restric
                  const T* __restrict__ w, const T* dx_add, T* dx) {
   constexpr int KS = (MT + 1) / 2;
   constexpr int TILES = STEPS * (int)sizeof(rbwd_tile_t) / 4;
-  constexpr int SUMS = dw_lds_floats<T, MT>();
+  constexpr int SUMS = sizeof(T) == 2 ? STEPS * DW_STEP_FLOATS : dw_lds_floats<T, MT>();
   constexpr int FX = 2 * KS * RBWD_DX_PARTS * 64, FW = MT * RBWD_DW_PARTS * 64;  // a step's
   constexpr int PACK = sizeof(T) == 2 ? (FX > FW ? FX : FW) : RBWD_STEP * 16 * MT / 4;
   __shared__ __align__(16) float lds[TILES > SUMS ? TILES : SUMS];  // the tiles, then dW's sums
@@ -763,7 +783,7 @@ route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restric
   a.fx = a.fw = packed;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (for_dw) {
-    if (wv < PROD_WAVES) route_dw<T, MT>(a, blockIdx.x, x, lds);  // its barriers wait for these
+    if (wv < PROD_WAVES) route_dw<MT>(a, blockIdx.x, x, lds);  // its barriers wait for these
   } else {
     const int item = (blockIdx.x - a.dw_blocks) * (RBWD_THREADS / MOE_WAVE) + wv;
     if (item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);
@@ -857,7 +877,7 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!dx && !dw)) return e;
   }
-  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.splits, p.dx_tiles,
+  const RouteBwdArgs a{T, d.hidden, d.n_experts, p.ncg, p.steps, p.per, p.splits, p.dx_tiles,
                        dw ? p.splits * p.ncg : 0, pad, fx, fw,
                        p.splits > 1 ? reinterpret_cast<float*>(base + p.part) : nullptr, dw, accumulate};
   const int dx_items = dx ? (2 * p.steps + p.dx_tiles - 1) / p.dx_tiles * p.ncg : 0;

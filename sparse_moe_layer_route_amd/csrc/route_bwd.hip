@@ -721,8 +721,8 @@ __device__ __forceinline__ int xcd_item(int b, int n) {
 }
 
 // Blocks 0 .. dw_blocks-1 (rounded up to eights) form dW, the others dx: one
-// launch, and a CU may hold a block of each (8192 x 2048, 64 experts: 29.0 us for
-// the whole call, 30.6 with a launch each).
+// launch, and a CU may hold a block of each (bf16, 4096 x 1536, 40 experts: 17.8 us
+// for the whole call, 22.3 with a launch each).
 template <typename T, int MT>
 __global__ void __launch_bounds__(PROD_THREADS, 2)
 route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,

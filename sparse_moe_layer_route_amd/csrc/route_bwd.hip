@@ -790,20 +790,49 @@ route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restric
   }
 }
 
-// dW = (dW +) the sum of the ranges' partials, in range order; splits = 0 clears
-// dW.
+// dW = (dW +) the sum of the ranges' partials; splits = 0 clears dW.  R threads an
+// element add a run of ranges each, in order, and the first adds the runs, in order.
+template <int R>
 __global__ void __launch_bounds__(PROD_THREADS)
 route_dw_sum_kernel(int n4, int splits, const float4* __restrict__ part, int accumulate,
                     float4* __restrict__ dw) {
-  const int i = blockIdx.x * PROD_THREADS + threadIdx.x;
-  if (i >= n4) return;
-  float4 s = accumulate ? dw[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int N = PROD_THREADS / R;
+  __shared__ float4 runs[R][N];
+  const int l = threadIdx.x % N, r = threadIdx.x / N, i = blockIdx.x * N + l;
+  const int per = (splits + R - 1) / R, p1 = min(splits, (r + 1) * per);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < n4) {
+    if (r == 0 && accumulate) s = dw[i];
 #pragma unroll 8
-  for (int p = 0; p < splits; ++p) {
-    const float4 v = part[(int64_t)p * n4 + i];
-    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    for (int p = r * per; p < p1; ++p) {
+      const float4 v = part[(int64_t)p * n4 + i];
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
   }
-  dw[i] = s;
+  if (R > 1) {
+    runs[r][l] = s;
+    __syncthreads();
+    if (r > 0) return;
+#pragma unroll
+    for (int q = 1; q < R; ++q) {
+      const float4 v = runs[q][l];
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
+  }
+  if (i < n4) dw[i] = s;
+}
+// Eight threads an element from SUM_RUNS ranges on (bf16, 16384 x 64, 64 experts, 128
+// ranges: 17.1 us for the call, 21.8 with one; 1515 x 64, 62 experts, 12 ranges: 11.8,
+// 12.7; 4096 x 1536, 40 experts, 16 ranges: 18.6 both).
+constexpr int SUM_RUNS = 8;
+static hipError_t launch_dw_sum(int n4, int splits, const float* part, int accumulate, float* dw,
+                                hipStream_t s) {
+  const bool runs = splits >= SUM_RUNS;
+  const int per = runs ? PROD_THREADS / 8 : PROD_THREADS;
+  const auto kernel = runs ? route_dw_sum_kernel<8> : route_dw_sum_kernel<1>;
+  kernel<<<(n4 + per - 1) / per, PROD_THREADS, 0, s>>>(n4, splits, (const float4*)part, accumulate,
+                                                       (float4*)dw);
+  return hipGetLastError();
 }
 
 int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
@@ -833,10 +862,7 @@ static hipError_t launch_products(const RouteBwdPlan& p, const DlogitsArgs* few,
   hipError_t e = run(a, a.dw_blocks, apart ? 0 : dx_items);
   if (e == hipSuccess && apart) e = run(a, 0, dx_items);
   if (e != hipSuccess || !a.dw || a.splits == 1) return e;
-  const int n4 = (int)((int64_t)a.E * a.H / 4);
-  route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
-      n4, a.splits, (const float4*)a.part, a.accumulate, (float4*)a.dw);
-  return hipGetLastError();
+  return launch_dw_sum((int)((int64_t)a.E * a.H / 4), a.splits, a.part, a.accumulate, a.dw, s);
 }
 template <typename T>
 static hipError_t launch_products_t(const RouteBwdPlan& p, const DlogitsArgs* few,
@@ -856,13 +882,9 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
                                  const int32_t* ids, const float* logits, const float* dtopk_w,
                                  const float* dlogits_add, float* dlogits, const void* dx_add,
                                  void* dx, float* dw, int accumulate, void* ws, hipStream_t s) {
-  if (T == 0) {
-    const int n4 = (int)((int64_t)d.n_experts * d.hidden / 4);
-    if (dw)
-      route_dw_sum_kernel<<<(n4 + PROD_THREADS - 1) / PROD_THREADS, PROD_THREADS, 0, s>>>(
-          n4, 0, nullptr, accumulate, (float4*)dw);
-    return hipGetLastError();
-  }
+  if (T == 0)
+    return dw ? launch_dw_sum((int)((int64_t)d.n_experts * d.hidden / 4), 0, nullptr, accumulate, dw, s)
+              : hipSuccess;
   const RouteBwdPlan p = route_bwd_plan(d, T);
   const bool packs = d.dtype == MOE_BF16;
   char* base = static_cast<char*>(ws);

@@ -134,15 +134,14 @@ struct DlogitsArgs {
   const float* add;  // may be dlogits itself
   float* dlogits;
 };
-constexpr int RBWD_Q = MOE_MAX_EXPERTS / 16;
 typedef float rbwd_tile_t[RBWD_STEP][MOE_MAX_EXPERTS + 1];
 
-// dl of token t by 16 lanes: lane l holds experts l + 16 q and slot l's id and
-// gradient.  Tokens past T get the last one's.  No branch on a lane's expert or
+// dl of token t by 16 lanes: lane l holds experts l + 16 q (q < Q, E <= 16 Q) and
+// slot l's id and gradient.  Tokens past T get the last one's.  No branch on a lane's expert or
 // slot: selects only, so that all loads of a token go out together (64 x 64: 8.7
 // us with branches, 3.9 without, a launch and a chain of short steps).
-__device__ __forceinline__ void token_dlogits(const DlogitsArgs& a, int t, float (&dl)[RBWD_Q]) {
-  constexpr int Q = RBWD_Q;
+template <int Q>
+__device__ __forceinline__ void token_dlogits(const DlogitsArgs& a, int t, float (&dl)[Q]) {
   const int l = threadIdx.x & 15, E = a.E, k = a.k;
   const bool renorm = a.renorm;
   const int64_t tc = min(t, a.T - 1);
@@ -203,10 +202,11 @@ __device__ __forceinline__ void token_dlogits(const DlogitsArgs& a, int t, float
   }
 }
 // Token t's row of dlogits (store), of a tile of 32 tokens and of pad (or null).
-__device__ __forceinline__ void put_dlogits(const DlogitsArgs& a, int t, const float (&dl)[RBWD_Q],
+template <int Q>
+__device__ __forceinline__ void put_dlogits(const DlogitsArgs& a, int t, const float (&dl)[Q],
                                             bool store, rbwd_tile_t& tile, int mt, float* pad) {
 #pragma unroll
-  for (int q = 0; q < RBWD_Q; ++q) {
+  for (int q = 0; q < Q; ++q) {
     const int e = (threadIdx.x & 15) + 16 * q;
     const bool on = e < a.E && t < a.T;
     if (on && store) a.dlogits[(int64_t)t * a.E + e] = dl[q];
@@ -220,15 +220,15 @@ __device__ __forceinline__ void put_dlogits(const DlogitsArgs& a, int t, const f
 //   fw [expert tile][part][lane]: expert lane % 16, tokens 8 (lane / 16) .. +7.
 // The parts of a value are it rounded to bf16, what is left rounded, and so on
 // (a value that is not finite leaves NaN).
-template <int NT>
-__device__ __forceinline__ void pack_dlogits(const rbwd_tile_t& tile, int mt, int ks, uint4* fx,
+template <int KS>
+__device__ __forceinline__ void pack_dlogits(const rbwd_tile_t& tile, int mt, uint4* fx,
                                              uint4* fw) {
   // one thread per fragment slot, all of its parts
-  const int nx = fx ? 2 * ks * 64 : 0, nw = fw ? mt * 64 : 0;
-  for (int i = threadIdx.x; i < nx + nw; i += NT) {
+  const int nx = fx ? 2 * KS * 64 : 0, nw = fw ? mt * 64 : 0;
+  for (int i = threadIdx.x; i < nx + nw; i += RBWD_THREADS) {
     const bool to_x = i < nx;
     const int l16 = i & 15, g8 = 8 * ((i >> 4) & 3), f = (to_x ? i : i - nx) >> 6;
-    const int half = ks == 2 ? f >> 1 : f, st = ks == 2 ? f & 1 : 0;
+    const int half = f / KS, st = f % KS;
     const float* src = to_x ? &tile[16 * half + l16][32 * st + g8] : &tile[g8][16 * f + l16];
     const int step = to_x ? 1 : MOE_MAX_EXPERTS + 1;
     float v[8];
@@ -253,20 +253,21 @@ __device__ __forceinline__ void pack_dlogits(const rbwd_tile_t& tile, int mt, in
 // One block per 32 tokens.  pad (fp32 layers, else null): dlogits again as [32
 // steps][16 mt], zero past T and E.  fx / fw (bf16 layers, else null): the
 // fragments of all steps in turn.  16384 x 64: 7.9 us, of 8 MB read and 14 written.
+template <int KS>
 __global__ void __launch_bounds__(RBWD_THREADS)
-route_dlogits_kernel(DlogitsArgs a, int mt, int ks, float* __restrict__ pad,
+route_dlogits_kernel(DlogitsArgs a, int mt, float* __restrict__ pad,
                      uint4* __restrict__ fx, uint4* __restrict__ fw) {
   static_assert(RBWD_THREADS == 16 * RBWD_STEP, "16 lanes a token");
   __shared__ rbwd_tile_t tile;
   const int t = blockIdx.x * RBWD_STEP + (threadIdx.x >> 4);
-  float dl[RBWD_Q];
+  float dl[2 * KS];  // the fragments of dx take whole k steps of 32 experts
   token_dlogits(a, t, dl);
   put_dlogits(a, t, dl, true, tile, mt, pad);
   if (!fx && !fw) return;
   __syncthreads();
-  pack_dlogits<RBWD_THREADS>(
-      tile, mt, ks, fx ? fx + (int64_t)blockIdx.x * 2 * ks * RBWD_DX_PARTS * 64 : nullptr,
-      fw ? fw + (int64_t)blockIdx.x * mt * RBWD_DW_PARTS * 64 : nullptr);
+  pack_dlogits<KS>(tile, mt,
+                   fx ? fx + (int64_t)blockIdx.x * 2 * KS * RBWD_DX_PARTS * 64 : nullptr,
+                   fw ? fw + (int64_t)blockIdx.x * mt * RBWD_DW_PARTS * 64 : nullptr);
 }
 
 // Eight columns of eight rows -> fragment c: column c, the eight rows in k
@@ -765,7 +766,7 @@ route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restric
   const bool for_dw = (int)blockIdx.x < a.dw_blocks;
   // the loads of all steps go out together
   const int t = threadIdx.x >> 4;
-  float dl[STEPS][RBWD_Q];
+  float dl[STEPS][2 * KS];
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) token_dlogits(g, t + s * RBWD_STEP, dl[s]);
 #pragma unroll
@@ -775,8 +776,8 @@ route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restric
   if (sizeof(T) == 2) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
-      pack_dlogits<RBWD_THREADS>(tile[s], MT, KS, for_dw ? nullptr : packed + s * FX,
-                                 for_dw ? packed + s * FW : nullptr);
+      pack_dlogits<KS>(tile[s], MT, for_dw ? nullptr : packed + s * FX,
+                       for_dw ? packed + s * FW : nullptr);
     __syncthreads();
   }
   a.pad = pad;
@@ -895,7 +896,10 @@ hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, cons
                       dlogits};
   const bool few = (dx || dw) && p.steps <= 2 && p.splits == 1 && dlogits_add != dlogits;
   if (!few) {
-    route_dlogits_kernel<<<p.steps, RBWD_THREADS, 0, s>>>(g, p.mt, p.ks, pad, fx, fw);
+    // up to 32 experts two a lane (16384 x 64, 8 experts: 12.6 us for the call, 13.8
+    // with four)
+    const auto kernel = p.ks == 1 ? route_dlogits_kernel<1> : route_dlogits_kernel<2>;
+    kernel<<<p.steps, RBWD_THREADS, 0, s>>>(g, p.mt, pad, fx, fw);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!dx && !dw)) return e;
   }

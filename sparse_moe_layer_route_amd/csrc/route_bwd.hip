@@ -59,10 +59,8 @@ struct RouteBwdPlan {
                                // dlogits at fx), dW partials
 };
 
-// A dx wave takes as many token tiles as leave all waves a place beside dW's at
-// once, one a SIMD (bf16, 4096 x 1536, 40 experts: 20.3 us for the call, 21.4 with
-// twice the waves; 16384 x 3584: 74.7, 75.2; fp32 dx alone, 1024 x 2048: 9.7, 11.3).
-constexpr int RBWD_DX_WAVES = 1024;
+// Blocks of the products that an XCD holds at once: two a CU.
+constexpr int RBWD_XCD_BLOCKS = 64;
 // One dW block a CU: more ranges cost more partials than they gain (bf16 dW of
 // 16384 x 3584: 45 us with 9 ranges, 48 with 18).
 constexpr int RBWD_DW_BLOCKS = 256;
@@ -90,7 +88,14 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   p.splits = (p.steps + p.per - 1) / p.per;
   const int tiles = 2 * p.steps;
   p.apart = d.dtype == MOE_F32 && (int64_t)T * d.hidden * (16 * p.mt) >= RBWD_APART;
-  const int ranges = std::max(1, RBWD_DX_WAVES / p.ncg);
+  // A dx wave takes as many token tiles as leave all blocks a place beside dW's, half
+  // the places at least: one more an XCD waits for a place to the end (bf16, 16384 x
+  // 3584, 64 experts: 74 us for the call with 252 blocks beside 252 of dW, 83 with 259;
+  // 4096 x 1536, 40 experts: 19.6 with 258 beside 192, 20.5 with 192, 21.4 with 384).
+  const int dw_places = (p.splits * p.ncg + 7) / 8;
+  const int places =
+      p.apart ? RBWD_XCD_BLOCKS / 2 : std::max(RBWD_XCD_BLOCKS / 2, RBWD_XCD_BLOCKS - dw_places);
+  const int ranges = std::max(1, 8 * places * PROD_WAVES / p.ncg);
   p.dx_tiles = (tiles + ranges - 1) / ranges;
   size_t o = 0;
   auto take = [&](size_t n) {

@@ -449,8 +449,8 @@ moe_status_t moe_undispatch_backward(const moe_dims_t* dims, int32_t T, const vo
                                      const int32_t* inv, const float* topk_w_opt,
                                      void* dy_perm_opt, float* dtopk_w_opt, void* stream);
 
-/* Bytes of workspace moe_route_backward needs for dx or dw_router (host output;
- * may be 0). */
+/* Bytes of workspace moe_route_backward needs for dx or dw_router, with T tokens
+ * or fewer (host output; may be 0). */
 moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* bytes /* host */);
 
 /* Gradient of the router l = x W_r^T and of moe_route's weights:
@@ -478,7 +478,8 @@ moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x
                                 const void* dx_add_opt, void* dx_opt, float* dw_router_opt,
                                 int32_t accumulate_dw, void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace moe_distill_topk needs (host output; may be 0). */
+/* Bytes of workspace moe_distill_topk needs, with T rows or fewer of V classes
+ * (host output; may be 0). */
 moe_status_t moe_distill_topk_size(int32_t T, int32_t V, size_t* bytes /* host */);
 
 /* Distillation from a teacher's top logits, forward and backward.  Per row t,

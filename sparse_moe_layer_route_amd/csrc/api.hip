@@ -81,12 +81,15 @@ hipError_t launch_undispatch(const moe_dims_t& d, int T, const void* y_perm, boo
 hipError_t launch_undispatch_backward(const moe_dims_t& d, int T, const void* dout,
                                       const void* y_perm, bool rows_bf16, const int32_t* inv,
                                       const float* topk_w, void* dy, float* dw, hipStream_t s);
+// Bytes that a call of T tokens takes, and bytes enough for any of up to T.
 int64_t route_backward_ws_bytes(const moe_dims_t& d, int T);
+int64_t route_backward_ws_bytes_up_to(const moe_dims_t& d, int T);
 hipError_t launch_route_backward(const moe_dims_t& d, int T, const void* x, const void* w_router,
                                  const int32_t* ids, const float* logits, const float* dtopk_w,
                                  const float* dlogits_add, float* dlogits, const void* dx_add,
                                  void* dx, float* dw, int accumulate, void* ws, hipStream_t s);
 int64_t distill_ws_bytes(int T, int V);
+int64_t distill_ws_bytes_up_to(int T, int V);
 hipError_t launch_distill(int T, int V, int64_t ld, int K, const void* student, bool is_bf16,
                           const int32_t* ids, const float* t_logits, const float* t_lse,
                           const float* token_w, float tau, float scale, float* loss,
@@ -683,7 +686,7 @@ moe_status_t moe_route_backward_size(const moe_dims_t* dims, int32_t T, size_t* 
   const moe_status_t st = check_router(dims, T);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_EINVAL;
-  *bytes = (size_t)route_backward_ws_bytes(*dims, T);
+  *bytes = (size_t)route_backward_ws_bytes_up_to(*dims, T);
   return MOE_OK;
 }
 
@@ -738,7 +741,7 @@ moe_status_t moe_route_backward(const moe_dims_t* dims, int32_t T, const void* x
 moe_status_t moe_distill_topk_size(int32_t T, int32_t V, size_t* bytes) {
   if (!bytes || T < 0 || V <= 0) return MOE_EINVAL;
   if (T > kMaxTokens || V > MOE_DISTILL_MAX_CLASSES) return MOE_EUNSUPPORTED;
-  *bytes = (size_t)distill_ws_bytes(T, V);
+  *bytes = (size_t)distill_ws_bytes_up_to(T, V);
   return MOE_OK;
 }
 

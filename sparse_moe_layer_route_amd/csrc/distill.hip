@@ -676,6 +676,12 @@ int64_t distill_ws_bytes(int T, int V) {
   }
   return most;
 }
+// Enough for any T' <= T: few rows are cut where many are not.
+int64_t distill_ws_bytes_up_to(int T, int V) {
+  int64_t most = distill_ws_bytes(T, V);
+  for (int t = 1; t <= std::min(T, SEG_TOKENS); ++t) most = std::max(most, distill_ws_bytes(t, V));
+  return most;
+}
 
 template <typename T, int NT, int NU, int PHASE, int OCC>
 static void block_launch(const DistillArgs& a, dim3 grid, const T* student, T* dstudent, hipStream_t s) {

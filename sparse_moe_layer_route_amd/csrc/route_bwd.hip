@@ -57,6 +57,7 @@ struct RouteBwdPlan {
   bool apart;              // dW and dx in launches of their own
   size_t fx, fw, part, total;  // workspace offsets: dx and dW fragments (fp32 layers: padded
                                // dlogits at fx), dW partials
+  size_t up_to;                // bytes enough for any smaller T too
 };
 
 // Blocks of the products that an XCD holds at once: two a CU.
@@ -109,7 +110,11 @@ static RouteBwdPlan route_bwd_plan(const moe_dims_t& d, int T) {
   } else {
     p.fx = take((size_t)p.steps * RBWD_STEP * p.mt * 16 * 4);
   }
-  if (p.splits > 1) p.part = take((size_t)p.splits * d.n_experts * d.hidden * 4);
+  // fewer tokens may have more ranges, up to one a unit of steps
+  const size_t partial = (size_t)d.n_experts * d.hidden * 4;
+  const int units = one ? 1 : std::min(most, (p.steps + unit - 1) / unit);
+  p.up_to = o + (units > 1 ? units * partial : 0);
+  if (p.splits > 1) p.part = take(p.splits * partial);
   p.total = o;
   return p;
 }
@@ -843,6 +848,9 @@ static hipError_t launch_dw_sum(int n4, int splits, const float* part, int accum
 
 int64_t route_backward_ws_bytes(const moe_dims_t& d, int T) {
   return T > 0 ? (int64_t)route_bwd_plan(d, T).total : 0;
+}
+int64_t route_backward_ws_bytes_up_to(const moe_dims_t& d, int T) {
+  return T > 0 ? (int64_t)((route_bwd_plan(d, T).up_to + 255) & ~(size_t)255) : 0;
 }
 
 template <typename T, int MT>

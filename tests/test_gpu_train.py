@@ -800,6 +800,35 @@ def test_train_step_in_a_graph():
             assert torch.equal(b[n], eager[n]), (i, n)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_workspaces_of_the_largest_batch(dtype):
+    """Made once for the most tokens, they serve every smaller batch."""
+    most, H, E, k, V = 2112, 256, 33, 3, 33001 if dtype == "bf16" else 17001
+    g, d = gen(83), make_dims(H, E, k, dtype, True)
+    x, w = randn(g, most, H, dtype=dtype), randn(g, E, H, dtype=dtype, std=0.05)
+    add = randn(g, most, E)
+    s, u = randn(g, most, V, dtype=dtype), randn(g, most, 4)
+    ids = torch.randint(0, V, (most, 4), generator=g).to(torch.int32).cuda()
+    rws = torch.empty(M.moe_route_backward_size(d, most), dtype=torch.uint8, device="cuda")
+    dws = torch.empty(M.moe_distill_topk_size(most, V), dtype=torch.uint8, device="cuda")
+    for T in (1, 63, 64, 65, 257, 700, 2080, most):
+        say(f"[workspaces] {dtype} T={T}")
+        got = [torch.zeros(T, E, device="cuda"), torch.zeros_like(x[:T]), torch.zeros(E, H, device="cuda")]
+        want = [torch.zeros_like(t) for t in got]
+        own = torch.empty(M.moe_route_backward_size(d, T), dtype=torch.uint8, device="cuda")
+        for out, ws in ((got, rws), (want, own)):
+            M.moe_route_backward(d, T, x, w, None, None, None, *out, ws, dlogits_add=add)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        ref, tol = f64(add[:T]).T @ f64(x[:T]), (T + 8) * U * (np.abs(f64(add[:T])).T @ np.abs(f64(x[:T])))
+        near(got[2], ref, tol, "dw_router")
+        got = [torch.zeros(T, device="cuda"), torch.zeros_like(s[:T])]
+        want = [torch.zeros_like(t) for t in got]
+        own = torch.empty(M.moe_distill_topk_size(T, V), dtype=torch.uint8, device="cuda")
+        for out, ws in ((got, dws), (want, own)):
+            M.moe_distill_topk(T, V, 4, s, ids, u, *out, ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.isfinite(got[0]).all()
+
+
 def test_two_streams_at_once():
     """Two steps with buffers of their own on two streams."""
     layer = small_layer("bf16", False)

@@ -186,3 +186,18 @@ def test_binding_refuses_host_tensors_and_other_types():
         M.moe_undispatch_backward(d, 4, x, None, inv, None, None, None)
     with pytest.raises(TypeError):
         M.moe_dispatch(d, 4, None, inv, rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,E", [(64, 2), (64, 17), (1536, 40), (3584, 64), (40000 // 64 * 64, 9)])
+def test_route_workspace_serves_fewer_tokens(H, E, dtype):
+    """A workspace made for T tokens is no smaller than one for any fewer."""
+    d = M.Dims(hidden=H, n_experts=E, top_k=2, inter=64, dtype=dtype)
+    sizes = [M.moe_route_backward_size(d, T) for T in range(0, 20000, 13)]
+    assert sizes == sorted(sizes) and sizes[0] == 0
+
+
+@pytest.mark.parametrize("V", [3, 4096, 16380, 33000, 66000, 131080, 262144])
+def test_distill_workspace_serves_fewer_rows(V):
+    sizes = [M.moe_distill_topk_size(T, V) for T in [*range(300), *range(300, 40000, 997)]]
+    assert sizes == sorted(sizes) and sizes[0] == 0

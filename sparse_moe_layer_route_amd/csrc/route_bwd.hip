@@ -419,13 +419,15 @@ constexpr int dw_lds_floats() {
 // call, 14.3 with the waves of a pair each loading and interleaving what both need;
 // 16384 x 3584: 74.7, 74.0.  A second buffer, which spares one of the two barriers a
 // group, gains nothing (12.7, 75) and halves the blocks that a CU has LDS for.
-template <int MT>
+// WAVES: of the block; those from PROD_WAVES on only take part in its barriers.
+template <int MT, int WAVES>
 __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
                                          const bf16* __restrict__ x, float* lds) {
   constexpr int TILES = MT == 3 ? 4 : MT, NC = 8 * TILES / PROD_WAVES;
   const int split = item / a.ncg, cg = item - split * a.ncg;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool on = WAVES == PROD_WAVES || wv < PROD_WAVES;
   const int m = wv % TILES, c0 = wv / TILES * NC;
   const int s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
   const int whole = a.T / RBWD_STEP, e = min(s1, whole);  // steps with all their rows
@@ -467,23 +469,25 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
   auto group = [&](int gi, uint4 (&v)[8]) {
     const int s = s0 + gi * DW_GROUP;
     if (gi > 0) __syncthreads();  // all are through with the group before
-    if (s + wv < e) put(frags + wv * 512, v);
-    rows(gi + 2, v);
+    if (on && s + wv < e) put(frags + wv * 512, v);
+    if (on) rows(gi + 2, v);
     // the scheduler would move the loads down to their uses
     __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < DW_GROUP; ++q) {
-      if (s + q < e && m < MT) mfma(frags + q * 512, q);
-      parts(min(s + DW_GROUP + q, e - 1), q);
+      if (s + q < e && m < MT && on) mfma(frags + q * 512, q);
+      if (on) parts(min(s + DW_GROUP + q, e - 1), q);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   if (groups > 0) {
-    rows(0, v0);
+    if (on) {
+      rows(0, v0);
 #pragma unroll
-    for (int q = 0; q < DW_GROUP; ++q) parts(min(s0 + q, e - 1), q);
-    rows(1, v1);
+      for (int q = 0; q < DW_GROUP; ++q) parts(min(s0 + q, e - 1), q);
+      rows(1, v1);
+    }
     for (int gi = 0; gi < groups; gi += 2) {
       group(gi, v0);
       if (gi + 1 < groups) group(gi + 1, v1);
@@ -491,15 +495,15 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
   }
   if (s0 <= whole && whole < s1) {  // the last step, not whole
     __syncthreads();
-    parts(whole, 0);
+    if (on) parts(whole, 0);
     if (wv == 0) {
       load_rows8_below(x, (int64_t)whole * RBWD_STEP, a.T, a.H, off, v0);
       put(frags, v0);
     }
     __syncthreads();
-    if (m < MT) mfma(frags, 0);
+    if (m < MT && on) mfma(frags, 0);
   }
-  if (m >= MT) return;
+  if (m >= MT || !on) return;
   const bool direct = a.splits == 1;
   float* out = direct ? a.dw : a.part + (int64_t)split * a.E * a.H;
   typedef float vec_t __attribute__((ext_vector_type(NC < 4 ? NC : 4)));
@@ -519,8 +523,9 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
   }
 }
 // dW of a wave's columns over one range of tokens, fp32.  The waves of way 1 and up
-// leave their tiles in LDS, those of way 0 add them in way order and store.
-template <int MT>
+// leave their tiles in LDS, those of way 0 add them in way order and store.  WAVES as
+// above.
+template <int MT, int WAVES>
 __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
                                          const float* __restrict__ x, float* lds) {
   using S = DwShape<MT>;
@@ -528,6 +533,7 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
   const int split = item / a.ncg, cg = item - split * a.ncg;
   const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool on = WAVES == PROD_WAVES || wv < PROD_WAVES;
   const int half = wv % S::MH, way = wv / S::MH, m0 = half * MW;
   const int s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
   f32x4_t acc[MW][NC];
@@ -536,7 +542,7 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // lanes past H read the row's last columns; their results are dropped below
-  dw_steps<MT>(a, x, min(cg * COLS + NC * n, a.H - NC), m0, s0, way, s1, acc);
+  if (on) dw_steps<MT>(a, x, min(cg * COLS + NC * n, a.H - NC), m0, s0, way, s1, acc);
   auto each = [&](auto f) {
 #pragma unroll
     for (int m = 0; m < MW; ++m)
@@ -550,9 +556,9 @@ __device__ __forceinline__ void route_dw(const RouteBwdArgs& a, int item,
   auto slot = [&](int w, int r, int c) {
     return reinterpret_cast<float4*>(lds + ((w - 1) * S::MH + half) * TILE + r * COLS + c);
   };
-  if (way > 0) each([&](int r, int c, float4 v) { *slot(way, r, c) = v; });
+  if (on && way > 0) each([&](int r, int c, float4 v) { *slot(way, r, c) = v; });
   __syncthreads();
-  if (way > 0) return;
+  if (way > 0) return;  // the waves that are not on as well
   const bool direct = a.splits == 1;
   float* out = direct ? a.dw : a.part + (int64_t)split * a.E * a.H;
   each([&](int r, int c, float4 v) {
@@ -742,7 +748,7 @@ route_products_kernel(RouteBwdArgs a, int dx_items, const T* __restrict__ x,
   const int nw = (a.dw_blocks + 7) & ~7, b0 = blockIdx.x;
   if (b0 < nw) {
     const int item = xcd_item(b0, a.dw_blocks);
-    if (item < a.dw_blocks) route_dw<MT>(a, item, x, lds);
+    if (item < a.dw_blocks) route_dw<MT, PROD_WAVES>(a, item, x, lds);
   } else {
     // fp32: dx first, so that dW's long waves have a SIMD to themselves early (2048
     // x 2048, 40 experts: 22.1 us for the call, 25.3 at one priority; a bf16 call
@@ -794,7 +800,7 @@ route_few_kernel(DlogitsArgs g, RouteBwdArgs a, int dx_items, const T* __restric
   a.fx = a.fw = packed;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (for_dw) {
-    if (wv < PROD_WAVES) route_dw<MT>(a, blockIdx.x, x, lds);  // its barriers wait for these
+    route_dw<MT, RBWD_THREADS / MOE_WAVE>(a, blockIdx.x, x, lds);  // all waves: it has barriers
   } else {
     const int item = (blockIdx.x - a.dw_blocks) * (RBWD_THREADS / MOE_WAVE) + wv;
     if (item < dx_items) route_dx<MT>(a, item, w, dx_add, dx);

@@ -2,6 +2,8 @@
 differences and identities, and the entry points' refusals (status codes from
 include/moe_route.h, before any HIP call)."""
 import ctypes
+import pathlib
+import re
 
 import numpy as np
 import pytest
@@ -201,3 +203,21 @@ def test_route_workspace_serves_fewer_tokens(H, E, dtype):
 def test_distill_workspace_serves_fewer_rows(V):
     sizes = [M.moe_distill_topk_size(T, V) for T in [*range(300), *range(300, 40000, 997)]]
     assert sizes == sorted(sizes) and sizes[0] == 0
+
+
+# ----------------------------------------------------------------- sources --
+def test_barriers_are_for_whole_blocks():
+    """A device function with a barrier in it is never called for some of a
+    block's waves or lanes only: a barrier that part of a block does not reach
+    has no meaning."""
+    csrc = pathlib.Path(M.__file__).parent / "csrc"
+    text = "\n".join(re.sub(r"//[^\n]*", "", f.read_text()) for f in sorted(csrc.iterdir())
+                     if f.suffix in (".hip", ".h"))
+    bodies = re.split(r"\n}", text)                     # functions end in column 0
+    names = {re.findall(r"\b(?:void|int|float|bool) (\w+)\(", b)[0] for b in bodies
+             if "__syncthreads()" in b and re.search(r"__device__[^;{]*\b(?:void|int|float|bool) \w+\(", b)}
+    assert "route_dw" in names
+    own = r"\b(?:wv|wave|lane|tid|threadIdx|l)\b"
+    for name in names | {"__syncthreads"}:
+        for cond in re.findall(r"if \(([^;{}]*?)\)\s*" + name + r"\s*[<(]", text):
+            assert not re.search(own, cond), f"{name} under if ({cond})"

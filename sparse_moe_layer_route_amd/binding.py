@@ -145,8 +145,14 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_workspace_size", "moe_r
 
 
 # ------------------------------------------------------------------ helpers --
+_FIXED = frozenset((int, float, bool, str))     # types whose values cannot change
+
+
 @dataclasses.dataclass
 class Dims:
+    # _dims' converted copy, beside the fields rather than among them
+    __slots__ = ("__dict__", "__weakref__", "_struct")
+
     hidden: int
     n_experts: int
     top_k: int
@@ -162,9 +168,8 @@ class Dims:
     tie_margin: float = 1e-4
     weight_layout: str = "rows"      # "rows" or "mfma16" (see pack_weights)
 
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        self.__dict__.pop("_struct", None)   # _dims' converted copy
+    def __getstate__(self):                      # copies and pickles hold the fields alone
+        return self.__dict__
 
     def c(self) -> MoeDims:
         return MoeDims(self.hidden, self.n_experts, self.top_k, self.inter, self.n_shared,
@@ -216,9 +221,20 @@ def _mode(mode) -> int:
 def _dims(d) -> MoeDims:
     if not isinstance(d, Dims):
         return d
-    c = d.__dict__.get("_struct")    # converted once, until a field changes
-    if c is None:
-        c = d.__dict__["_struct"] = d.c()
+    # converted once for the same fields (0.2 us to compare them, 1 to convert)
+    try:
+        fields, c = d._struct
+        if d.__dict__ == fields:
+            return c
+    except AttributeError:
+        pass
+    fields = dict(d.__dict__)
+    if type(d) is not Dims or not _FIXED.issuperset(map(type, fields.values())):
+        return d.c()
+    then = object.__new__(Dims)      # these fields, whatever another thread sets meanwhile
+    then.__dict__.update(fields)
+    c = then.c()
+    d._struct = (fields, c)
     return c
 
 

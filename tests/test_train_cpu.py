@@ -1,8 +1,11 @@
 """Training operators, without a GPU: the fp64 oracle against finite
 differences and identities, and the entry points' refusals (status codes from
 include/moe_route.h, before any HIP call)."""
+import copy
 import ctypes
+import dataclasses
 import pathlib
+import pickle
 import re
 
 import numpy as np
@@ -221,3 +224,69 @@ def test_barriers_are_for_whole_blocks():
     for name in names | {"__syncthreads"}:
         for cond in re.findall(r"if \(([^;{}]*?)\)\s*" + name + r"\s*[<(]", text):
             assert not re.search(own, cond), f"{name} under if ({cond})"
+
+
+# -------------------------------------------------------------------- Dims --
+def as_dict(c):
+    return {n: getattr(c, n) for n, _ in c._fields_}
+
+
+def test_dims_hold_their_fields_alone():
+    """A call leaves a Dims as it was: its attributes are the fields."""
+    d = dims(renormalize=True)
+    before = dict(vars(d))
+    M.moe_route_backward_size(d, 16)
+    M.moe_workspace_size(d, 16, "standard")
+    assert vars(d) == before and set(before) == {f.name for f in dataclasses.fields(d)}
+    assert M.Dims(**vars(d)) == d
+    for e in (copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d)), dataclasses.replace(d)):
+        assert e == d and vars(e) == before and as_dict(B._dims(e)) == as_dict(d.c())
+        e.hidden = 512
+        assert B._dims(e).hidden == 512 and B._dims(d).hidden == 256
+
+
+def test_dims_changed_between_calls():
+    """Whatever way a field changes, the next call takes the new value."""
+    d = dims()
+    steps = [lambda: setattr(d, "hidden", 128), lambda: d.__dict__.update(n_experts=16),
+             lambda: object.__setattr__(d, "top_k", 4), lambda: setattr(d, "renormalize", True),
+             lambda: setattr(d, "n_shared", 2), lambda: delattr(d, "n_shared"),
+             lambda: setattr(d, "dtype", "f32"), lambda: setattr(d, "tie_margin", 0.5),
+             lambda: [delattr(d, "lore_rank"), delattr(d, "floe_keep"), setattr(d, "floe_keep", 8),
+                      setattr(d, "lore_rank", 16)],
+             lambda: [delattr(d, "lore_rank"), delattr(d, "floe_keep"), setattr(d, "lore_rank", 8),
+                      setattr(d, "floe_keep", 16)]]
+    for step in steps:
+        B._dims(d)
+        step()
+        assert as_dict(B._dims(d)) == as_dict(d.c())
+
+    class Wide(M.Dims):
+        scale = 1
+
+        def c(self):
+            c = super().c()
+            c.hidden *= self.scale
+            return c
+
+    w = Wide(hidden=64, n_experts=4, top_k=2, inter=64)
+    assert B._dims(w).hidden == 64
+    Wide.scale = 2
+    assert B._dims(w).hidden == 128
+
+
+def test_dims_changed_while_converted():
+    """A field set while another thread converts the old values is not lost."""
+    d = dims()
+    convert = M.Dims.c
+
+    def slow(self):
+        c = convert(self)
+        d.hidden = 1024                      # what another thread does here
+        return c
+    M.Dims.c = slow
+    try:
+        B._dims(d)
+    finally:
+        M.Dims.c = convert
+    assert B._dims(d).hidden == 1024

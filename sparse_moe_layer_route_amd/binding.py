@@ -444,6 +444,15 @@ def _arg(dev, name, t, n, dtype, optional=False):
     raise ValueError(f"{name} lives on {t.device}, not on the current GPU")
 
 
+def _rows(name, t, T, n):
+    """Refuses a tensor whose rows are not the n elements that the call steps by:
+    T > 1 rows would be taken from the wrong places.  Flat tensors, and other
+    shapes of the same T n elements, pass."""
+    if (T > 1 and isinstance(t, torch.Tensor) and t.dim() > 1 and t.shape[-1] != n
+            and t.numel() != T * n):
+        raise ValueError(f"{name}: expected rows of {n} elements, got {t.shape[-1]}")
+
+
 def _row_dtype(t):
     if t is None:
         raise TypeError("expected a torch.Tensor")
@@ -524,9 +533,14 @@ def moe_distill_topk(T, V, K, student, teacher_ids, teacher_logits, loss, dstude
                      teacher_lse=None, token_w=None, temperature=1.0, scale=1.0, ld=None,
                      stream=None):
     """ld: elements from one row of student (and dstudent) to the next; None:
-    the length of student's last axis."""
+    the length of student's last axis, and of dstudent's."""
     row, dev = _row_dtype(student), _device(stream)
-    ld = student.shape[-1] if ld is None else int(ld)
+    if ld is None:
+        ld = student.shape[-1]
+        _rows("dstudent", dstudent, T, ld)
+    ld = int(ld)
+    _rows("teacher_ids", teacher_ids, T, K)
+    _rows("teacher_logits", teacher_logits, T, K)
     n = (T - 1) * ld + V if T > 0 else 0
     ws_p, ws_n = _ws(dev, ws)
     _check(_lib.moe_distill_topk(

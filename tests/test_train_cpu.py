@@ -290,3 +290,25 @@ def test_dims_changed_while_converted():
     finally:
         M.Dims.c = convert
     assert B._dims(d).hidden == 1024
+
+
+# ------------------------------------------------------------ row lengths --
+def test_distill_refuses_rows_of_other_lengths():
+    """The first K of a teacher's longer rows, or a gradient in rows of another
+    stride, would be taken from the wrong places: refused, not answered."""
+    T, V, K = 6, 20, 4
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)
+
+    def call(ids=(T, K), u=(T, K), ds=(T, V), student=(T, V), T=T, **kw):
+        M.moe_distill_topk(T, V, K, z(*student), z(*ids, dtype=torch.int32), z(*u), z(T),
+                           None if ds is None else z(*ds), None, **kw)
+    for kw in [dict(ids=(T, 2 * K)), dict(u=(T, 2 * K)), dict(ds=(T, V + 4)), dict(ids=(2, 3, K + 1))]:
+        with pytest.raises(ValueError, match="rows of"):
+            call(**kw)
+    # one row, flat tensors, more rows than the call's, other shapes of as many elements, a
+    # stride of the caller's: as far as the host tensors take them
+    for kw in [dict(T=1, ids=(1, 2 * K), ds=(1, V + 4)), dict(ids=(2 * T * K,)), dict(ids=(T + 3, K)),
+               dict(ids=(2, 3, K)), dict(ids=(T * K, 1)), dict(ds=(T, 2, V // 2)), dict(ds=(2, 3, V)),
+               dict(ds=None), dict(student=(T, 2, V), ds=(T, 2, V), ld=2 * V), dict(ds=(T * V + 8,))]:
+        with pytest.raises(ValueError, match="lives on"):
+            call(**kw)

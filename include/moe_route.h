@@ -414,7 +414,7 @@ moe_status_t moe_layer_forward_noalloc(const moe_dims_t* dims, int32_t T, const 
  * fp32 (moe_distill_topk: the teacher's entries in 64 bits) in a fixed order,
  * so results are bitwise reproducible.  Shape limits are those of the head of
  * this file, but the intermediate sizes do not count: T * k * hidden < 2^31
- * and T <= 2^22.  Results depend on no state between calls; two captured
+ * (moe_route_backward, which has no sorted rows, takes any) and T <= 2^22.  Results depend on no state between calls; two captured
  * graphs need a workspace each when they can run at the same time.  T = 0
  * enqueues nothing (but see moe_route_backward), and no buffer is looked at. */
 

@@ -620,12 +620,14 @@ moe_status_t check_rows(const moe_dims_t* d, int32_t T, moe_dtype_t row_dtype) {
   return rows_fit(*d, T) ? MOE_OK : MOE_EUNSUPPORTED;
 }
 
-// The router's matrix is indexed below 2^31 elements as well, and a lane's
-// place in a tile of rows in 32-bit bytes.
+// No sorted rows here: x, dx and dlogits are indexed in 64 bits.  The router's
+// matrix is indexed below 2^31 elements, and a lane's place in a tile of rows in
+// 32-bit bytes.
 moe_status_t check_router(const moe_dims_t* d, int32_t T) {
-  const moe_status_t st = check_rows(d, T, d ? d->dtype : MOE_F32);
+  const moe_status_t st = check_dims(d);
   if (st != MOE_OK) return st;
-  if (d->hidden > (1 << 24)) return MOE_EUNSUPPORTED;
+  if (T < 0) return MOE_EINVAL;
+  if (T > kMaxTokens || d->hidden > (1 << 24)) return MOE_EUNSUPPORTED;
   return (int64_t)d->n_experts * d->hidden < (int64_t(1) << 31) ? MOE_OK : MOE_EUNSUPPORTED;
 }
 

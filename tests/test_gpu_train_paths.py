@@ -61,6 +61,33 @@ def test_route_backward_paths(T, H, E, k, dtype, renorm, form):
     base.test_route_backward(T, H, E, k, dtype, renorm, form)
 
 
+@pytest.mark.parametrize("T,H,dtype", [((1 << 20) + 45, 2112, "bf16"), ((1 << 19) + 45, 4160, "f32")])
+def test_route_backward_past_2_31_elements(T, H, dtype):
+    """x and dx of more than 2^31 elements each.  Small whole numbers: every sum
+    is below 2^24 (dx below 2^8) and exact."""
+    E, k = 9, 4
+    assert T * H > 1 << 31 and T < 1 << 24
+    say(f"[route_backward] T={T} H={H} {dtype} whole numbers")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    whole = lambda m, *shape: torch.randint(-m, m + 1, shape, generator=g, device="cuda", dtype=torch.int8)
+    x, w = whole(1, T, H).to(TT[dtype]), whole(8, E, H).to(TT[dtype])
+    add = whole(1, T, E).float()
+    add[T // 2:T // 2 + 7] = 0.0
+    d = make_dims(H, E, k, dtype)
+    dl, dx, dw = torch.empty_like(add), torch.empty_like(x), torch.empty(E, H, device="cuda")
+    ws = torch.empty(M.moe_route_backward_size(d, T), dtype=torch.uint8, device="cuda")
+    M.moe_route_backward(d, T, x, w, None, None, None, dl, dx, dw, ws, dlogits_add=add)
+    assert torch.equal(dl, add)
+    want = torch.zeros(E, H, device="cuda")
+    at = add.t().contiguous()
+    for t0 in range(0, T, 65536):
+        t1 = min(T, t0 + 65536)
+        assert torch.equal(dx[t0:t1].float(), add[t0:t1] @ w.float()), t0
+        want += at[:, t0:t1].contiguous() @ x[t0:t1].float()
+    assert torch.equal(dw, want)
+
+
 # ------------------------------------------------------------ distillation --
 LONG = [  # T, V, K, dtype: about the longest rows of one block, odd lengths
     (66, 40001, 20, "f32"), (65, 128257, 64, "bf16"),

@@ -312,3 +312,21 @@ def test_distill_refuses_rows_of_other_lengths():
                dict(ds=None), dict(student=(T, 2, V), ds=(T, 2, V), ld=2 * V), dict(ds=(T * V + 8,))]:
         with pytest.raises(ValueError, match="lives on"):
             call(**kw)
+
+
+def test_route_backward_takes_batches_that_sorted_rows_do_not():
+    """Its limits are T <= 2^22, E * hidden < 2^31 and hidden <= 2^24 alone."""
+    for H, k, T in [(2048, 8, 1 << 17), (2048, 8, (1 << 20) + 3), (2048, 1, 1 << 22), (1 << 20, 8, 1 << 22)]:
+        assert T * k * H >= 1 << 31
+        d = dims(hidden=H, n_experts=64, top_k=k, inter=64, dtype="f32")
+        n = M.moe_route_backward_size(d, T)
+        assert n >= T * 64 * 4
+        far = lambda i: (1 << 56) + (i << 46)          # buffers of up to 2^44 bytes, never looked at
+        names = ["x", "w", "ids", "logits", "dtopk_w", "dl", "dx", "dw", "ws"]
+        at = {m: far(i) for i, m in enumerate(names)}
+        assert route_bwd(d, T, **at, n=n - 1 - n // 2) == B.MOE_EWORKSPACE
+        assert route_bwd(d, T, **{**at, "dx": at["x"] + T * H * 4 - 16}, n=n) == B.MOE_EINVAL
+    n = ctypes.c_size_t(0)
+    for T in (-1, (1 << 22) + 1):
+        st = L.moe_route_backward_size(ctypes.byref(dims().c()), T, ctypes.byref(n))
+        assert st == (B.MOE_EINVAL if T < 0 else B.MOE_EUNSUPPORTED)

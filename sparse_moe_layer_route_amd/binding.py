@@ -422,13 +422,16 @@ def _device(stream):
     return dev
 
 
-def _arg(dev, name, t, n, dtype, optional=False):
+def _arg(dev, name, t, n, dtype, optional=False, row=0):
     """Address of a contiguous tensor of at least n elements of `dtype` on
-    GPU `dev`; None where optional."""
+    GPU `dev`; None where optional.  row: the call steps by rows of so many
+    elements, so a tensor of other rows is refused (flat ones, and other shapes
+    of the n elements, are not)."""
     if t is None and optional:
         return None
     try:
-        if (t.dtype is dtype and t.numel() >= n and t.get_device() == dev
+        m = t.numel()
+        if (t.dtype is dtype and (m == n or m > n and not row) and t.get_device() == dev
                 and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
@@ -439,18 +442,13 @@ def _arg(dev, name, t, n, dtype, optional=False):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() < n:
         raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
+    if row and t.numel() != n and t.dim() > 1 and t.shape[-1] != row:
+        raise ValueError(f"{name}: expected rows of {row} elements, got {t.shape[-1]}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
-    raise ValueError(f"{name} lives on {t.device}, not on the current GPU")
-
-
-def _rows(name, t, T, n):
-    """Refuses a tensor whose rows are not the n elements that the call steps by:
-    T > 1 rows would be taken from the wrong places.  Flat tensors, and other
-    shapes of the same T n elements, pass."""
-    if (T > 1 and isinstance(t, torch.Tensor) and t.dim() > 1 and t.shape[-1] != n
-            and t.numel() != T * n):
-        raise ValueError(f"{name}: expected rows of {n} elements, got {t.shape[-1]}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lives on {t.device}, not on the current GPU")
+    return t.data_ptr()
 
 
 def _row_dtype(t):
@@ -535,21 +533,20 @@ def moe_distill_topk(T, V, K, student, teacher_ids, teacher_logits, loss, dstude
     """ld: elements from one row of student (and dstudent) to the next; None:
     the length of student's last axis, and of dstudent's."""
     row, dev = _row_dtype(student), _device(stream)
+    ds_row = 0                       # rows to step by, where there is more than one
     if ld is None:
         ld = student.shape[-1]
-        _rows("dstudent", dstudent, T, ld)
-    ld = int(ld)
-    _rows("teacher_ids", teacher_ids, T, K)
-    _rows("teacher_logits", teacher_logits, T, K)
+        ds_row = ld if T > 1 else 0
+    ld, k_row = int(ld), K if T > 1 else 0
     n = (T - 1) * ld + V if T > 0 else 0
     ws_p, ws_n = _ws(dev, ws)
     _check(_lib.moe_distill_topk(
         T, V, ld, K, _arg(dev, "student", student, n, student.dtype), row,
-        _arg(dev, "teacher_ids", teacher_ids, T * K, torch.int32),
-        _arg(dev, "teacher_logits", teacher_logits, T * K, torch.float32),
+        _arg(dev, "teacher_ids", teacher_ids, T * K, torch.int32, row=k_row),
+        _arg(dev, "teacher_logits", teacher_logits, T * K, torch.float32, row=k_row),
         _arg(dev, "teacher_lse", teacher_lse, T, torch.float32, True),
         _arg(dev, "token_w", token_w, T, torch.float32, True), float(temperature), float(scale),
-        _arg(dev, "loss", loss, T, torch.float32), _arg(dev, "dstudent", dstudent, n, student.dtype, True),
+        _arg(dev, "loss", loss, T, torch.float32), _arg(dev, "dstudent", dstudent, n, student.dtype, True, ds_row),
         ws_p, ws_n, _stream(stream, dev)), "moe_distill_topk")
 
 

@@ -7,6 +7,7 @@ import dataclasses
 import pathlib
 import pickle
 import re
+import types
 
 import numpy as np
 import pytest
@@ -293,11 +294,17 @@ def test_dims_changed_while_converted():
 
 
 # ------------------------------------------------------------ row lengths --
-def test_distill_refuses_rows_of_other_lengths():
+def test_distill_refuses_rows_of_other_lengths(monkeypatch):
     """The first K of a teacher's longer rows, or a gradient in rows of another
     stride, would be taken from the wrong places: refused, not answered."""
     T, V, K = 6, 20, 4
     z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)
+    calls = []
+    # host tensors for the current GPU's, and a library that only counts
+    monkeypatch.setattr(B, "_device", lambda stream: -1)
+    monkeypatch.setattr(B, "_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(B, "_lib", types.SimpleNamespace(
+        moe_distill_topk=lambda *a: calls.append(a) or B.MOE_OK))
 
     def call(ids=(T, K), u=(T, K), ds=(T, V), student=(T, V), T=T, **kw):
         M.moe_distill_topk(T, V, K, z(*student), z(*ids, dtype=torch.int32), z(*u), z(T),
@@ -305,13 +312,16 @@ def test_distill_refuses_rows_of_other_lengths():
     for kw in [dict(ids=(T, 2 * K)), dict(u=(T, 2 * K)), dict(ds=(T, V + 4)), dict(ids=(2, 3, K + 1))]:
         with pytest.raises(ValueError, match="rows of"):
             call(**kw)
+    assert not calls
     # one row, flat tensors, more rows than the call's, other shapes of as many elements, a
-    # stride of the caller's: as far as the host tensors take them
-    for kw in [dict(T=1, ids=(1, 2 * K), ds=(1, V + 4)), dict(ids=(2 * T * K,)), dict(ids=(T + 3, K)),
-               dict(ids=(2, 3, K)), dict(ids=(T * K, 1)), dict(ds=(T, 2, V // 2)), dict(ds=(2, 3, V)),
-               dict(ds=None), dict(student=(T, 2, V), ds=(T, 2, V), ld=2 * V), dict(ds=(T * V + 8,))]:
-        with pytest.raises(ValueError, match="lives on"):
-            call(**kw)
+    # stride of the caller's
+    fine = [dict(T=1, ids=(1, 2 * K), ds=(1, V + 4)), dict(ids=(2 * T * K,)), dict(ids=(T + 3, K)),
+            dict(ids=(2, 3, K)), dict(ids=(T * K, 1)), dict(ds=(T, 2, V // 2)), dict(ds=(2, 3, V)),
+            dict(ds=None), dict(student=(T, 2, V), ds=(T, 2, V), ld=2 * V), dict(ds=(T * V + 8,)),
+            dict(student=(T, V + 4), ds=(T, V + 4))]
+    for kw in fine:
+        call(**kw)
+    assert len(calls) == len(fine) and calls[-1][2] == V + 4
 
 
 def test_route_backward_takes_batches_that_sorted_rows_do_not():

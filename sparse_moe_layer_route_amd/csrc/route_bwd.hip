@@ -224,6 +224,12 @@ __device__ __forceinline__ void put_dlogits(const DlogitsArgs& a, int t, const f
     tile[t % RBWD_STEP][e] = on ? dl[q] : 0.f;
   }
 }
+// A finite value past the largest bf16 would round to infinity: that largest, and
+// the next parts hold the rest.
+__device__ __forceinline__ float bf16_finite(float v) {
+  constexpr float MOST = 0x1.FEp127f;
+  return fabsf(v) > MOST && fabsf(v) < __builtin_inff() ? copysignf(MOST, v) : v;
+}
 // The fragments of a tile, fx and fw each where not null:
 //   fx [16-token tile][k step][part][lane]: token lane % 16, experts
 //     32 s + 8 (lane / 16) .. +7 (zero past T and E),
@@ -251,7 +257,8 @@ __device__ __forceinline__ void pack_dlogits(const rbwd_tile_t& tile, int mt, ui
       uint32_t w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        w[c] = f2_to_bf16x2(v[2 * c], v[2 * c + 1]);
+        w[c] = p == 0 ? f2_to_bf16x2(bf16_finite(v[2 * c]), bf16_finite(v[2 * c + 1]))
+                      : f2_to_bf16x2(v[2 * c], v[2 * c + 1]);
         v[2 * c] -= bf16_lo(w[c]);
         v[2 * c + 1] -= bf16_hi(w[c]);
       }

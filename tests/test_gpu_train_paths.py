@@ -61,6 +61,38 @@ def test_route_backward_paths(T, H, E, k, dtype, renorm, form):
     base.test_route_backward(T, H, E, k, dtype, renorm, form)
 
 
+@pytest.mark.parametrize("T", [20, 60, 300])
+def test_route_backward_of_the_largest_logit_gradients(T):
+    """fp32's largest values, which no bf16 part can round to, are finite, and so
+    are the products; infinite and NaN ones give NaN."""
+    H, E = 192, 20
+    g = gen(71 + T)
+    say(f"[route_backward] T={T} largest logit gradients")
+    x, w = randn(g, T, H, dtype="bf16", std=1e-3), randn(g, E, H, dtype="bf16", std=1e-3)
+    add = randn(g, T, E)
+    most = torch.finfo(torch.float32).max
+    at = torch.arange(T, device="cuda")
+    add[at, at % 7] = torch.where(at % 2 == 0, most, -most)
+    add[at, 7 + at % 3] = torch.where(at % 3 == 0, 3.39e38, -3.3961e38)   # below and past half a step
+    d = make_dims(H, E, 2, "bf16")
+    dl, dx, dw = torch.empty_like(add), torch.empty_like(x), torch.empty(E, H, device="cuda")
+    ws = torch.empty(M.moe_route_backward_size(d, T), dtype=torch.uint8, device="cuda")
+    run = lambda: M.moe_route_backward(d, T, x, w, None, None, None, dl, dx, dw, ws, dlogits_add=add)
+    run()
+    rdx, rdw = TO.router_linear_backward(f64(add), f64(x), f64(w))
+    mx, mw = TO.router_linear_backward(np.abs(f64(add)), np.abs(f64(x)), np.abs(f64(w)))
+    near(dx, rdx, ((2 * E + 2) * base.U + 2.0 ** -16) * mx + base.HALF["bf16"] * 1.01 * np.abs(rdx), "dx")
+    near(dw, rdw, (T + 8) * base.U * mw, "dw_router")
+    add[3, 2], add[5, 4] = float("inf"), float("nan")
+    run()
+    assert torch.isnan(dx[3]).all() and torch.isnan(dx[5]).all()
+    assert torch.isnan(dw[2]).all() and torch.isnan(dw[4]).all()
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[[3, 5]] = False
+    assert torch.isfinite(dx[rest]).all()
+    assert torch.isfinite(dw[[e for e in range(E) if e not in (2, 4)]]).all()
+
+
 @pytest.mark.parametrize("T,H,dtype", [((1 << 20) + 45, 2112, "bf16"), ((1 << 19) + 45, 4160, "f32")])
 def test_route_backward_past_2_31_elements(T, H, dtype):
     """x and dx of more than 2^31 elements each.  Small whole numbers: every sum

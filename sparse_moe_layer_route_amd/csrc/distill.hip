@@ -356,9 +356,10 @@ template <int NU> __device__ __forceinline__ float units_max(const uint4 (&x)[NU
 
 // Segment blockIdx.x of row blockIdx.y (DISTILL_ROW: row blockIdx.x), NT
 // threads of at most NU units each.  OCC: waves a SIMD should hold.
-// 2048 x 32000 bf16, 64 entries, a tenth of the rows masked (250 MB): 54 us, 4.6
-// TB/s; vector instructions (15 an element) fill 56% of the time beside the
-// loads and stores of other rows.  Cut rows, 7 x 100003 fp32: 11.2 us, two launches.
+// 2048 x 32000 bf16, 64 entries, a tenth of the rows masked (250 MB): 59 us over
+// changing inputs, 4.2 TB/s (50 replayed on one set, part of which stays in the
+// caches); vector instructions (15 an element) are issued in half of a CU's busy
+// cycles, beside the loads and stores of other rows.  Cut rows, 7 x 100003 fp32: 11.2 us, two launches.
 template <typename T, int NT, int NU, int PHASE, int OCC>
 __global__ void __launch_bounds__(NT, OCC)
 distill_block_kernel(DistillArgs a, const T* student, T* dstudent) {

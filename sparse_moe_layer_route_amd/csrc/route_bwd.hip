@@ -26,9 +26,11 @@
 // fp32 layers run v_mfma_f32_16x16x4_f32, whose operands are single values.
 //
 // bf16, 16384 x 3584, 64 experts (246 MB, 45.5 us at the rate of a large copy):
-// 75 us, of which 8 the logits' gradient, 61 the products, 5 the sum of the
-// ranges.  dW alone reads its 117 MB at about 4 TB/s, dx alone writes as much at
-// 4.5, and side by side they do not gain on one another.
+// 73 us, of which 8 the logits' gradient, 61 the products, 5 the sum of the
+// ranges.  With a launch each dW's products take 35 us (117 MB of x read at 3.4
+// TB/s), dx's 27 (as much written at 4.3): side by side they gain nothing.  That is
+// no bound of the memory, which does both at 5.4 in a copy, but of the waits in
+// the two loops (see route_dw and route_dx).
 #include <algorithm>
 #include <type_traits>
 
@@ -420,8 +422,10 @@ constexpr int dw_lds_floats() {
 // of x each, interleave it into fragments and leave them in LDS for all four, which
 // own an expert tile each (of fewer than three tiles a part of the columns), so no
 // row is read or interleaved twice and a wave holds 32 accumulators.  Rows are asked
-// for two groups of steps ahead, a step's fragments of dlogits as soon as the group
-// before is through with theirs.  The last step, if it is not whole, runs by itself, so
+// for two groups of steps ahead and a step's fragments of dlogits as soon as the group
+// before is through with theirs, which is after the rows of the group behind it: loads
+// retire in order, so a group's first product waits for those rows too, and of the
+// two groups asked for one is in flight.  The last step, if it is not whole, runs by itself, so
 // that the loop has one way to load its rows.  1024 x 2048, 64 experts: 12.7 us for the
 // call, 14.3 with the waves of a pair each loading and interleaving what both need;
 // 16384 x 3584: 74.7, 74.0.  A second buffer, which spares one of the two barriers a
@@ -608,8 +612,10 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
   }
   const uint32_t off = (uint32_t)(n * a.H + 8 * g) * 2u;  // the lane's runs: 64 i bytes on
   const int runs = min(4, (a.H - cg * 128) / 32);         // 2 or 4 of them inside H
-  // a tile's fragments and addend are asked for before the tile before it is
-  // stored: loads and stores retire in one order
+  // A tile's fragments and addend are asked for before the tile before it is
+  // stored: loads and stores retire in one order.  Both are conditional, so their
+  // number is not known and the wait before the second half of a tile's products
+  // is for all of them, the stores of the tile before included.
   uint4 f[NF], add[4];
   auto load = [&](int tl) {
     const char* src = reinterpret_cast<const char*>(a.fx + (int64_t)tl * NF * 64);
@@ -681,8 +687,9 @@ __device__ __forceinline__ void route_dx(const RouteBwdArgs& a, int item,
         wf[q][r] = *reinterpret_cast<const float4*>(w + (int64_t)e * a.H + cg * 64 +
                                                     4 * (n >> 2) + 16 * (n & 3));
     }
-  // a tile's loads go out before the products of the tile before it: loads and
-  // stores retire in one order, so they wait for the stores of the one before that
+  // A tile's loads go out before the products of the tile before it.  Loads and
+  // stores retire in one order, and both are conditional: the wait for a tile is
+  // for all that is out, the next tile's loads and earlier stores included.
   struct Tile {
     float4 d[MT], add[4];
   } b0, b1;

@@ -219,9 +219,9 @@ def _pack(v):
     f = torch.nn.functional.pad(v.float(), (0, blocks * BLOCK - cols))
     f = f.view(*v.shape[:-1], blocks, BLOCK)
     top = f.abs().amax(-1, keepdim=True)
-    inv = torch.where(top >= SMALL, 127 / top.double(), torch.zeros_like(top, dtype=torch.float64))
-    codes = (f * inv).round().to(torch.int8)
-    scale = torch.where(top >= SMALL, top.double() / 127, torch.zeros_like(inv)).float()
+    live, wide = top >= SMALL, top.double()
+    codes = torch.where(live, (f.double() * 127 / wide).round(), 0.0).to(torch.int8)
+    scale = torch.where(live, wide / 127, 0.0).float()
     return codes.view(*v.shape[:-1], -1)[..., :cols].contiguous(), scale[..., 0].contiguous()
 
 
@@ -283,10 +283,10 @@ def _exact8(v):
     out = torch.zeros_like(v)
     for c in range(0, v.shape[-1], BLOCK):
         b = v[..., c:c + BLOCK]
-        step = b.abs().amax(-1, keepdim=True) / 127
-        live = step * 127 >= SMALL
-        q = torch.round(b / torch.where(live, step, torch.ones_like(step)))
-        out[..., c:c + BLOCK] = torch.where(live, q * step, torch.zeros_like(b))
+        top = b.abs().amax(-1, keepdim=True)
+        live = top >= SMALL
+        q = torch.round(b * 127 / torch.where(live, top, torch.ones_like(top)))
+        out[..., c:c + BLOCK] = torch.where(live, q * top / 127, torch.zeros_like(b))
     return out
 
 

@@ -88,6 +88,9 @@ typedef enum {
 
 typedef enum { MOE_UP_DENSE = 0, MOE_UP_INT2_G64 = 1 } moe_up_format_t;
 
+/* How moe_expert_ffn_train keeps gate and up for its backward pass. */
+typedef enum { MOE_KEEP_ROWS = 0, MOE_KEEP_INT8 = 1 } moe_keep_t;
+
 /* Storage of the routed and shared expert matrices (w_gate, w_up, w_down,
  * ws_gate, ws_up, ws_down).  The router, prefetch router, shared gate, LoRE
  * factors and FloE tensors are row-major in either case.
@@ -512,6 +515,80 @@ moe_status_t moe_distill_topk(int32_t T, int32_t V, int64_t ld, int32_t K, const
                               const float* token_w_opt, float temperature, float scale,
                               float* loss, void* dstudent_opt, void* ws, size_t ws_bytes,
                               void* stream);
+
+/* ---- Training: the experts' gated feed-forward block, rows kept in 8 bits
+ *
+ * The rules at the head of the training section hold here too: no output may
+ * overlap another buffer of the call (MOE_EINVAL), sums run in fp32 in a fixed
+ * order, results are bitwise reproducible and depend on no state between
+ * calls, and two captured graphs need a workspace each when they can run at
+ * the same time.
+ *
+ * Pairs are moe_permute's: expert_offsets [E+1], perm [T*k], row p of a sorted
+ * buffer belongs to pair perm[p] of token perm[p] / k.  Rows from
+ * expert_offsets[E] on are neither read nor written.  The experts' rows and
+ * gradients go in and out as moe_undispatch and moe_undispatch_backward have
+ * them: y_perm to moe_undispatch with the slot weights, dy_perm from its
+ * backward, dx_perm back to the tokens by moe_undispatch without weights.
+ * Shared experts are a call of their own with n_experts = top_k = 1, offsets
+ * 0 and T and perm 0..T-1.
+ * w: w_gate, w_up [E][I][H] and w_down [E][H][I] of dims.dtype (the others may
+ * be NULL); MOE_UP_DENSE and MOE_LAYOUT_ROWS only.
+ * Limits: T <= 2^22, T * k * max(H, 2 I) < 2^31, H and I <= 2^20.
+ * A bf16 layer rounds SiLU(g) u (and, backward, the gradients of g and u) to
+ * bf16 for the products that follow, which sum in fp32. */
+
+/* Rows kept in 8 bits: blocks of 64 columns of a row (the last may be
+ * shorter) with scale = top / 127, top the block's largest |value|; a value is
+ * code * scale with code the nearest of -127..127 (ties to even).  A block
+ * with top < 2^-100 is kept as zeros; one that holds an infinity or a NaN
+ * comes back as NaN throughout (scale NaN, codes 0).
+ *   src, dst: rows of cols elements of dtype, ld from one to the next (ld >=
+ *     cols; what lies between is neither read nor written).
+ *   codes [rows][cols] int8, scale [rows][ceil(cols / 64)] fp32.
+ * Limits: cols <= 2^24, ld <= 2^31, rows and rows * ceil(cols / 64) < 2^28.
+ * rows = 0 enqueues nothing. */
+moe_status_t moe_rows_pack8(int64_t rows, int64_t cols, int64_t ld, const void* src,
+                            moe_dtype_t dtype, int8_t* codes, float* scale, void* stream);
+moe_status_t moe_rows_unpack8(int64_t rows, int64_t cols, int64_t ld, const int8_t* codes,
+                              const float* scale, void* dst, moe_dtype_t dtype, void* stream);
+
+/* Bytes of workspace moe_expert_ffn_train and moe_expert_ffn_backward need,
+ * with T tokens or fewer (host output). */
+moe_status_t moe_expert_ffn_train_size(const moe_dims_t* dims, int32_t T, size_t* bytes /* host */);
+
+/* Forward: g = x W_g^T, u = x W_u^T, y_perm = (SiLU(g) u) W_d^T for every pair.
+ *   y_perm [T*k][H] dtype.
+ *   kept: MOE_KEEP_ROWS: [T*k][2][I] dtype, a pair's g and then its u (rounded
+ *     once), kept_scale_opt NULL.  MOE_KEEP_INT8: the same [2*T*k] rows of I
+ *     columns in 8 bits as moe_rows_pack8 has them (but for which of two codes
+ *     is nearer, decided in fp32), kept_scale_opt [T*k][2][ceil(I / 64)].
+ * The product itself takes g and u in fp32.  T = 0 enqueues nothing. */
+moe_status_t moe_expert_ffn_train(const moe_dims_t* dims, int32_t T, const void* x,
+                                  const moe_weights_t* w, const int32_t* expert_offsets,
+                                  const int32_t* perm, moe_keep_t keep, void* kept,
+                                  float* kept_scale_opt, void* y_perm, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Backward, at the kept g and u (their values in 8 bits, if so kept):
+ *   with s = sigmoid(g), da = dy W_d:
+ *     dg = da u s (1 + g (1 - s)), du = da g s
+ *   dx_perm_opt [T*k][H] dtype = dg W_g + du W_u (needs w_gate and w_up)
+ *   dw_gate_opt, dw_up_opt [E][I][H] = dg^T x, du^T x (need x and perm)
+ *   dw_down_opt [E][H][I] = dy^T (g s u)
+ * any of which may be NULL, not all (MOE_EINVAL).  dw_dtype: dims.dtype, or
+ * MOE_F32 for a bf16 layer (MOE_EUNSUPPORTED otherwise).  accumulate_dw 1: the
+ * weights' gradients are added in fp32 to what they hold and rounded once; 0:
+ * overwritten, with zeros for an expert without pairs; any other value is
+ * MOE_EINVAL.  T = 0 clears them unless they accumulate, and looks at no other
+ * buffer. */
+moe_status_t moe_expert_ffn_backward(const moe_dims_t* dims, int32_t T, const void* x_opt,
+                                     const moe_weights_t* w, const int32_t* expert_offsets,
+                                     const int32_t* perm_opt, moe_keep_t keep, const void* kept,
+                                     const float* kept_scale_opt, const void* dy_perm,
+                                     void* dx_perm_opt, void* dw_gate_opt, void* dw_up_opt,
+                                     void* dw_down_opt, moe_dtype_t dw_dtype, int32_t accumulate_dw,
+                                     void* ws, size_t ws_bytes, void* stream);
 
 /* ---- Exact execution of missed experts on the host or after a fetch ------
  * [SPICE page, "CPU-GPU collaboration: handling prefetch misses", cost rule

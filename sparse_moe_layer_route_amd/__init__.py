@@ -12,4 +12,6 @@ from .binding import (  # noqa: F401
     moe_host_expert_ffn, moe_layer_forward_offload,
     moe_dispatch, moe_undispatch, moe_undispatch_backward, moe_route_backward_size,
     moe_route_backward, moe_distill_topk_size, moe_distill_topk,
+    moe_expert_ffn_train_size, moe_expert_ffn_train, moe_expert_ffn_backward,
+    moe_rows_pack8, moe_rows_unpack8,
 )

@@ -21,6 +21,8 @@ MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
 MODES = {"standard": 0, "lore": 1, "stall_free": 2, "floe": 3}
 MOE_UP_DENSE, MOE_UP_INT2_G64 = 0, 1
+MOE_KEEP_ROWS, MOE_KEEP_INT8 = 0, 1
+KEEP_BLOCK = 64                      # columns that share a scale in 8 bits
 LAYOUTS = {"rows": 0, "mfma16": 1}
 
 
@@ -116,6 +118,12 @@ def _load():
         "moe_distill_topk_size": ([I32, I32, ctypes.POINTER(SZ)], ctypes.c_int),
         "moe_distill_topk": ([I32, I32, I64, I32, P, ctypes.c_int, P, P, P, P, ctypes.c_float,
                               ctypes.c_float, P, P, P, SZ, P], ctypes.c_int),
+        "moe_expert_ffn_train_size": ([D, I32, ctypes.POINTER(SZ)], ctypes.c_int),
+        "moe_expert_ffn_train": ([D, I32, P, Wp, P, P, ctypes.c_int, P, P, P, P, SZ, P], ctypes.c_int),
+        "moe_expert_ffn_backward": ([D, I32, P, Wp, P, P, ctypes.c_int, P, P, P, P, P, P, P,
+                                     ctypes.c_int, I32, P, SZ, P], ctypes.c_int),
+        "moe_rows_pack8": ([I64, I64, I64, P, ctypes.c_int, P, P, P], ctypes.c_int),
+        "moe_rows_unpack8": ([I64, I64, I64, P, P, P, ctypes.c_int, P], ctypes.c_int),
         "moe_offload_plan": ([D, P, P, ctypes.POINTER(MoeOffloadCost), P], ctypes.c_int),
         "moe_offload_workspace_size": ([D, I32, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
                                        ctypes.c_int),
@@ -139,7 +147,9 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_workspace_size", "moe_r
             "moe_lore_fit_size", "moe_lore_fit", "moe_expert_ffn", "moe_lore_surrogate",
             "moe_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_dispatch",
             "moe_undispatch", "moe_undispatch_backward", "moe_route_backward_size",
-            "moe_route_backward", "moe_distill_topk_size", "moe_distill_topk", "moe_offload_plan",
+            "moe_route_backward", "moe_distill_topk_size", "moe_distill_topk",
+            "moe_expert_ffn_train_size", "moe_expert_ffn_train", "moe_expert_ffn_backward",
+            "moe_rows_pack8", "moe_rows_unpack8", "moe_offload_plan",
             "moe_offload_workspace_size", "moe_host_ffn_workspace_size", "moe_host_expert_ffn",
             "moe_layer_forward_offload")
 
@@ -548,6 +558,108 @@ def moe_distill_topk(T, V, K, student, teacher_ids, teacher_logits, loss, dstude
         _arg(dev, "token_w", token_w, T, torch.float32, True), float(temperature), float(scale),
         _arg(dev, "loss", loss, T, torch.float32), _arg(dev, "dstudent", dstudent, n, student.dtype, True, ds_row),
         ws_p, ws_n, _stream(stream, dev)), "moe_distill_topk")
+
+
+def moe_expert_ffn_train_size(dims, T) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_expert_ffn_train_size(ctypes.byref(_dims(dims)), T, ctypes.byref(n)),
+           "moe_expert_ffn_train_size")
+    return n.value
+
+
+def _train_weights(dev, d, w, dt, names=("w_gate", "w_up", "w_down")):
+    """The experts' matrices as a struct; `names` are required."""
+    if isinstance(w, MoeWeights):
+        return w
+    n, st = d.n_experts * d.inter * d.hidden, MoeWeights()
+    st.w_gate = _arg(dev, "w_gate", w.get("w_gate"), n, dt, "w_gate" not in names)
+    st.w_up = _arg(dev, "w_up", w.get("w_up"), n, dt, "w_up" not in names)
+    st.w_down = _arg(dev, "w_down", w.get("w_down"), n, dt, "w_down" not in names)
+    return st
+
+
+def _kept(dev, d, P, dt, kept, kept_scale):
+    """(moe_keep_t, address, scales' address) of what is kept: 8 bits where
+    there are scales."""
+    n, rows = P * 2 * d.inter, d.inter if P else 0
+    if kept_scale is None:
+        return MOE_KEEP_ROWS, _arg(dev, "kept", kept, n, dt, row=rows), None
+    blocks = -(-d.inter // KEEP_BLOCK)
+    return (MOE_KEEP_INT8, _arg(dev, "kept", kept, n, torch.int8, row=rows),
+            _arg(dev, "kept_scale", kept_scale, P * 2 * blocks, torch.float32, row=blocks if P else 0))
+
+
+def moe_expert_ffn_train(dims, T, x, weights, expert_offsets, perm, y_perm, kept, ws,
+                         kept_scale=None, stream=None):
+    """weights: a dict with w_gate, w_up and w_down, or a MoeWeights.  kept: rows
+    of the layer's type, or int8 where kept_scale is given."""
+    d, dev = _dims(dims), _device(stream)
+    dt, P, H = _TORCH_DTYPES[d.dtype], T * d.top_k, d.hidden
+    keep, kept_p, scale_p = _kept(dev, d, P, dt, kept, kept_scale)
+    ws_p, ws_n = _ws(dev, ws)
+    _check(_lib.moe_expert_ffn_train(
+        ctypes.byref(d), T, _arg(dev, "x", x, T * H, dt),
+        ctypes.byref(_train_weights(dev, d, weights, dt)),
+        _arg(dev, "expert_offsets", expert_offsets, d.n_experts + 1, torch.int32),
+        _arg(dev, "perm", perm, P, torch.int32), keep, kept_p, scale_p,
+        _arg(dev, "y_perm", y_perm, P * H, dt), ws_p, ws_n, _stream(stream, dev)),
+        "moe_expert_ffn_train")
+
+
+def moe_expert_ffn_backward(dims, T, x, weights, expert_offsets, perm, kept, dy_perm, dx_perm,
+                            dw_gate, dw_up, dw_down, ws, kept_scale=None, accumulate_dw=False,
+                            stream=None):
+    """Any of dx_perm, dw_gate, dw_up and dw_down may be None; the last three are
+    of the layer's type, or all float32.  x and perm are needed for dw_gate and
+    dw_up, w_gate and w_up for dx_perm."""
+    d, dev = _dims(dims), _device(stream)
+    dt, P, H = _TORCH_DTYPES[d.dtype], T * d.top_k, d.hidden
+    dws = [t for t in (dw_gate, dw_up, dw_down) if t is not None]
+    dwt, n = dws[0].dtype if dws else dt, d.n_experts * d.inter * H
+    if dwt not in _MOE_DTYPES:
+        raise TypeError(f"expected float32 or bfloat16 gradients, got {dwt}")
+    keep, kept_p, scale_p = _kept(dev, d, P, dt, kept, kept_scale)
+    ws_p, ws_n = _ws(dev, ws)
+    names = ("w_gate", "w_up", "w_down") if dx_perm is not None else ("w_down",)
+    _check(_lib.moe_expert_ffn_backward(
+        ctypes.byref(d), T, _arg(dev, "x", x, T * H, dt, True),
+        ctypes.byref(_train_weights(dev, d, weights, dt, names)),
+        _arg(dev, "expert_offsets", expert_offsets, d.n_experts + 1, torch.int32),
+        _arg(dev, "perm", perm, P, torch.int32, True), keep, kept_p, scale_p,
+        _arg(dev, "dy_perm", dy_perm, P * H, dt), _arg(dev, "dx_perm", dx_perm, P * H, dt, True),
+        _arg(dev, "dw_gate", dw_gate, n, dwt, True), _arg(dev, "dw_up", dw_up, n, dwt, True),
+        _arg(dev, "dw_down", dw_down, n, dwt, True), _MOE_DTYPES[dwt], int(accumulate_dw), ws_p, ws_n,
+        _stream(stream, dev)), "moe_expert_ffn_backward")
+
+
+def _rows8_args(dev, rows, cols, name, t, codes, scale, ld):
+    dtype, row = _row_dtype(t), 0
+    if ld is None:                   # the length of the rows' last axis
+        ld = t.shape[-1] if rows > 1 else cols
+        row = ld if rows > 1 else 0
+    ld, blocks = int(ld), -(-cols // KEEP_BLOCK)
+    n = (rows - 1) * ld + cols if rows > 0 else 0
+    return (dtype, ld, _arg(dev, name, t, n, t.dtype, row=row),
+            _arg(dev, "codes", codes, rows * cols, torch.int8, row=cols if rows > 1 else 0),
+            _arg(dev, "scale", scale, rows * blocks, torch.float32, row=blocks if rows > 1 else 0))
+
+
+def moe_rows_pack8(rows, cols, src, codes, scale, ld=None, stream=None):
+    """ld: elements from one row of src to the next; None: the length of src's
+    last axis."""
+    dev = _device(stream)
+    dtype, ld, src_p, codes_p, scale_p = _rows8_args(dev, rows, cols, "src", src, codes, scale, ld)
+    _check(_lib.moe_rows_pack8(rows, cols, ld, src_p, dtype, codes_p, scale_p, _stream(stream, dev)),
+           "moe_rows_pack8")
+
+
+def moe_rows_unpack8(rows, cols, codes, scale, dst, ld=None, stream=None):
+    """ld: elements from one row of dst to the next; None: the length of dst's
+    last axis."""
+    dev = _device(stream)
+    dtype, ld, dst_p, codes_p, scale_p = _rows8_args(dev, rows, cols, "dst", dst, codes, scale, ld)
+    _check(_lib.moe_rows_unpack8(rows, cols, ld, codes_p, scale_p, dst_p, dtype, _stream(stream, dev)),
+           "moe_rows_unpack8")
 
 
 # ------------------------------------------------- exact miss execution --

@@ -8,10 +8,12 @@
 #include <algorithm>
 #include <chrono>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <thread>
 
 #include "common.h"
+#include "ffn_train.h"
 
 namespace moe {
 hipError_t launch_route(const moe_dims_t& d, int T, const void* x, const void* w_router,
@@ -785,6 +787,202 @@ moe_status_t moe_distill_topk(int32_t T, int32_t V, int64_t ld, int32_t K, const
   return hip_status(launch_distill(T, V, ld, K, student, dtype == MOE_BF16, teacher_ids,
                                    teacher_logits, teacher_lse_opt, token_w_opt, temperature, scale,
                                    loss, dstudent_opt, ws, (hipStream_t)stream));
+}
+
+// ---- training: the experts' gated feed-forward block, rows kept in 8 bits
+
+namespace {
+
+// Sorted rows of hidden and of 2 * inter elements are indexed below 2^31; tiles
+// of either size lie on a grid axis.
+moe_status_t check_ffn_train(const moe_dims_t* d, int32_t T) {
+  const moe_status_t st = check_dims(d);
+  if (st != MOE_OK) return st;
+  if (T < 0) return MOE_EINVAL;
+  if (d->up_format != MOE_UP_DENSE || d->weight_layout != MOE_LAYOUT_ROWS) return MOE_EUNSUPPORTED;
+  const int64_t wide = std::max<int64_t>(d->hidden, 2LL * d->inter);
+  if (d->hidden > (1 << 20) || d->inter > (1 << 20) || T > kMaxTokens ||
+      (int64_t)T * d->top_k * wide >= (int64_t(1) << 31))
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+struct Span { const void* p; size_t n; };
+
+// Whether an output shares a byte with an input or with another output.
+bool shared(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    for (const Span& r : in)
+      if (overlap(o->p, o->n, r.p, r.n)) return true;
+    for (const Span* q = out.begin(); q != o; ++q)
+      if (overlap(o->p, o->n, q->p, q->n)) return true;
+  }
+  return false;
+}
+
+// What is kept of P rows: bytes of the rows and of their scales.
+struct Kept { size_t rows, scale; int blocks; };
+Kept kept_of(const moe_dims_t& d, size_t P, moe_keep_t keep) {
+  const int blocks = (d.inter + kKeepBlock - 1) / kKeepBlock;
+  const size_t n = P * 2 * d.inter;
+  if (keep == MOE_KEEP_INT8) return {n, P * 2 * blocks * sizeof(float), blocks};
+  return {n * dtype_bytes(d.dtype), 0, blocks};
+}
+
+moe_status_t check_rows8(int64_t rows, int64_t cols, int64_t ld, moe_dtype_t dtype) {
+  if (rows < 0 || cols <= 0 || ld < cols) return MOE_EINVAL;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
+  const int64_t blocks = (cols + kKeepBlock - 1) / kKeepBlock;
+  // lanes over all blocks are counted in 32 bits by the launch
+  if (cols > (1 << 24) || ld > (int64_t(1) << 31) || rows >= (int64_t(1) << 28) ||
+      rows * blocks >= (int64_t(1) << 28))
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_expert_ffn_train_size(const moe_dims_t* dims, int32_t T, size_t* bytes) {
+  const moe_status_t st = check_ffn_train(dims, T);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_EINVAL;
+  *bytes = (size_t)train_ws_bytes(*dims, T);
+  return MOE_OK;
+}
+
+moe_status_t moe_expert_ffn_train(const moe_dims_t* dims, int32_t T, const void* x,
+                                  const moe_weights_t* w, const int32_t* expert_offsets,
+                                  const int32_t* perm, moe_keep_t keep, void* kept,
+                                  float* kept_scale_opt, void* y_perm, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  const moe_status_t st = check_ffn_train(dims, T);
+  if (st != MOE_OK) return st;
+  if (keep != MOE_KEEP_ROWS && keep != MOE_KEEP_INT8) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!w || !ok_ptr(x) || !ok_ptr(w->w_gate) || !ok_ptr(w->w_up) || !ok_ptr(w->w_down) ||
+      !ok_ptr(expert_offsets) || !ok_ptr(perm) || !ok_ptr(kept) || !ok_opt(kept_scale_opt) ||
+      !ok_ptr(y_perm) || !ok_ptr(ws))
+    return MOE_EINVAL;
+  if ((keep == MOE_KEEP_INT8) != (kept_scale_opt != nullptr)) return MOE_EINVAL;
+  const size_t b = dtype_bytes(dims->dtype), H = dims->hidden, E = dims->n_experts;
+  const size_t P = (size_t)T * dims->top_k, wb = E * dims->inter * H * b;
+  const size_t need = (size_t)train_ws_bytes(*dims, T);
+  if (ws_bytes < need) return MOE_EWORKSPACE;
+  const Kept kb = kept_of(*dims, P, keep);
+  const std::initializer_list<Span> in = {{x, T * H * b}, {w->w_gate, wb}, {w->w_up, wb}, {w->w_down, wb},
+                     {expert_offsets, (E + 1) * 4}, {perm, P * 4}};
+  const std::initializer_list<Span> out = {{kept, kb.rows}, {kept_scale_opt, kb.scale}, {y_perm, P * H * b}, {ws, need}};
+  if (shared(in, out)) return MOE_EINVAL;
+  TrainArgs a{};
+  a.x = x;
+  a.w_gate = w->w_gate;
+  a.w_up = w->w_up;
+  a.w_down = w->w_down;
+  a.offsets = expert_offsets;
+  a.perm = perm;
+  a.kept = kept;
+  a.scale = kept_scale_opt;
+  a.y = y_perm;
+  a.act = ws;
+  a.E = dims->n_experts;
+  a.H = dims->hidden;
+  a.I = dims->inter;
+  a.k = dims->top_k;
+  a.blocks = kb.blocks;
+  a.keep8 = keep == MOE_KEEP_INT8;
+  return hip_status(launch_ffn_train(a, (int)P, dims->dtype == MOE_BF16, (hipStream_t)stream));
+}
+
+moe_status_t moe_expert_ffn_backward(const moe_dims_t* dims, int32_t T, const void* x,
+                                     const moe_weights_t* w, const int32_t* expert_offsets,
+                                     const int32_t* perm, moe_keep_t keep, const void* kept,
+                                     const float* kept_scale_opt, const void* dy_perm,
+                                     void* dx_perm_opt, void* dw_gate_opt, void* dw_up_opt,
+                                     void* dw_down_opt, moe_dtype_t dw_dtype, int32_t accumulate_dw,
+                                     void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t st = check_ffn_train(dims, T);
+  if (st != MOE_OK) return st;
+  if (keep != MOE_KEEP_ROWS && keep != MOE_KEEP_INT8) return MOE_EINVAL;
+  if (dw_dtype != MOE_F32 && dw_dtype != MOE_BF16) return MOE_EINVAL;
+  if (accumulate_dw != 0 && accumulate_dw != 1) return MOE_EINVAL;
+  if (dims->dtype == MOE_F32 && dw_dtype == MOE_BF16) return MOE_EUNSUPPORTED;
+  if (!ok_opt(dx_perm_opt) || !ok_opt(dw_gate_opt) || !ok_opt(dw_up_opt) || !ok_opt(dw_down_opt))
+    return MOE_EINVAL;
+  const bool any_dw = dw_gate_opt || dw_up_opt || dw_down_opt;
+  if (!dx_perm_opt && !any_dw) return MOE_EINVAL;
+  const size_t b = dtype_bytes(dims->dtype), H = dims->hidden, E = dims->n_experts;
+  const size_t P = (size_t)T * dims->top_k, wn = E * dims->inter * H;
+  const size_t db = wn * dtype_bytes(dw_dtype), need = (size_t)train_ws_bytes(*dims, T);
+  const Kept kb = kept_of(*dims, P, keep);
+  TrainArgs a{};
+  a.dw[0] = dw_gate_opt;
+  a.dw[1] = dw_up_opt;
+  a.dw[2] = dw_down_opt;
+  a.dw_f32 = dw_dtype == MOE_F32;
+  a.accumulate = accumulate_dw;
+  a.E = dims->n_experts;
+  a.H = dims->hidden;
+  a.I = dims->inter;
+  a.k = dims->top_k;
+  a.blocks = kb.blocks;
+  a.keep8 = keep == MOE_KEEP_INT8;
+  if (T == 0) {  // empty sums
+    if (shared({}, {{a.dw[0], db}, {a.dw[1], db}, {a.dw[2], db}})) return MOE_EINVAL;
+    if (!any_dw || accumulate_dw) return MOE_OK;
+    return hip_status(launch_ffn_backward(a, 0, dims->dtype == MOE_BF16, (hipStream_t)stream));
+  }
+  if (!w || !ok_opt(x) || !ok_opt(w->w_gate) || !ok_opt(w->w_up) || !ok_ptr(w->w_down) ||
+      !ok_ptr(expert_offsets) || !ok_opt(perm) || !ok_ptr(kept) || !ok_opt(kept_scale_opt) ||
+      !ok_ptr(dy_perm) || !ok_ptr(ws))
+    return MOE_EINVAL;
+  if ((keep == MOE_KEEP_INT8) != (kept_scale_opt != nullptr)) return MOE_EINVAL;
+  if (dx_perm_opt && (!w->w_gate || !w->w_up)) return MOE_EINVAL;
+  if ((dw_gate_opt || dw_up_opt) && (!x || !perm)) return MOE_EINVAL;
+  if (ws_bytes < need) return MOE_EWORKSPACE;
+  const std::initializer_list<Span> in = {{x, T * H * b},   {w->w_gate, wn * b},         {w->w_up, wn * b},
+                     {w->w_down, wn * b}, {expert_offsets, (E + 1) * 4}, {perm, P * 4},
+                     {kept, kb.rows},  {kept_scale_opt, kb.scale},  {dy_perm, P * H * b}};
+  const std::initializer_list<Span> out = {{dx_perm_opt, P * H * b}, {a.dw[0], db}, {a.dw[1], db}, {a.dw[2], db}, {ws, need}};
+  if (shared(in, out)) return MOE_EINVAL;
+  a.x = x;
+  a.w_gate = w->w_gate;
+  a.w_up = w->w_up;
+  a.w_down = w->w_down;
+  a.dy = dy_perm;
+  a.offsets = expert_offsets;
+  a.perm = perm;
+  a.kept = const_cast<void*>(kept);
+  a.scale = const_cast<float*>(kept_scale_opt);
+  a.dx = dx_perm_opt;
+  a.act = ws;
+  a.dgu = (char*)ws + P * dims->inter * b;
+  return hip_status(launch_ffn_backward(a, (int)P, dims->dtype == MOE_BF16, (hipStream_t)stream));
+}
+
+moe_status_t moe_rows_pack8(int64_t rows, int64_t cols, int64_t ld, const void* src,
+                            moe_dtype_t dtype, int8_t* codes, float* scale, void* stream) {
+  const moe_status_t st = check_rows8(rows, cols, ld, dtype);
+  if (st != MOE_OK || rows == 0) return st;
+  if (!ok_ptr(src) || !ok_ptr(codes) || !ok_ptr(scale)) return MOE_EINVAL;
+  const size_t n = rows, c = cols, blocks = (c + kKeepBlock - 1) / kKeepBlock;
+  const std::initializer_list<Span> in = {{src, ((n - 1) * ld + c) * dtype_bytes(dtype)}};
+  const std::initializer_list<Span> out = {{codes, n * c}, {scale, n * blocks * 4}};
+  if (shared(in, out)) return MOE_EINVAL;
+  return hip_status(launch_rows_pack8(rows, cols, ld, src, dtype == MOE_BF16, codes, scale,
+                                      (hipStream_t)stream));
+}
+
+moe_status_t moe_rows_unpack8(int64_t rows, int64_t cols, int64_t ld, const int8_t* codes,
+                              const float* scale, void* dst, moe_dtype_t dtype, void* stream) {
+  const moe_status_t st = check_rows8(rows, cols, ld, dtype);
+  if (st != MOE_OK || rows == 0) return st;
+  if (!ok_ptr(dst) || !ok_ptr(codes) || !ok_ptr(scale)) return MOE_EINVAL;
+  const size_t n = rows, c = cols, blocks = (c + kKeepBlock - 1) / kKeepBlock;
+  const std::initializer_list<Span> in = {{codes, n * c}, {scale, n * blocks * 4}};
+  const std::initializer_list<Span> out = {{dst, ((n - 1) * ld + c) * dtype_bytes(dtype)}};
+  if (shared(in, out)) return MOE_EINVAL;
+  return hip_status(launch_rows_unpack8(rows, cols, ld, codes, scale, dst, dtype == MOE_BF16,
+                                        (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -888,6 +888,7 @@ moe_status_t moe_expert_ffn_train(const moe_dims_t* dims, int32_t T, const void*
   a.H = dims->hidden;
   a.I = dims->inter;
   a.k = dims->top_k;
+  a.pairs = (int)P;
   a.blocks = kb.blocks;
   a.keep8 = keep == MOE_KEEP_INT8;
   return hip_status(launch_ffn_train(a, (int)P, dims->dtype == MOE_BF16, (hipStream_t)stream));
@@ -924,6 +925,7 @@ moe_status_t moe_expert_ffn_backward(const moe_dims_t* dims, int32_t T, const vo
   a.H = dims->hidden;
   a.I = dims->inter;
   a.k = dims->top_k;
+  a.pairs = (int)P;
   a.blocks = kb.blocks;
   a.keep8 = keep == MOE_KEEP_INT8;
   if (T == 0) {  // empty sums

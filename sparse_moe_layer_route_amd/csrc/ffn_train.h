@@ -13,8 +13,9 @@ struct TrainArgs {
   void *y, *dx;      // [P][H]
   void* dw[3];       // gate, up [E][I][H]; down [E][H][I]
   void *act, *dgu;   // workspace: SiLU(g) u [P][I]; dg and du [P][2][I]
-  int E, H, I, k, blocks;
+  int E, H, I, k, blocks, pairs;   // pairs: T * k
   int keep8, dw_f32, accumulate;
+  int n_dw, dw_list; // the matrices whose gradients are asked for: how many, 2 bits each
 };
 
 // ------------------------------------------------- rows kept in 8 bits ----
@@ -59,6 +60,7 @@ __device__ __forceinline__ void gated_grad(float g, float u, float da, float& a,
   dg = da * u * (s * (1.0f + (g - gs)));
 }
 
+hipError_t launch_train_gemm(int mode, const TrainArgs& a, int P, hipStream_t s);
 int64_t train_ws_bytes(const moe_dims_t& d, int64_t T);
 hipError_t launch_ffn_train(const TrainArgs& a, int P, bool is_bf16, hipStream_t s);
 hipError_t launch_ffn_backward(const TrainArgs& a, int P, bool is_bf16, hipStream_t s);

@@ -341,7 +341,14 @@ __global__ void __launch_bounds__(256) train_dw_kernel(TrainArgs a) {
 
 }  // namespace
 
+// Rows enough for the 256 x 256 tiles of ffn_train_gemm.hip.
+static bool large(const TrainArgs& a, int P) { return P >= 64 * a.E && a.I >= 128 && a.H >= 128; }
+
 template <typename T> static hipError_t forward(const TrainArgs& a, int P, hipStream_t s) {
+  if (sizeof(T) == 2 && large(a, P)) {
+    const hipError_t e = launch_train_gemm(0, a, P, s);
+    return e != hipSuccess ? e : launch_train_gemm(1, a, P, s);
+  }
   const int tiles = P / TN + std::min(a.E, P);
   train_gate_up_kernel<T><<<dim3(tiles, (a.I + TM - 1) / TM), 256, 0, s>>>(a);
   train_down_kernel<T><<<dim3(tiles, a.H / TM), 256, 0, s>>>(a);
@@ -349,6 +356,11 @@ template <typename T> static hipError_t forward(const TrainArgs& a, int P, hipSt
 }
 
 template <typename T> static hipError_t backward(const TrainArgs& a, int P, hipStream_t s) {
+  if (sizeof(T) == 2 && P > 0 && large(a, P)) {
+    hipError_t e = launch_train_gemm(2, a, P, s);
+    if (e == hipSuccess && a.dx) e = launch_train_gemm(3, a, P, s);
+    return e != hipSuccess ? e : launch_train_gemm(4, a, P, s);
+  }
   const int tiles = P / TN + std::min(a.E, P);
   const int hi = a.H / TM, ii = (a.I + TM - 1) / TM;
   if (P > 0) {

@@ -1,0 +1,468 @@
+// The products of the experts' training on the matrix cores, bf16, for
+// experts with many rows: 256 x 256 outputs a block, v_mfma_f32_16x16x32_bf16.
+//
+//   C[n][m] = sum_k A[m][k] B[n][k], m the fast axis of the output
+//
+//   GATE_UP  m: 128 channels of W_g and of W_u   n: token rows    k: H
+//   DOWN     m: H (W_d)                          n: token rows    k: I
+//   DACT     m: I (W_d turned)                   n: token rows    k: H
+//   DX       m: H (W_g, then W_u, turned)        n: token rows    k: I, twice
+//   DW       m: H (x) or I (a), both turned      n: I (dg, du) or H (dy), turned; k: the expert's rows
+//
+// Four waves, one a SIMD, of 128 x 128 outputs each (256 accumulators a lane):
+// per 32 k a wave reads 16 fragments from LDS for 64 matrix instructions, a
+// quarter less LDS traffic than eight waves of 128 x 64 would need, and LDS
+// reads and the arriving tiles share its 128 bytes a cycle.  Stages of 32 k
+// (32 KiB) go from memory to LDS directly into a ring of four; three are in
+// flight while a wave's fragments for the next stage are read beside the
+// matrix instructions of the present one.  An operand whose k is its fast
+// axis lies in LDS by rows of 64 bytes, 16-byte chunk c of row r at c ^ (r / 2
+// % 4); one whose k is the slow axis by rows of 256 outputs (512 bytes),
+// 32-byte chunk p of row k at p ^ (k % 4 + 4 (k / 8 % 2)), and is turned on
+// its way to the registers by the transposing LDS read.  Either way the lanes
+// that LDS serves together cover all its banks.
+//
+// Blocks are persistent: the stages of a block's tiles form one stream, so the
+// next tile's first stages load while the present one's outputs are formed.
+#include <algorithm>
+
+#include "common.h"
+#include "ffn_train.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// GATE_UP8, DACT8: gate and up kept in 8 bits; DW_ANY: gradients of the
+// weights in fp32, or added to what is there
+enum { GATE_UP, GATE_UP8, DOWN, DACT, DACT8, DX, DW, DW_ANY };
+
+constexpr int TILE = 256;           // outputs of a block along m and along n
+constexpr int HALF_SLOT = 16384;    // an operand's stage: 256 outputs x 32 k
+constexpr int SLOT = 2 * HALF_SLOT;
+constexpr int RING = 4;
+constexpr int STAGING = 6144;       // a wave's: three pieces of 16 rows x 64 bf16
+constexpr int NXCD = 8;
+constexpr int CUS = 256;
+constexpr int MAX_TILES = 8;        // tiles of a block whose token rows are looked up ahead
+
+__device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
+
+// 16 bytes a lane from `from` to LDS, lane l at `to` + 16 l.  Outside the
+// compiler's wait counting (it would drain all loads before the next LDS
+// read): landing is waited for by count, below.  M0, which holds the LDS
+// address, is reserved to such code: nothing else in these kernels uses it.
+__device__ __forceinline__ void dma16(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               : : "v"(from), "s"(to) : "memory");
+}
+template <int N> __device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+typedef __attribute__((address_space(3))) u32x4 lds16_t;
+typedef __attribute__((address_space(3))) u32x2 lds8_t;
+typedef __attribute__((address_space(3))) uint32_t lds4_t;
+typedef __attribute__((address_space(3))) s16x4 lds_turn_t;
+
+__device__ __forceinline__ u32x4 read16(uint32_t at) { return *(const lds16_t*)(uintptr_t)at; }
+__device__ __forceinline__ u32x2 read8(uint32_t at) { return *(const lds8_t*)(uintptr_t)at; }
+__device__ __forceinline__ void write8(uint32_t at, uint32_t lo, uint32_t hi) {
+  *(lds8_t*)(uintptr_t)at = u32x2{lo, hi};
+}
+// Rows k..k+3 and k+4..k+7 (512 bytes apart) of 16 outputs: this lane's output, its 8 k.
+__device__ __forceinline__ bf16x8_t read_turned(uint32_t at) {
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_turn_t*)(uintptr_t)at);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_turn_t*)(uintptr_t)(at + 2048));
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// An accumulator where it is used: left to itself the compiler moves all 256
+// to the other half of the register file at once and spills.  The matrix
+// instructions before it have ended (matrix_done).
+__device__ __forceinline__ float acc_read(float v) {
+  float r;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(r) : "a"(v));
+  return r;
+}
+__device__ __forceinline__ void acc_read4(const f32x4_t& v, float (&r)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) r[q] = acc_read(v[q]);
+}
+__device__ __forceinline__ void matrix_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+// One tile of the launch: expert, its first row and rows, n and m origins, and
+// for DW which matrix.
+struct Meta { int e, start, n, n0, m0, which; };
+
+template <int MODE>
+__global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
+  constexpr bool GU = MODE == GATE_UP || MODE == GATE_UP8, DA = MODE == DACT || MODE == DACT8;
+  constexpr bool DWS = MODE == DW || MODE == DW_ANY;
+  constexpr bool AT = DA || MODE == DX || DWS, BT = DWS;   // operands whose k is the slow axis
+  __shared__ __attribute__((aligned(1024))) char ring[RING * SLOT];
+  __shared__ __attribute__((aligned(16))) char staging[4][STAGING];
+  __shared__ int token[GU ? MAX_TILES : 1][GU ? TILE : 1];
+
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, kg = lane >> 4;
+  const int H = a.H, I = a.I;
+
+  // ---- this block's tiles: its XCD's share, every nbx-th ------------------
+  const int tiles_m = GU ? (I + 127) / 128 : DA ? (I + TILE - 1) / TILE : (H + TILE - 1) / TILE;
+  const int per_matrix = DWS ? ((H + TILE - 1) / TILE) * ((I + TILE - 1) / TILE) : 0;
+  int off = 0, cnt = 0;
+  if (lane < a.E) {
+    off = a.offsets[lane];
+    cnt = a.offsets[lane + 1] - off;
+  }
+  const int mine = lane < a.E ? (DWS ? per_matrix * a.n_dw : (cnt + TILE - 1) / TILE * tiles_m) : 0;
+  const int incl = wave_incl_scan_i(mine);
+  const int total = __builtin_amdgcn_readlane(incl, 63);
+  const int nbx = gridDim.x / NXCD, xcd = blockIdx.x % NXCD, bi = blockIdx.x / NXCD;
+  const int per_x = (total + NXCD - 1) / NXCD;
+  const int first = xcd * per_x + bi, past = min(total, (xcd + 1) * per_x);
+  if (first >= past) return;
+  const int n_my = (past - first + nbx - 1) / nbx;
+
+  auto decode = [&](int j) __attribute__((always_inline)) {
+    const int t = first + j * nbx;
+    const uint64_t in = __ballot(t >= incl - mine && t < incl);
+    Meta m;
+    m.e = __builtin_ctzll(in);
+    const int r = t - (__builtin_amdgcn_readlane(incl, m.e) - __builtin_amdgcn_readlane(mine, m.e));
+    m.start = __builtin_amdgcn_readlane(off, m.e);
+    m.n = __builtin_amdgcn_readlane(cnt, m.e);
+    if constexpr (DWS) {
+      const int w = r / per_matrix, q = r % per_matrix;
+      m.which = (a.dw_list >> (2 * w)) & 3;
+      const int nm = ((m.which == 2 ? I : H) + TILE - 1) / TILE;
+      m.m0 = q % nm * TILE;
+      m.n0 = q / nm * TILE;
+    } else {
+      m.which = 0;
+      m.m0 = r % tiles_m * (GU ? 128 : TILE);
+      m.n0 = r / tiles_m * TILE;
+    }
+    return m;
+  };
+  if (GU) {
+    for (int j = 0; j < n_my; ++j) {
+      const Meta m = decode(j);
+      const int row = min(m.n0 + (int)threadIdx.x, m.n - 1);
+      token[j][threadIdx.x] = a.perm[m.start + row] / a.k;
+    }
+    __syncthreads();
+  }
+  // pairs of stages of a tile (DX: of each of its two halves)
+  const int pairs_i = (I + 63) / 64;
+  auto pairs_of = [&](const Meta& m) __attribute__((always_inline)) {
+    return DWS ? max(1, (m.n + 63) / 64) : MODE == DX ? 2 * pairs_i : MODE == DOWN ? pairs_i : H / 64;
+  };
+  // stages of kept rows that follow a tile's own (DACT)
+  constexpr int EXTRA = MODE == DACT ? 8 : MODE == DACT8 ? 4 : 0;
+
+  // ---- loading stream -----------------------------------------------------
+  // Wave w moves, of either operand, rows 64 w..+63 (k fast) or k 8 w..+7 (k
+  // slow) of a stage, four instructions of 1 KiB.  The stream's position is a
+  // pair of stages of a tile; it ends with the block's last tile.
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&ring[0];
+  int dj = 0, dpair = 0, dpairs;
+  bool more = true;
+  Meta dm = decode(0);
+  const char* pa[4];                   // this lane's next 16 bytes, by instruction
+  const char* pb[4];                   // (DW's pa: its column, the rows being looked up)
+  int64_t step_a = 0, step_b = 0;
+  const int kchunk = (lane & 3) ^ ((lane >> 3) & 3);    // k fast: the 16-byte chunk this lane moves
+  const int slow_k0 = 8 * wv + (lane >> 5);             // k slow: row (+ 2 q) this lane moves
+  auto slow_col = [&](int q) __attribute__((always_inline)) {
+    const int k = slow_k0 + 2 * q, f = (k & 3) | (((k >> 3) & 1) << 2);
+    return 16 * (((lane & 31) >> 1) ^ f) + 8 * (lane & 1);
+  };
+  // DW: x's rows of a stage are looked up through scalar loads a stage ahead
+  const __attribute__((address_space(4))) int32_t* perm_s =
+      (const __attribute__((address_space(4))) int32_t*)(uintptr_t)a.perm;
+  // p / k, p < 2^25: the high word of p ceil(2^32 / k)
+  const uint32_t per_k = (uint32_t)(((1ull << 32) + a.k - 1) / a.k);
+  int rows[8];
+  auto look_up = [&](int stage) __attribute__((always_inline)) {
+    if (!DWS) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = min(dm.start + 32 * stage + 8 * wv + i, a.pairs - 1);
+      const uint32_t t = (uint32_t)perm_s[p];
+      rows[i] = dm.which == 2 ? p : (int)(a.k == 1 ? t : __umulhi(t, per_k));
+    }
+  };
+  auto set_tile = [&]() __attribute__((always_inline)) {
+    const int64_t we = (int64_t)dm.e * I * H;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = 64 * wv + 16 * q + (lane >> 2);       // k fast: row of the tile
+      const int64_t k = slow_k0 + 2 * q;
+      const int row = min(dm.n0 + r, dm.n - 1);
+      if (GU) {
+        const int ch = min(dm.m0 + (r >> 7) * 64 + (r & 63), I - 1);
+        pa[q] = (const char*)((const bf16*)((r >> 6) & 1 ? a.w_up : a.w_gate) + we + (int64_t)ch * H + 8 * kchunk);
+        pb[q] = (const char*)((const bf16*)a.x + (int64_t)token[dj][r] * H + 8 * kchunk);
+      } else if (MODE == DOWN) {
+        pa[q] = (const char*)((const bf16*)a.w_down + we + (int64_t)min(dm.m0 + r, H - 1) * I + 8 * kchunk);
+        pb[q] = (const char*)((const bf16*)a.act + (int64_t)(dm.start + row) * I + 8 * kchunk);
+      } else if (DA) {
+        pa[q] = (const char*)((const bf16*)a.w_down + we + k * I + min(dm.m0 + slow_col(q), I - 8));
+        pb[q] = (const char*)((const bf16*)a.dy + (int64_t)(dm.start + row) * H + 8 * kchunk);
+      } else if (MODE == DX) {
+        const bool up = dpair >= pairs_i;                 // on to W_u and du
+        pa[q] = (const char*)((const bf16*)(up ? a.w_up : a.w_gate) + we + k * H + min(dm.m0 + slow_col(q), H - 8));
+        pb[q] = (const char*)((const bf16*)a.dgu + ((int64_t)(dm.start + row) * 2 + up) * I + 8 * kchunk);
+      } else {
+        const bool down = dm.which == 2;
+        const int M = down ? I : H, N = down ? H : I;
+        pa[q] = (const char*)((const bf16*)(down ? a.act : a.x) + min(dm.m0 + slow_col(q), M - 8));
+        pb[q] = (const char*)((const bf16*)(down ? a.dy : a.dgu) +
+                              (int64_t)(dm.start + k) * (down ? H : 2 * I) + (down ? 0 : dm.which * I) +
+                              min(dm.n0 + slow_col(q), N - 8));
+      }
+    }
+    step_a = !AT ? 64 : DWS ? 2 * (int64_t)(dm.which == 2 ? I : H) : 64 * (int64_t)(MODE == DX ? H : I);
+    step_b = !BT ? 64 : 64 * (int64_t)(dm.which == 2 ? H : 2 * I);
+    dpairs = pairs_of(dm);
+  };
+  auto load_a = [&](uint32_t slot, int stage) __attribute__((always_inline)) {
+    const uint32_t to = ring0 + slot + 4096 * wv;
+    const int k0 = 32 * (MODE == DX && stage >= 2 * pairs_i ? stage - 2 * pairs_i : stage);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const char* p = pa[q];
+      if (DWS) p += (int64_t)(lane < 32 ? rows[2 * q] : rows[2 * q + 1]) * step_a;
+      else pa[q] += step_a;
+      bool live = true;
+      if (MODE == DOWN) live = k0 + 8 * kchunk < I;
+      if (MODE == DX) live = k0 + slow_k0 + 2 * q < I;
+      if (DWS) live = k0 + slow_k0 + 2 * q < dm.n;
+      dma16(live ? p : (const char*)zero_chunk, to + 1024 * q);
+    }
+  };
+  auto load_b = [&](uint32_t slot, int stage) __attribute__((always_inline)) {
+    const uint32_t to = ring0 + slot + HALF_SLOT + 4096 * wv;
+    const int k0 = 32 * (MODE == DX && stage >= 2 * pairs_i ? stage - 2 * pairs_i : stage);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bool live = true;
+      if (MODE == DOWN || MODE == DX) live = k0 + 8 * kchunk < I;
+      if (DWS) live = k0 + slow_k0 + 2 * q < dm.n;
+      dma16(live ? pb[q] : (const char*)zero_chunk, to + 1024 * q);
+      pb[q] += step_b;
+    }
+  };
+  // DACT: stage e of kept rows into this wave's own 8 KiB of a slot: 32 rows x
+  // 64 channels (8 bits: 128) of g, then of u, rows of 128 bytes with 16-byte
+  // chunk c of row r at c ^ (r % 8)
+  auto load_kept = [&](uint32_t slot, int e) __attribute__((always_inline)) {
+    const uint32_t to = ring0 + slot + 8192 * wv;
+    const int row0 = dm.n0 + 128 * wn + 32 * (MODE == DACT ? e >> 1 : e);
+    const int c0 = dm.m0 + 128 * wm + (MODE == DACT ? 64 * (e & 1) : 0);
+    const int c = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int64_t p = dm.start + min(row0 + 8 * (q & 3) + (lane >> 3), dm.n - 1);
+      const int64_t at = (2 * p + (q >> 2)) * I;
+      dma16(MODE == DACT ? (const char*)((const bf16*)a.kept + at + min(c0 + 8 * c, I - 8))
+                         : (const char*)a.kept + at + min(c0 + 16 * c, I - 16),
+            to + 1024 * q);
+    }
+  };
+  // half of the stream's pair into a slot; the second half moves on
+  auto load_stage = [&](uint32_t slot, int odd) __attribute__((always_inline)) {
+    if (EXTRA > 0 && dpair >= dpairs) {
+      load_kept(slot, 2 * (dpair - dpairs) + odd);
+    } else {
+      load_a(slot, 2 * dpair + odd);
+      load_b(slot, 2 * dpair + odd);
+    }
+  };
+  auto next_pair = [&]() __attribute__((always_inline)) {
+    ++dpair;
+    bool fresh = MODE == DX && dpair == pairs_i;
+    if (dpair == dpairs + EXTRA / 2) {
+      if (dj + 1 < n_my) {
+        ++dj;
+        dm = decode(dj);
+        dpair = 0;
+        fresh = true;
+      } else {
+        more = false;
+      }
+    }
+    if (fresh) set_tile();
+    look_up(2 * dpair);
+  };
+
+  // ---- fragments ----------------------------------------------------------
+  bf16x8_t fa[2][8], fb[2][8];
+  f32x4_t acc[8][8];
+  const uint32_t f = ((r16 >> 2) & 3) | ((kg & 1) << 2);
+  const uint32_t turned = (uint32_t)((8 * kg + (r16 >> 2)) * 512 + (f << 5) + (r16 & 3) * 8);
+  const uint32_t straight = (uint32_t)(r16 * 64 + ((kg ^ ((r16 >> 1) & 3)) * 16));
+  const uint32_t base_a = ring0 + (AT ? turned + wm * 256 : straight + wm * 8192);
+  const uint32_t base_b = ring0 + HALF_SLOT + (BT ? turned + wn * 256 : straight + wn * 8192);
+  auto read_a = [&](int i, uint32_t slot) __attribute__((always_inline)) {
+    return AT ? read_turned((base_a ^ (i << 5)) + slot) : __builtin_bit_cast(bf16x8_t, read16(base_a + slot + 1024 * i));
+  };
+  auto read_b = [&](int i, uint32_t slot) __attribute__((always_inline)) {
+    return BT ? read_turned((base_b ^ (i << 5)) + slot) : __builtin_bit_cast(bf16x8_t, read16(base_b + slot + 1024 * i));
+  };
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+
+  // One stage: the matrix instructions of fragments P, the next stage's
+  // fragments from slot `from` read into the others, half ODD of the stream's
+  // pair loaded into `into` (whose fragments were read a step ago).  Before
+  // the barrier the loads that the next step reads have landed: of three
+  // stages in flight all but the last two.
+#define STEP(P, from, into, ODD)                                                               \
+  {                                                                                            \
+    _Pragma("unroll") for (int j = 0; j < 8; ++j) {                                            \
+      fa[1 - (P)][j] = read_a(j, from);                                                        \
+      fb[1 - (P)][j] = read_b(j, from);                                                        \
+      if (j == 3 && more) load_stage(into, ODD);                                               \
+      _Pragma("unroll") for (int i = 0; i < 8; ++i)                                            \
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[P][i], fb[P][j], acc[i][j], 0, 0, 0); \
+      __builtin_amdgcn_sched_barrier(0);                                                       \
+    }                                                                                          \
+    wait_lds();                                                                                \
+    if (!more) wait_loads<0>(); else if (settled > 0) --settled; else wait_loads<16>();        \
+    if (ODD) { if (more) next_pair(); } else look_up(2 * dpair + 1);                           \
+    __builtin_amdgcn_s_barrier();                                                              \
+  }
+
+  // ---- outputs ------------------------------------------------------------
+  const uint32_t mine0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&staging[wv][0];
+#include "ffn_train_gemm_out.h"
+
+  set_tile();
+  look_up(0);
+  for (int s = 0; s < 2 && more; ++s) {
+    load_stage(2 * s * SLOT, 0);
+    look_up(2 * dpair + 1);
+    load_stage((2 * s + 1) * SLOT, 1);
+    next_pair();
+  }
+  if (more) wait_loads<16>(); else wait_loads<0>();      // stages 0 and 1
+  __builtin_amdgcn_s_barrier();
+  auto first_fragments = [&](uint32_t slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      fa[0][j] = read_a(j, slot);
+      fb[0][j] = read_b(j, slot);
+    }
+    wait_lds();
+    __builtin_amdgcn_s_barrier();      // the slot may be filled again
+  };
+  first_fragments(0);
+  clear();
+  int settled = 0;                     // steps whose loads have landed already
+  uint32_t even = 0;                   // slot of the pair's first stage: 0 or 2
+  for (int cj = 0; cj < n_my; ++cj) {
+    const Meta cm = decode(cj);
+    const int pairs = pairs_of(cm);
+    before_tile(cm);
+    for (int p = 0; p < pairs; ++p) {
+      STEP(0, even + SLOT, even, 0)
+      STEP(1, even ^ (2 * SLOT), even + SLOT, 1)
+      even ^= 2 * SLOT;
+    }
+    if constexpr (DA) {
+      // The kept rows' stages follow: a wave works on its own part of each and
+      // the slot is filled again once all are done.  A wave whose outputs are
+      // all there issues S stores a stage; of any other only loads are counted.
+      constexpr int S = MODE == DACT ? 12 : 24;
+      const int left = cm.n - cm.n0 - 128 * wn, cols = I - cm.m0 - 128 * wm;
+      const bool full = left >= 128 && cols >= 128;
+      matrix_done();
+#pragma unroll
+      for (int e = 0; e < EXTRA; ++e) {
+        const uint32_t slot = (even + e * SLOT) & (RING * SLOT - 1);
+        if (e >= 2) {
+          if (!more) wait_loads<0>();
+          else if (full && e == 2) wait_loads<(24 + 2 * S > 63 ? 63 : 24 + 2 * S)>();
+          else if (full) wait_loads<(24 + 3 * S > 63 ? 63 : 24 + 3 * S)>();
+          else wait_loads<24>();
+        }
+        if (left > 0 && cols > 0) gradients(cm, e, slot);
+        __builtin_amdgcn_s_barrier();
+        if (more) {
+          load_stage(slot, e & 1);
+          if (e & 1) next_pair();
+        }
+      }
+      even = (even + EXTRA * SLOT) & (RING * SLOT - 1);
+      if (!more) wait_loads<0>();
+      else if (full) wait_loads<(16 + 2 * S > 63 ? 63 : 16 + 2 * S)>();
+      else wait_loads<16>();
+      __builtin_amdgcn_s_barrier();
+      first_fragments(even);
+    } else {
+      // what is in flight lands before the first store, so that the next
+      // steps need not wait for the stores behind it
+      wait_loads<0>();
+      settled = 2;
+      matrix_done();
+      outputs(cm);
+    }
+    clear();
+  }
+  wait_loads<0>();                     // no load outlives the block's LDS
+#undef STEP
+}
+
+}  // namespace
+
+// Persistent grid: a block fills a CU; a multiple of the XCDs, and enough
+// blocks that none has more than MAX_TILES tiles.
+static int gemm_grid(int64_t tiles) {
+  int64_t g = std::min<int64_t>(tiles, CUS);
+  const int64_t per_x = (tiles + NXCD - 1) / NXCD;
+  g = std::max(g, NXCD * ((per_x + MAX_TILES - 1) / MAX_TILES));
+  return (int)((g + NXCD - 1) / NXCD * NXCD);
+}
+
+hipError_t launch_train_gemm(int which, const TrainArgs& a, int P, hipStream_t s) {
+  const int64_t row_tiles = P / TILE + std::min(a.E, P);     // an upper bound
+  const int64_t mh = (a.H + TILE - 1) / TILE, mi = (a.I + TILE - 1) / TILE;
+  if (which == 0) {
+    const int grid = gemm_grid(row_tiles * ((a.I + 127) / 128));
+    if (a.keep8) train_gemm_kernel<GATE_UP8><<<grid, 256, 0, s>>>(a);
+    else train_gemm_kernel<GATE_UP><<<grid, 256, 0, s>>>(a);
+  } else if (which == 1) {
+    train_gemm_kernel<DOWN><<<gemm_grid(row_tiles * mh), 256, 0, s>>>(a);
+  } else if (which == 2) {
+    const int grid = gemm_grid(row_tiles * mi);
+    if (a.keep8) train_gemm_kernel<DACT8><<<grid, 256, 0, s>>>(a);
+    else train_gemm_kernel<DACT><<<grid, 256, 0, s>>>(a);
+  } else if (which == 3) {
+    train_gemm_kernel<DX><<<gemm_grid(row_tiles * mh), 256, 0, s>>>(a);
+  } else {
+    TrainArgs b = a;
+    b.n_dw = b.dw_list = 0;
+    for (int w = 0; w < 3; ++w)
+      if (a.dw[w]) b.dw_list |= w << (2 * b.n_dw++);
+    if (!b.n_dw) return hipSuccess;
+    const int grid = gemm_grid(a.E * b.n_dw * mh * mi);
+    if (a.dw_f32 || a.accumulate) train_gemm_kernel<DW_ANY><<<grid, 256, 0, s>>>(b);
+    else train_gemm_kernel<DW><<<grid, 256, 0, s>>>(b);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -49,7 +49,7 @@ constexpr int RING = 4;
 constexpr int STAGING = 6144;       // a wave's: three pieces of 16 rows x 64 bf16
 constexpr int NXCD = 8;
 constexpr int CUS = 256;
-constexpr int MAX_TILES = 8;        // tiles of a block whose token rows are looked up ahead
+constexpr int LOOK_UP = 8;          // tiles of a block whose token rows are looked up at once
 
 __device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 
@@ -83,9 +83,13 @@ __device__ __forceinline__ bf16x8_t read_turned(uint32_t at) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// An accumulator where it is used: left to itself the compiler moves all 256
-// to the other half of the register file at once and spills.  The matrix
-// instructions before it have ended (matrix_done).
+// The accumulators stay in the accumulation half of the register file: left to
+// itself the compiler moves them to the other and back in every step.  Before
+// they are read, and after they are cleared, matrix_done waits as many cycles
+// as the longest of the hazards between these instructions takes.
+__device__ __forceinline__ void mac(const bf16x8_t& a, const bf16x8_t& b, f32x4_t& c) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
 __device__ __forceinline__ float acc_read(float v) {
   float r;
   asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(r) : "a"(v));
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
   constexpr bool AT = DA || MODE == DX || DWS, BT = DWS;   // operands whose k is the slow axis
   __shared__ __attribute__((aligned(1024))) char ring[RING * SLOT];
   __shared__ __attribute__((aligned(16))) char staging[4][STAGING];
-  __shared__ int token[GU ? MAX_TILES : 1][GU ? TILE : 1];
+  __shared__ int token[GU ? LOOK_UP : 1][GU ? TILE : 1];
 
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, kg = lane >> 4;
@@ -152,14 +156,6 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
     }
     return m;
   };
-  if (GU) {
-    for (int j = 0; j < n_my; ++j) {
-      const Meta m = decode(j);
-      const int row = min(m.n0 + (int)threadIdx.x, m.n - 1);
-      token[j][threadIdx.x] = a.perm[m.start + row] / a.k;
-    }
-    __syncthreads();
-  }
   // pairs of stages of a tile (DX: of each of its two halves)
   const int pairs_i = (I + 63) / 64;
   auto pairs_of = [&](const Meta& m) __attribute__((always_inline)) {
@@ -202,6 +198,15 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
   };
   auto set_tile = [&]() __attribute__((always_inline)) {
     const int64_t we = (int64_t)dm.e * I * H;
+    if (GU && dj % LOOK_UP == 0 && dpair == 0) {   // the rows of the next tiles, by all waves
+      for (int j = dj; j < min(dj + LOOK_UP, n_my); ++j) {
+        const Meta m = decode(j);
+        const int row = min(m.n0 + (int)threadIdx.x, m.n - 1);
+        token[j - dj][threadIdx.x] = a.perm[m.start + row] / a.k;
+      }
+      wait_lds();
+      __builtin_amdgcn_s_barrier();
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = 64 * wv + 16 * q + (lane >> 2);       // k fast: row of the tile
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
       if (GU) {
         const int ch = min(dm.m0 + (r >> 7) * 64 + (r & 63), I - 1);
         pa[q] = (const char*)((const bf16*)((r >> 6) & 1 ? a.w_up : a.w_gate) + we + (int64_t)ch * H + 8 * kchunk);
-        pb[q] = (const char*)((const bf16*)a.x + (int64_t)token[dj][r] * H + 8 * kchunk);
+        pb[q] = (const char*)((const bf16*)a.x + (int64_t)token[dj % LOOK_UP][r] * H + 8 * kchunk);
       } else if (MODE == DOWN) {
         pa[q] = (const char*)((const bf16*)a.w_down + we + (int64_t)min(dm.m0 + r, H - 1) * I + 8 * kchunk);
         pb[q] = (const char*)((const bf16*)a.act + (int64_t)(dm.start + row) * I + 8 * kchunk);
@@ -323,6 +328,7 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    matrix_done();
   };
 
   // One stage: the matrix instructions of fragments P, the next stage's
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
       fb[1 - (P)][j] = read_b(j, from);                                                        \
       if (j == 3 && more) load_stage(into, ODD);                                               \
       _Pragma("unroll") for (int i = 0; i < 8; ++i)                                            \
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[P][i], fb[P][j], acc[i][j], 0, 0, 0); \
+          mac(fa[P][i], fb[P][j], acc[i][j]);                                                  \
       __builtin_amdgcn_sched_barrier(0);                                                       \
     }                                                                                          \
     wait_lds();                                                                                \
@@ -428,12 +434,9 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
 
 }  // namespace
 
-// Persistent grid: a block fills a CU; a multiple of the XCDs, and enough
-// blocks that none has more than MAX_TILES tiles.
+// Persistent grid: a block fills a CU; a multiple of the XCDs.
 static int gemm_grid(int64_t tiles) {
-  int64_t g = std::min<int64_t>(tiles, CUS);
-  const int64_t per_x = (tiles + NXCD - 1) / NXCD;
-  g = std::max(g, NXCD * ((per_x + MAX_TILES - 1) / MAX_TILES));
+  const int64_t g = std::min<int64_t>(tiles, CUS);
   return (int)((g + NXCD - 1) / NXCD * NXCD);
 }
 

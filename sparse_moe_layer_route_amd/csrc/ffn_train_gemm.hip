@@ -42,14 +42,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // weights in fp32, or added to what is there
 enum { GATE_UP, GATE_UP8, DOWN, DACT, DACT8, DX, DW, DW_ANY };
 
-constexpr int TILE = 256;           // outputs of a block along m and along n
-constexpr int HALF_SLOT = 16384;    // an operand's stage: 256 outputs x 32 k
-constexpr int SLOT = 2 * HALF_SLOT;
-constexpr int RING = 4;
-constexpr int STAGING = 6144;       // a wave's: three pieces of 16 rows x 64 bf16
+constexpr int TM = 256, TN = 128;   // outputs of a block along m and along n
+constexpr int A_STAGE = TM * 64;    // bytes of 32 k of either operand
+constexpr int B_STAGE = TN * 64;
+constexpr int SLOT = A_STAGE + B_STAGE;
+constexpr int RING = 3;
+constexpr int LOADS = 6;            // instructions a wave loads a stage with
+constexpr int STAGING = 2048;       // a wave's: 16 rows x 64 bf16
 constexpr int NXCD = 8;
-constexpr int CUS = 256;
-constexpr int LOOK_UP = 8;          // tiles of a block whose token rows are looked up at once
+constexpr int BLOCKS = 512;         // two a CU
 
 __device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 
@@ -76,10 +77,10 @@ __device__ __forceinline__ u32x2 read8(uint32_t at) { return *(const lds8_t*)(ui
 __device__ __forceinline__ void write8(uint32_t at, uint32_t lo, uint32_t hi) {
   *(lds8_t*)(uintptr_t)at = u32x2{lo, hi};
 }
-// Rows k..k+3 and k+4..k+7 (512 bytes apart) of 16 outputs: this lane's output, its 8 k.
-__device__ __forceinline__ bf16x8_t read_turned(uint32_t at) {
+// Rows k..k+3 and k+4..k+7 (PITCH bytes apart) of 16 outputs: this lane's output, its 8 k.
+template <int PITCH> __device__ __forceinline__ bf16x8_t read_turned(uint32_t at) {
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_turn_t*)(uintptr_t)at);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_turn_t*)(uintptr_t)(at + 2048));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_turn_t*)(uintptr_t)(at + 4 * PITCH));
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -99,6 +100,13 @@ __device__ __forceinline__ void acc_read4(const f32x4_t& v, float (&r)[4]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) r[q] = acc_read(v[q]);
 }
+// The lane, as a value that nothing derived from is kept in registers for the
+// next use across the steps in between.
+__device__ __forceinline__ int fresh_lane() {
+  int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(l));
+  return l;
+}
 __device__ __forceinline__ void matrix_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // One tile of the launch: expert, its first row and rows, n and m origins, and
@@ -106,27 +114,30 @@ __device__ __forceinline__ void matrix_done() { asm volatile("s_nop 15\n\ts_nop 
 struct Meta { int e, start, n, n0, m0, which; };
 
 template <int MODE>
-__global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
+__global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
   constexpr bool GU = MODE == GATE_UP || MODE == GATE_UP8, DA = MODE == DACT || MODE == DACT8;
   constexpr bool DWS = MODE == DW || MODE == DW_ANY;
   constexpr bool AT = DA || MODE == DX || DWS, BT = DWS;   // operands whose k is the slow axis
   __shared__ __attribute__((aligned(1024))) char ring[RING * SLOT];
   __shared__ __attribute__((aligned(16))) char staging[4][STAGING];
-  __shared__ int token[GU ? LOOK_UP : 1][GU ? TILE : 1];
 
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1, r16 = lane & 15, kg = lane >> 4;
   const int H = a.H, I = a.I;
 
   // ---- this block's tiles: its XCD's share, every nbx-th ------------------
-  const int tiles_m = GU ? (I + 127) / 128 : DA ? (I + TILE - 1) / TILE : (H + TILE - 1) / TILE;
-  const int per_matrix = DWS ? ((H + TILE - 1) / TILE) * ((I + TILE - 1) / TILE) : 0;
+  const int tiles_m = GU ? (I + 127) / 128 : DA ? (I + TM - 1) / TM : (H + TM - 1) / TM;
+  // DW: tiles of dW_g or dW_u (m over H), and of dW_d (m over I)
+  const int per_gu = DWS ? ((H + TM - 1) / TM) * ((I + TN - 1) / TN) : 0;
+  const int per_d = DWS ? ((I + TM - 1) / TM) * ((H + TN - 1) / TN) : 0;
+  const bool any_d = DWS && a.dw[2] != nullptr;
+  const int n_gu = DWS ? a.n_dw - any_d : 0;
   int off = 0, cnt = 0;
   if (lane < a.E) {
     off = a.offsets[lane];
     cnt = a.offsets[lane + 1] - off;
   }
-  const int mine = lane < a.E ? (DWS ? per_matrix * a.n_dw : (cnt + TILE - 1) / TILE * tiles_m) : 0;
+  const int mine = lane < a.E ? (DWS ? per_gu * n_gu + (any_d ? per_d : 0) : (cnt + TN - 1) / TN * tiles_m) : 0;
   const int incl = wave_incl_scan_i(mine);
   const int total = __builtin_amdgcn_readlane(incl, 63);
   const int nbx = gridDim.x / NXCD, xcd = blockIdx.x % NXCD, bi = blockIdx.x / NXCD;
@@ -144,15 +155,17 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
     m.start = __builtin_amdgcn_readlane(off, m.e);
     m.n = __builtin_amdgcn_readlane(cnt, m.e);
     if constexpr (DWS) {
-      const int w = r / per_matrix, q = r % per_matrix;
-      m.which = (a.dw_list >> (2 * w)) & 3;
-      const int nm = ((m.which == 2 ? I : H) + TILE - 1) / TILE;
-      m.m0 = q % nm * TILE;
-      m.n0 = q / nm * TILE;
+      const int w = r / per_gu;
+      const bool down = w >= n_gu;
+      const int q = down ? r - n_gu * per_gu : r - w * per_gu;
+      m.which = down ? 2 : a.dw[0] ? w : 1;
+      const int nm = ((down ? I : H) + TM - 1) / TM;
+      m.m0 = q % nm * TM;
+      m.n0 = q / nm * TN;
     } else {
       m.which = 0;
-      m.m0 = r % tiles_m * (GU ? 128 : TILE);
-      m.n0 = r / tiles_m * TILE;
+      m.m0 = r % tiles_m * (GU ? 128 : TM);
+      m.n0 = r / tiles_m * TN;
     }
     return m;
   };
@@ -165,21 +178,26 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
   constexpr int EXTRA = MODE == DACT ? 8 : MODE == DACT8 ? 4 : 0;
 
   // ---- loading stream -----------------------------------------------------
-  // Wave w moves, of either operand, rows 64 w..+63 (k fast) or k 8 w..+7 (k
-  // slow) of a stage, four instructions of 1 KiB.  The stream's position is a
-  // pair of stages of a tile; it ends with the block's last tile.
+  // Wave w moves rows 64 w..+63 of A and 32 w..+31 of B (k fast), or k 8 w..+7
+  // of either (k slow), in four and two instructions of 1 KiB.  The stream's
+  // position is a pair of stages of a tile; it ends with the block's last tile.
   const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&ring[0];
   int dj = 0, dpair = 0, dpairs;
   bool more = true;
   Meta dm = decode(0);
   const char* pa[4];                   // this lane's next 16 bytes, by instruction
-  const char* pb[4];                   // (DW's pa: its column, the rows being looked up)
+  const char* pb[2];                   // (DW's pa: its column, the rows being looked up)
   int64_t step_a = 0, step_b = 0;
   const int kchunk = (lane & 3) ^ ((lane >> 3) & 3);    // k fast: the 16-byte chunk this lane moves
   const int slow_k0 = 8 * wv + (lane >> 5);             // k slow: row (+ 2 q) this lane moves
   auto slow_col = [&](int q) __attribute__((always_inline)) {
     const int k = slow_k0 + 2 * q, f = (k & 3) | (((k >> 3) & 1) << 2);
     return 16 * (((lane & 31) >> 1) ^ f) + 8 * (lane & 1);
+  };
+  const int slow_kb0 = 8 * wv + (lane >> 4);            // B's: (+ 4 q)
+  auto slow_col_b = [&](int q) __attribute__((always_inline)) {
+    const int k = slow_kb0 + 4 * q, f = (k & 3) | (((k >> 3) & 1) << 2);
+    return 16 * (((lane & 15) >> 1) ^ f) + 8 * (lane & 1);
   };
   // DW: x's rows of a stage are looked up through scalar loads a stage ahead
   const __attribute__((address_space(4))) int32_t* perm_s =
@@ -198,41 +216,41 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
   };
   auto set_tile = [&]() __attribute__((always_inline)) {
     const int64_t we = (int64_t)dm.e * I * H;
-    if (GU && dj % LOOK_UP == 0 && dpair == 0) {   // the rows of the next tiles, by all waves
-      for (int j = dj; j < min(dj + LOOK_UP, n_my); ++j) {
-        const Meta m = decode(j);
-        const int row = min(m.n0 + (int)threadIdx.x, m.n - 1);
-        token[j - dj][threadIdx.x] = a.perm[m.start + row] / a.k;
-      }
-      wait_lds();
-      __builtin_amdgcn_s_barrier();
-    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = 64 * wv + 16 * q + (lane >> 2);       // k fast: row of the tile
       const int64_t k = slow_k0 + 2 * q;
-      const int row = min(dm.n0 + r, dm.n - 1);
       if (GU) {
         const int ch = min(dm.m0 + (r >> 7) * 64 + (r & 63), I - 1);
         pa[q] = (const char*)((const bf16*)((r >> 6) & 1 ? a.w_up : a.w_gate) + we + (int64_t)ch * H + 8 * kchunk);
-        pb[q] = (const char*)((const bf16*)a.x + (int64_t)token[dj % LOOK_UP][r] * H + 8 * kchunk);
       } else if (MODE == DOWN) {
         pa[q] = (const char*)((const bf16*)a.w_down + we + (int64_t)min(dm.m0 + r, H - 1) * I + 8 * kchunk);
-        pb[q] = (const char*)((const bf16*)a.act + (int64_t)(dm.start + row) * I + 8 * kchunk);
       } else if (DA) {
         pa[q] = (const char*)((const bf16*)a.w_down + we + k * I + min(dm.m0 + slow_col(q), I - 8));
-        pb[q] = (const char*)((const bf16*)a.dy + (int64_t)(dm.start + row) * H + 8 * kchunk);
-      } else if (MODE == DX) {
-        const bool up = dpair >= pairs_i;                 // on to W_u and du
-        pa[q] = (const char*)((const bf16*)(up ? a.w_up : a.w_gate) + we + k * H + min(dm.m0 + slow_col(q), H - 8));
-        pb[q] = (const char*)((const bf16*)a.dgu + ((int64_t)(dm.start + row) * 2 + up) * I + 8 * kchunk);
+      } else if (MODE == DX) {                            // W_g, then W_u
+        pa[q] = (const char*)((const bf16*)(dpair >= pairs_i ? a.w_up : a.w_gate) + we + k * H +
+                              min(dm.m0 + slow_col(q), H - 8));
       } else {
         const bool down = dm.which == 2;
-        const int M = down ? I : H, N = down ? H : I;
-        pa[q] = (const char*)((const bf16*)(down ? a.act : a.x) + min(dm.m0 + slow_col(q), M - 8));
+        pa[q] = (const char*)((const bf16*)(down ? a.act : a.x) + min(dm.m0 + slow_col(q), (down ? I : H) - 8));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t row = dm.start + min(dm.n0 + 32 * wv + 16 * q + (lane >> 2), dm.n - 1);
+      if (GU) {
+        pb[q] = (const char*)((const bf16*)a.x + (int64_t)(a.perm[row] / a.k) * H + 8 * kchunk);
+      } else if (MODE == DOWN) {
+        pb[q] = (const char*)((const bf16*)a.act + row * I + 8 * kchunk);
+      } else if (DA) {
+        pb[q] = (const char*)((const bf16*)a.dy + row * H + 8 * kchunk);
+      } else if (MODE == DX) {
+        pb[q] = (const char*)((const bf16*)a.dgu + (2 * row + (dpair >= pairs_i)) * I + 8 * kchunk);
+      } else {
+        const bool down = dm.which == 2;
         pb[q] = (const char*)((const bf16*)(down ? a.dy : a.dgu) +
-                              (int64_t)(dm.start + k) * (down ? H : 2 * I) + (down ? 0 : dm.which * I) +
-                              min(dm.n0 + slow_col(q), N - 8));
+                              (int64_t)(dm.start + slow_kb0 + 4 * q) * (down ? H : 2 * I) + (down ? 0 : dm.which * I) +
+                              min(dm.n0 + slow_col_b(q), (down ? H : I) - 8));
       }
     }
     step_a = !AT ? 64 : DWS ? 2 * (int64_t)(dm.which == 2 ? I : H) : 64 * (int64_t)(MODE == DX ? H : I);
@@ -255,29 +273,29 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
     }
   };
   auto load_b = [&](uint32_t slot, int stage) __attribute__((always_inline)) {
-    const uint32_t to = ring0 + slot + HALF_SLOT + 4096 * wv;
+    const uint32_t to = ring0 + slot + A_STAGE + 2048 * wv;
     const int k0 = 32 * (MODE == DX && stage >= 2 * pairs_i ? stage - 2 * pairs_i : stage);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
       bool live = true;
       if (MODE == DOWN || MODE == DX) live = k0 + 8 * kchunk < I;
-      if (DWS) live = k0 + slow_k0 + 2 * q < dm.n;
+      if (DWS) live = k0 + slow_kb0 + 4 * q < dm.n;
       dma16(live ? pb[q] : (const char*)zero_chunk, to + 1024 * q);
       pb[q] += step_b;
     }
   };
-  // DACT: stage e of kept rows into this wave's own 8 KiB of a slot: 32 rows x
+  // DACT: stage e of kept rows into this wave's own 4 KiB of a slot: 16 rows x
   // 64 channels (8 bits: 128) of g, then of u, rows of 128 bytes with 16-byte
   // chunk c of row r at c ^ (r % 8)
   auto load_kept = [&](uint32_t slot, int e) __attribute__((always_inline)) {
-    const uint32_t to = ring0 + slot + 8192 * wv;
-    const int row0 = dm.n0 + 128 * wn + 32 * (MODE == DACT ? e >> 1 : e);
+    const uint32_t to = ring0 + slot + 4096 * wv;
+    const int row0 = dm.n0 + 64 * wn + 16 * (MODE == DACT ? e >> 1 : e);
     const int c0 = dm.m0 + 128 * wm + (MODE == DACT ? 64 * (e & 1) : 0);
-    const int c = (lane & 7) ^ (lane >> 3);
+    const int l = fresh_lane(), c = (l & 7) ^ (l >> 3);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int64_t p = dm.start + min(row0 + 8 * (q & 3) + (lane >> 3), dm.n - 1);
-      const int64_t at = (2 * p + (q >> 2)) * I;
+    for (int q = 0; q < 4; ++q) {
+      const int64_t p = dm.start + min(row0 + 8 * (q & 1) + (l >> 3), dm.n - 1);
+      const int64_t at = (2 * p + (q >> 1)) * I;
       dma16(MODE == DACT ? (const char*)((const bf16*)a.kept + at + min(c0 + 8 * c, I - 8))
                          : (const char*)a.kept + at + min(c0 + 16 * c, I - 16),
             to + 1024 * q);
@@ -310,121 +328,129 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
   };
 
   // ---- fragments ----------------------------------------------------------
-  bf16x8_t fa[2][8], fb[2][8];
-  f32x4_t acc[8][8];
+  bf16x8_t fa[8], fb[2][4];
+  f32x4_t acc[8][4];
   const uint32_t f = ((r16 >> 2) & 3) | ((kg & 1) << 2);
-  const uint32_t turned = (uint32_t)((8 * kg + (r16 >> 2)) * 512 + (f << 5) + (r16 & 3) * 8);
   const uint32_t straight = (uint32_t)(r16 * 64 + ((kg ^ ((r16 >> 1) & 3)) * 16));
-  const uint32_t base_a = ring0 + (AT ? turned + wm * 256 : straight + wm * 8192);
-  const uint32_t base_b = ring0 + HALF_SLOT + (BT ? turned + wn * 256 : straight + wn * 8192);
+  auto turned = [&](uint32_t pitch, uint32_t first) __attribute__((always_inline)) {
+    return (uint32_t)((8 * kg + (r16 >> 2)) * pitch + ((first ^ f) << 5) + (r16 & 3) * 8);
+  };
+  const uint32_t base_a = ring0 + (AT ? turned(512, 8 * wm) : straight + wm * 8192);
+  const uint32_t base_b = ring0 + A_STAGE + (BT ? turned(256, 4 * wn) : straight + wn * 4096);
   auto read_a = [&](int i, uint32_t slot) __attribute__((always_inline)) {
-    return AT ? read_turned((base_a ^ (i << 5)) + slot) : __builtin_bit_cast(bf16x8_t, read16(base_a + slot + 1024 * i));
+    return AT ? read_turned<512>((base_a ^ (i << 5)) + slot)
+              : __builtin_bit_cast(bf16x8_t, read16(base_a + slot + 1024 * i));
   };
   auto read_b = [&](int i, uint32_t slot) __attribute__((always_inline)) {
-    return BT ? read_turned((base_b ^ (i << 5)) + slot) : __builtin_bit_cast(bf16x8_t, read16(base_b + slot + 1024 * i));
+    return BT ? read_turned<256>((base_b ^ (i << 5)) + slot)
+              : __builtin_bit_cast(bf16x8_t, read16(base_b + slot + 1024 * i));
   };
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     matrix_done();
   };
+  auto after = [&](uint32_t slot) __attribute__((always_inline)) {
+    return slot == (RING - 1) * SLOT ? 0u : slot + SLOT;
+  };
 
-  // One stage: the matrix instructions of fragments P, the next stage's
-  // fragments from slot `from` read into the others, half ODD of the stream's
-  // pair loaded into `into` (whose fragments were read a step ago).  Before
-  // the barrier the loads that the next step reads have landed: of three
-  // stages in flight all but the last two.
-#define STEP(P, from, into, ODD)                                                               \
+  // One stage: the matrix instructions of its fragments (B's set P); the next
+  // stage's are read in their places as they fall free; half ODD of the
+  // stream's pair is loaded into this stage's slot, whose fragments were read
+  // a step ago.  Before the barrier the loads that the next step reads have
+  // landed: all but the last stage's.
+#define STEP(P, ODD)                                                                           \
   {                                                                                            \
-    _Pragma("unroll") for (int j = 0; j < 8; ++j) {                                            \
-      fa[1 - (P)][j] = read_a(j, from);                                                        \
-      fb[1 - (P)][j] = read_b(j, from);                                                        \
-      if (j == 3 && more) load_stage(into, ODD);                                               \
-      _Pragma("unroll") for (int i = 0; i < 8; ++i)                                            \
-          mac(fa[P][i], fb[P][j], acc[i][j]);                                                  \
+    const uint32_t from = after(slot);                                                         \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) {                                            \
+      _Pragma("unroll") for (int j = 0; j < 4; ++j) mac(fa[i], fb[P][j], acc[i][j]);           \
+      fa[i] = read_a(i, from);                                                                 \
+      if (i < 4) fb[1 - (P)][i] = read_b(i, from);                                             \
+      if (i == 1 && more) load_stage(slot, ODD);                                               \
       __builtin_amdgcn_sched_barrier(0);                                                       \
     }                                                                                          \
     wait_lds();                                                                                \
-    if (!more) wait_loads<0>(); else if (settled > 0) --settled; else wait_loads<16>();        \
+    if (!more) wait_loads<0>();                                                                \
+    else if (settled > 0) --settled;                                                           \
+    else if (EXTRA > 0 && dpair >= dpairs) wait_loads<4>();                                    \
+    else wait_loads<LOADS>();                                                                  \
     if (ODD) { if (more) next_pair(); } else look_up(2 * dpair + 1);                           \
     __builtin_amdgcn_s_barrier();                                                              \
+    slot = from;                                                                               \
   }
 
   // ---- outputs ------------------------------------------------------------
   const uint32_t mine0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&staging[wv][0];
 #include "ffn_train_gemm_out.h"
 
+  uint32_t slot = 0;                   // of the present stage
   set_tile();
   look_up(0);
-  for (int s = 0; s < 2 && more; ++s) {
-    load_stage(2 * s * SLOT, 0);
-    look_up(2 * dpair + 1);
-    load_stage((2 * s + 1) * SLOT, 1);
-    next_pair();
-  }
-  if (more) wait_loads<16>(); else wait_loads<0>();      // stages 0 and 1
+  load_stage(0, 0);
+  look_up(1);
+  load_stage(SLOT, 1);
+  next_pair();
+  if (more) load_stage(2 * SLOT, 0);
+  if (more) { look_up(2 * dpair + 1); wait_loads<LOADS>(); } else wait_loads<0>();
   __builtin_amdgcn_s_barrier();
-  auto first_fragments = [&](uint32_t slot) __attribute__((always_inline)) {
+  auto first_fragments = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      fa[0][j] = read_a(j, slot);
-      fb[0][j] = read_b(j, slot);
-    }
+    for (int i = 0; i < 8; ++i) fa[i] = read_a(i, slot);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fb[0][j] = read_b(j, slot);
     wait_lds();
     __builtin_amdgcn_s_barrier();      // the slot may be filled again
   };
-  first_fragments(0);
+  first_fragments();
   clear();
   int settled = 0;                     // steps whose loads have landed already
-  uint32_t even = 0;                   // slot of the pair's first stage: 0 or 2
   for (int cj = 0; cj < n_my; ++cj) {
     const Meta cm = decode(cj);
     const int pairs = pairs_of(cm);
     before_tile(cm);
     for (int p = 0; p < pairs; ++p) {
-      STEP(0, even + SLOT, even, 0)
-      STEP(1, even ^ (2 * SLOT), even + SLOT, 1)
-      even ^= 2 * SLOT;
+      STEP(0, 1)
+      STEP(1, 0)
     }
     if constexpr (DA) {
       // The kept rows' stages follow: a wave works on its own part of each and
       // the slot is filled again once all are done.  A wave whose outputs are
-      // all there issues S stores a stage; of any other only loads are counted.
-      constexpr int S = MODE == DACT ? 12 : 24;
-      const int left = cm.n - cm.n0 - 128 * wn, cols = I - cm.m0 - 128 * wm;
-      const bool full = left >= 128 && cols >= 128;
+      // all there issues S stores a stage; of any other only loads (four a
+      // stage at least) are counted.
+      constexpr int S = MODE == DACT ? 6 : 12;
+      const int left = cm.n - cm.n0 - 64 * wn, cols = I - cm.m0 - 128 * wm;
+      const bool full = left >= 64 && cols >= 128;
       matrix_done();
 #pragma unroll
       for (int e = 0; e < EXTRA; ++e) {
-        const uint32_t slot = (even + e * SLOT) & (RING * SLOT - 1);
         if (e >= 2) {
           if (!more) wait_loads<0>();
-          else if (full && e == 2) wait_loads<(24 + 2 * S > 63 ? 63 : 24 + 2 * S)>();
-          else if (full) wait_loads<(24 + 3 * S > 63 ? 63 : 24 + 3 * S)>();
-          else wait_loads<24>();
+          else if (full) wait_loads<8 + 2 * S>();
+          else wait_loads<8>();
         }
         if (left > 0 && cols > 0) gradients(cm, e, slot);
         __builtin_amdgcn_s_barrier();
         if (more) {
-          load_stage(slot, e & 1);
-          if (e & 1) next_pair();
+          load_stage(slot, 1 - (e & 1));
+          if (e & 1) look_up(2 * dpair + 1); else next_pair();
         }
+        slot = after(slot);
       }
-      even = (even + EXTRA * SLOT) & (RING * SLOT - 1);
       if (!more) wait_loads<0>();
-      else if (full) wait_loads<(16 + 2 * S > 63 ? 63 : 16 + 2 * S)>();
-      else wait_loads<16>();
+      else if (full) wait_loads<LOADS + S>();
+      else wait_loads<LOADS>();
       __builtin_amdgcn_s_barrier();
-      first_fragments(even);
+      first_fragments();
     } else {
-      // what is in flight lands before the first store, so that the next
-      // steps need not wait for the stores behind it
+      // what is in flight lands before the first store, so that the next step
+      // need not wait for the stores behind it
       wait_loads<0>();
-      settled = 2;
+      settled = 1;
       matrix_done();
       outputs(cm);
+      if constexpr (GU) first_fragments();   // read again: they are not held across the outputs
     }
     clear();
   }
@@ -434,15 +460,15 @@ __global__ void __launch_bounds__(256, 1) train_gemm_kernel(TrainArgs a) {
 
 }  // namespace
 
-// Persistent grid: a block fills a CU; a multiple of the XCDs.
+// Persistent grid: two blocks fill a CU; a multiple of the XCDs.
 static int gemm_grid(int64_t tiles) {
-  const int64_t g = std::min<int64_t>(tiles, CUS);
+  const int64_t g = std::min<int64_t>(tiles, BLOCKS);
   return (int)((g + NXCD - 1) / NXCD * NXCD);
 }
 
 hipError_t launch_train_gemm(int which, const TrainArgs& a, int P, hipStream_t s) {
-  const int64_t row_tiles = P / TILE + std::min(a.E, P);     // an upper bound
-  const int64_t mh = (a.H + TILE - 1) / TILE, mi = (a.I + TILE - 1) / TILE;
+  const int64_t row_tiles = P / TN + std::min(a.E, P);       // an upper bound
+  const int64_t mh = (a.H + TM - 1) / TM, mi = (a.I + TM - 1) / TM;
   if (which == 0) {
     const int grid = gemm_grid(row_tiles * ((a.I + 127) / 128));
     if (a.keep8) train_gemm_kernel<GATE_UP8><<<grid, 256, 0, s>>>(a);
@@ -457,11 +483,10 @@ hipError_t launch_train_gemm(int which, const TrainArgs& a, int P, hipStream_t s
     train_gemm_kernel<DX><<<gemm_grid(row_tiles * mh), 256, 0, s>>>(a);
   } else {
     TrainArgs b = a;
-    b.n_dw = b.dw_list = 0;
-    for (int w = 0; w < 3; ++w)
-      if (a.dw[w]) b.dw_list |= w << (2 * b.n_dw++);
+    b.n_dw = (a.dw[0] != nullptr) + (a.dw[1] != nullptr) + (a.dw[2] != nullptr);
     if (!b.n_dw) return hipSuccess;
-    const int grid = gemm_grid(a.E * b.n_dw * mh * mi);
+    const int64_t tiles = std::max(mh * ((a.I + TN - 1) / TN), mi * ((a.H + TN - 1) / TN));
+    const int grid = gemm_grid(a.E * b.n_dw * tiles);
     if (a.dw_f32 || a.accumulate) train_gemm_kernel<DW_ANY><<<grid, 256, 0, s>>>(b);
     else train_gemm_kernel<DW><<<grid, 256, 0, s>>>(b);
   }

@@ -15,7 +15,7 @@ struct TrainArgs {
   void *act, *dgu;   // workspace: SiLU(g) u [P][I]; dg and du [P][2][I]
   int E, H, I, k, blocks, pairs;   // pairs: T * k
   int keep8, dw_f32, accumulate;
-  int n_dw, dw_list; // the matrices whose gradients are asked for: how many, 2 bits each
+  int n_dw;          // matrices whose gradients are asked for
 };
 
 // ------------------------------------------------- rows kept in 8 bits ----

@@ -24,6 +24,8 @@
 //
 // Blocks are persistent: the stages of a block's tiles form one stream, so the
 // next tile's first stages load while the present one's outputs are formed.
+#include <stdlib.h>
+
 #include <algorithm>
 
 #include "common.h"
@@ -42,15 +44,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // weights in fp32, or added to what is there
 enum { GATE_UP, GATE_UP8, DOWN, DACT, DACT8, DX, DW, DW_ANY };
 
-constexpr int TM = 256, TN = 128;   // outputs of a block along m and along n
-constexpr int A_STAGE = TM * 64;    // bytes of 32 k of either operand
-constexpr int B_STAGE = TN * 64;
-constexpr int SLOT = A_STAGE + B_STAGE;
-constexpr int RING = 3;
-constexpr int LOADS = 6;            // instructions a wave loads a stage with
+constexpr int TM = 256;             // outputs of a block along m
+constexpr int A_STAGE = TM * 64;    // bytes of 32 k of A
 constexpr int STAGING = 2048;       // a wave's: 16 rows x 64 bf16
 constexpr int NXCD = 8;
-constexpr int BLOCKS = 512;         // two a CU
+constexpr int CUS = 256;
 
 __device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 
@@ -109,15 +107,20 @@ __device__ __forceinline__ int fresh_lane() {
 }
 __device__ __forceinline__ void matrix_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+constexpr int most(int n) { return n > 63 ? 63 : n; }   // the counter's range
+
 // One tile of the launch: expert, its first row and rows, n and m origins, and
 // for DW which matrix.
 struct Meta { int e, start, n, n0, m0, which; };
 
-template <int MODE>
-__global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
+// NJ: a wave's outputs along n in sixteens; 4: two blocks a CU, 8: one.
+template <int MODE, int NJ>
+__global__ void __launch_bounds__(256, NJ == 4 ? 2 : 1) train_gemm_kernel(TrainArgs a) {
   constexpr bool GU = MODE == GATE_UP || MODE == GATE_UP8, DA = MODE == DACT || MODE == DACT8;
   constexpr bool DWS = MODE == DW || MODE == DW_ANY;
   constexpr bool AT = DA || MODE == DX || DWS, BT = DWS;   // operands whose k is the slow axis
+  constexpr int TN = 32 * NJ, B_STAGE = TN * 64, SLOT = A_STAGE + B_STAGE, RING = NJ == 4 ? 3 : 4;
+  constexpr int NB = NJ / 2, LOADS = 4 + NB;               // a wave's load instructions a stage, B's and all
   __shared__ __attribute__((aligned(1024))) char ring[RING * SLOT];
   __shared__ __attribute__((aligned(16))) char staging[4][STAGING];
 
@@ -175,18 +178,18 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
     return DWS ? max(1, (m.n + 63) / 64) : MODE == DX ? 2 * pairs_i : MODE == DOWN ? pairs_i : H / 64;
   };
   // stages of kept rows that follow a tile's own (DACT)
-  constexpr int EXTRA = MODE == DACT ? 8 : MODE == DACT8 ? 4 : 0;
+  constexpr int EXTRA = MODE == DACT ? 2 * NJ : MODE == DACT8 ? NJ : 0;
 
   // ---- loading stream -----------------------------------------------------
-  // Wave w moves rows 64 w..+63 of A and 32 w..+31 of B (k fast), or k 8 w..+7
-  // of either (k slow), in four and two instructions of 1 KiB.  The stream's
+  // Wave w moves rows 64 w..+63 of A and a quarter of B's (k fast), or k 8 w..+7
+  // of either (k slow), in instructions of 1 KiB.  The stream's
   // position is a pair of stages of a tile; it ends with the block's last tile.
   const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&ring[0];
   int dj = 0, dpair = 0, dpairs;
   bool more = true;
   Meta dm = decode(0);
   const char* pa[4];                   // this lane's next 16 bytes, by instruction
-  const char* pb[2];                   // (DW's pa: its column, the rows being looked up)
+  const char* pb[NB];                  // (DW's pa: its column, the rows being looked up)
   int64_t step_a = 0, step_b = 0;
   const int kchunk = (lane & 3) ^ ((lane >> 3) & 3);    // k fast: the 16-byte chunk this lane moves
   const int slow_k0 = 8 * wv + (lane >> 5);             // k slow: row (+ 2 q) this lane moves
@@ -194,10 +197,11 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
     const int k = slow_k0 + 2 * q, f = (k & 3) | (((k >> 3) & 1) << 2);
     return 16 * (((lane & 31) >> 1) ^ f) + 8 * (lane & 1);
   };
-  const int slow_kb0 = 8 * wv + (lane >> 4);            // B's: (+ 4 q)
+  constexpr int BL = TN / 8;                            // B's: lanes of a row
+  const int slow_kb0 = 8 * wv + lane / BL;              // (+ 64 / BL q)
   auto slow_col_b = [&](int q) __attribute__((always_inline)) {
-    const int k = slow_kb0 + 4 * q, f = (k & 3) | (((k >> 3) & 1) << 2);
-    return 16 * (((lane & 15) >> 1) ^ f) + 8 * (lane & 1);
+    const int k = slow_kb0 + 64 / BL * q, f = (k & 3) | (((k >> 3) & 1) << 2);
+    return 16 * (((lane % BL) >> 1) ^ f) + 8 * (lane & 1);
   };
   // DW: x's rows of a stage are looked up through scalar loads a stage ahead
   const __attribute__((address_space(4))) int32_t* perm_s =
@@ -236,8 +240,8 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
       }
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int64_t row = dm.start + min(dm.n0 + 32 * wv + 16 * q + (lane >> 2), dm.n - 1);
+    for (int q = 0; q < NB; ++q) {
+      const int64_t row = dm.start + min(dm.n0 + 16 * NB * wv + 16 * q + (lane >> 2), dm.n - 1);
       if (GU) {
         pb[q] = (const char*)((const bf16*)a.x + (int64_t)(a.perm[row] / a.k) * H + 8 * kchunk);
       } else if (MODE == DOWN) {
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
       } else {
         const bool down = dm.which == 2;
         pb[q] = (const char*)((const bf16*)(down ? a.dy : a.dgu) +
-                              (int64_t)(dm.start + slow_kb0 + 4 * q) * (down ? H : 2 * I) + (down ? 0 : dm.which * I) +
+                              (int64_t)(dm.start + slow_kb0 + 64 / BL * q) * (down ? H : 2 * I) + (down ? 0 : dm.which * I) +
                               min(dm.n0 + slow_col_b(q), (down ? H : I) - 8));
       }
     }
@@ -273,13 +277,13 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
     }
   };
   auto load_b = [&](uint32_t slot, int stage) __attribute__((always_inline)) {
-    const uint32_t to = ring0 + slot + A_STAGE + 2048 * wv;
+    const uint32_t to = ring0 + slot + A_STAGE + 1024 * NB * wv;
     const int k0 = 32 * (MODE == DX && stage >= 2 * pairs_i ? stage - 2 * pairs_i : stage);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < NB; ++q) {
       bool live = true;
       if (MODE == DOWN || MODE == DX) live = k0 + 8 * kchunk < I;
-      if (DWS) live = k0 + slow_kb0 + 4 * q < dm.n;
+      if (DWS) live = k0 + slow_kb0 + 64 / BL * q < dm.n;
       dma16(live ? pb[q] : (const char*)zero_chunk, to + 1024 * q);
       pb[q] += step_b;
     }
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
   // chunk c of row r at c ^ (r % 8)
   auto load_kept = [&](uint32_t slot, int e) __attribute__((always_inline)) {
     const uint32_t to = ring0 + slot + 4096 * wv;
-    const int row0 = dm.n0 + 64 * wn + 16 * (MODE == DACT ? e >> 1 : e);
+    const int row0 = dm.n0 + 16 * NJ * wn + 16 * (MODE == DACT ? e >> 1 : e);
     const int c0 = dm.m0 + 128 * wm + (MODE == DACT ? 64 * (e & 1) : 0);
     const int l = fresh_lane(), c = (l & 7) ^ (l >> 3);
 #pragma unroll
@@ -328,28 +332,28 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
   };
 
   // ---- fragments ----------------------------------------------------------
-  bf16x8_t fa[8], fb[2][4];
-  f32x4_t acc[8][4];
+  bf16x8_t fa[8], fb[2][NJ];
+  f32x4_t acc[8][NJ];
   const uint32_t f = ((r16 >> 2) & 3) | ((kg & 1) << 2);
   const uint32_t straight = (uint32_t)(r16 * 64 + ((kg ^ ((r16 >> 1) & 3)) * 16));
   auto turned = [&](uint32_t pitch, uint32_t first) __attribute__((always_inline)) {
     return (uint32_t)((8 * kg + (r16 >> 2)) * pitch + ((first ^ f) << 5) + (r16 & 3) * 8);
   };
   const uint32_t base_a = ring0 + (AT ? turned(512, 8 * wm) : straight + wm * 8192);
-  const uint32_t base_b = ring0 + A_STAGE + (BT ? turned(256, 4 * wn) : straight + wn * 4096);
+  const uint32_t base_b = ring0 + A_STAGE + (BT ? turned(2 * TN, NJ * wn) : straight + wn * 1024 * NJ);
   auto read_a = [&](int i, uint32_t slot) __attribute__((always_inline)) {
     return AT ? read_turned<512>((base_a ^ (i << 5)) + slot)
               : __builtin_bit_cast(bf16x8_t, read16(base_a + slot + 1024 * i));
   };
   auto read_b = [&](int i, uint32_t slot) __attribute__((always_inline)) {
-    return BT ? read_turned<256>((base_b ^ (i << 5)) + slot)
+    return BT ? read_turned<2 * TN>((base_b ^ (i << 5)) + slot)
               : __builtin_bit_cast(bf16x8_t, read16(base_b + slot + 1024 * i));
   };
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     matrix_done();
   };
   auto after = [&](uint32_t slot) __attribute__((always_inline)) {
@@ -360,22 +364,22 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
   // stage's are read in their places as they fall free; half ODD of the
   // stream's pair is loaded into this stage's slot, whose fragments were read
   // a step ago.  Before the barrier the loads that the next step reads have
-  // landed: all but the last stage's.
+  // landed: of the RING stages beyond the present one, all but the last RING - 2.
 #define STEP(P, ODD)                                                                           \
   {                                                                                            \
     const uint32_t from = after(slot);                                                         \
     _Pragma("unroll") for (int i = 0; i < 8; ++i) {                                            \
-      _Pragma("unroll") for (int j = 0; j < 4; ++j) mac(fa[i], fb[P][j], acc[i][j]);           \
+      _Pragma("unroll") for (int j = 0; j < NJ; ++j) mac(fa[i], fb[P][j], acc[i][j]);           \
       fa[i] = read_a(i, from);                                                                 \
-      if (i < 4) fb[1 - (P)][i] = read_b(i, from);                                             \
+      if (i < NJ) fb[1 - (P)][i] = read_b(i, from);                                            \
       if (i == 1 && more) load_stage(slot, ODD);                                               \
       __builtin_amdgcn_sched_barrier(0);                                                       \
     }                                                                                          \
     wait_lds();                                                                                \
     if (!more) wait_loads<0>();                                                                \
     else if (settled > 0) --settled;                                                           \
-    else if (EXTRA > 0 && dpair >= dpairs) wait_loads<4>();                                    \
-    else wait_loads<LOADS>();                                                                  \
+    else if (EXTRA > 0 && dpair >= dpairs) wait_loads<(RING - 2) * 4>();                       \
+    else wait_loads<(RING - 2) * LOADS>();                                                     \
     if (ODD) { if (more) next_pair(); } else look_up(2 * dpair + 1);                           \
     __builtin_amdgcn_s_barrier();                                                              \
     slot = from;                                                                               \
@@ -388,18 +392,21 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
   uint32_t slot = 0;                   // of the present stage
   set_tile();
   look_up(0);
-  load_stage(0, 0);
-  look_up(1);
-  load_stage(SLOT, 1);
-  next_pair();
-  if (more) load_stage(2 * SLOT, 0);
-  if (more) { look_up(2 * dpair + 1); wait_loads<LOADS>(); } else wait_loads<0>();
+#pragma unroll
+  for (int st = 0; st < RING; ++st)
+    if (more) {
+      load_stage(st * SLOT, st & 1);
+      if (st & 1) next_pair(); else look_up(2 * dpair + 1);
+    }
+  if (!more) wait_loads<0>();
+  else if (EXTRA > 0 && (dpair >= dpairs || dj > 0)) wait_loads<(RING - 2) * 4>();
+  else wait_loads<(RING - 2) * LOADS>();     // stages 0 and 1
   __builtin_amdgcn_s_barrier();
   auto first_fragments = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) fa[i] = read_a(i, slot);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fb[0][j] = read_b(j, slot);
+    for (int j = 0; j < NJ; ++j) fb[0][j] = read_b(j, slot);
     wait_lds();
     __builtin_amdgcn_s_barrier();      // the slot may be filled again
   };
@@ -411,8 +418,8 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
     const int pairs = pairs_of(cm);
     before_tile(cm);
     for (int p = 0; p < pairs; ++p) {
-      STEP(0, 1)
-      STEP(1, 0)
+      STEP(0, RING & 1)
+      STEP(1, 1 - (RING & 1))
     }
     if constexpr (DA) {
       // The kept rows' stages follow: a wave works on its own part of each and
@@ -420,34 +427,36 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
       // all there issues S stores a stage; of any other only loads (four a
       // stage at least) are counted.
       constexpr int S = MODE == DACT ? 6 : 12;
-      const int left = cm.n - cm.n0 - 64 * wn, cols = I - cm.m0 - 128 * wm;
-      const bool full = left >= 64 && cols >= 128;
+      const int left = cm.n - cm.n0 - 16 * NJ * wn, cols = I - cm.m0 - 128 * wm;
+      const bool full = left >= 16 * NJ && cols >= 128;
       matrix_done();
 #pragma unroll
       for (int e = 0; e < EXTRA; ++e) {
         if (e >= 2) {
           if (!more) wait_loads<0>();
-          else if (full) wait_loads<8 + 2 * S>();
-          else wait_loads<8>();
+          else if (full && e == 2) wait_loads<most(4 * (RING - 1) + 2 * S)>();
+          else if (full) wait_loads<most(4 * (RING - 1) + (RING - 1) * S)>();
+          else wait_loads<4 * (RING - 1)>();
         }
         if (left > 0 && cols > 0) gradients(cm, e, slot);
         __builtin_amdgcn_s_barrier();
         if (more) {
-          load_stage(slot, 1 - (e & 1));
-          if (e & 1) look_up(2 * dpair + 1); else next_pair();
+          load_stage(slot, (e + RING) & 1);
+          if ((e + RING) & 1) next_pair(); else look_up(2 * dpair + 1);
         }
         slot = after(slot);
       }
       if (!more) wait_loads<0>();
-      else if (full) wait_loads<LOADS + S>();
-      else wait_loads<LOADS>();
+      else if (dj > cj + 1 || dpair >= dpairs) wait_loads<4 * (RING - 2)>();
+      else if (full) wait_loads<most((RING - 2) * (LOADS + S))>();
+      else wait_loads<(RING - 2) * LOADS>();
       __builtin_amdgcn_s_barrier();
       first_fragments();
     } else {
       // what is in flight lands before the first store, so that the next step
       // need not wait for the stores behind it
       wait_loads<0>();
-      settled = 1;
+      settled = RING - 2;
       matrix_done();
       outputs(cm);
       if constexpr (GU) first_fragments();   // read again: they are not held across the outputs
@@ -460,36 +469,47 @@ __global__ void __launch_bounds__(256, 2) train_gemm_kernel(TrainArgs a) {
 
 }  // namespace
 
-// Persistent grid: two blocks fill a CU; a multiple of the XCDs.
-static int gemm_grid(int64_t tiles) {
-  const int64_t g = std::min<int64_t>(tiles, BLOCKS);
-  return (int)((g + NXCD - 1) / NXCD * NXCD);
+template <int MODE, int NJ>
+static void go(const TrainArgs& a, int64_t tiles, hipStream_t s) {
+  // persistent: the CUs' share, a multiple of the XCDs
+  const int64_t g = std::min<int64_t>(tiles, NJ == 4 ? 2 * CUS : CUS);
+  train_gemm_kernel<MODE, NJ><<<(unsigned)((g + NXCD - 1) / NXCD * NXCD), 256, 0, s>>>(a);
+}
+
+template <int NJ> static void launch(int which, TrainArgs a, int P, hipStream_t s) {
+  constexpr int TN = 32 * NJ;
+  const int64_t row_tiles = P / TN + std::min(a.E, P);       // an upper bound
+  const int64_t mh = (a.H + TM - 1) / TM, mi = (a.I + TM - 1) / TM;
+  if constexpr (NJ == 8) {
+    go<DX, NJ>(a, row_tiles * mh, s);
+  } else if (which == 0) {
+    const int64_t tiles = row_tiles * ((a.I + 127) / 128);
+    if (a.keep8) go<GATE_UP8, NJ>(a, tiles, s);
+    else go<GATE_UP, NJ>(a, tiles, s);
+  } else if (which == 1) {
+    go<DOWN, NJ>(a, row_tiles * mh, s);
+  } else if (which == 2) {
+    if (a.keep8) go<DACT8, NJ>(a, row_tiles * mi, s);
+    else go<DACT, NJ>(a, row_tiles * mi, s);
+  } else if (which == 3) {
+    go<DX, NJ>(a, row_tiles * mh, s);
+  } else {
+    a.n_dw = (a.dw[0] != nullptr) + (a.dw[1] != nullptr) + (a.dw[2] != nullptr);
+    if (!a.n_dw) return;
+    const int64_t tiles = a.E * a.n_dw * std::max(mh * ((a.I + TN - 1) / TN), mi * ((a.H + TN - 1) / TN));
+    if (a.dw_f32 || a.accumulate) go<DW_ANY, NJ>(a, tiles, s);
+    else go<DW, NJ>(a, tiles, s);
+  }
 }
 
 hipError_t launch_train_gemm(int which, const TrainArgs& a, int P, hipStream_t s) {
-  const int64_t row_tiles = P / TN + std::min(a.E, P);       // an upper bound
-  const int64_t mh = (a.H + TM - 1) / TM, mi = (a.I + TM - 1) / TM;
-  if (which == 0) {
-    const int grid = gemm_grid(row_tiles * ((a.I + 127) / 128));
-    if (a.keep8) train_gemm_kernel<GATE_UP8><<<grid, 256, 0, s>>>(a);
-    else train_gemm_kernel<GATE_UP><<<grid, 256, 0, s>>>(a);
-  } else if (which == 1) {
-    train_gemm_kernel<DOWN><<<gemm_grid(row_tiles * mh), 256, 0, s>>>(a);
-  } else if (which == 2) {
-    const int grid = gemm_grid(row_tiles * mi);
-    if (a.keep8) train_gemm_kernel<DACT8><<<grid, 256, 0, s>>>(a);
-    else train_gemm_kernel<DACT><<<grid, 256, 0, s>>>(a);
-  } else if (which == 3) {
-    train_gemm_kernel<DX><<<gemm_grid(row_tiles * mh), 256, 0, s>>>(a);
-  } else {
-    TrainArgs b = a;
-    b.n_dw = (a.dw[0] != nullptr) + (a.dw[1] != nullptr) + (a.dw[2] != nullptr);
-    if (!b.n_dw) return hipSuccess;
-    const int64_t tiles = std::max(mh * ((a.I + TN - 1) / TN), mi * ((a.H + TN - 1) / TN));
-    const int grid = gemm_grid(a.E * b.n_dw * tiles);
-    if (a.dw_f32 || a.accumulate) train_gemm_kernel<DW_ANY><<<grid, 256, 0, s>>>(b);
-    else train_gemm_kernel<DW><<<grid, 256, 0, s>>>(b);
-  }
+  // One block a CU and rows by 256 where the blocks of an XCD stream far more
+  // of the weights than its L2 holds, so that they are fetched again for every
+  // 128 rows (dx at 4096 x 3584, I 2560, 64 experts top-8: 1.54 against 1.88
+  // ms); elsewhere two blocks a CU, one's outputs beside the other's products
+  // (Granite-shaped dx 135 against 157 us, gate and up 149 against 188).
+  if (which == 3 && (int64_t)a.H * a.I >= (4 << 20) && P >= 256 * a.E) launch<8>(which, a, P, s);
+  else launch<4>(which, a, P, s);
   return hipGetLastError();
 }
 

@@ -1,13 +1,13 @@
-  // (part of train_gemm_kernel) A wave's 128 x 64 accumulators: lane (r16, kg)
+  // (part of train_gemm_kernel) A wave's 128 x 16 NJ accumulators: lane (r16, kg)
   // holds of tile (i, j) outputs m = 16 i + 4 kg..+3 of row n = 16 j + r16.
   // They go through LDS in pieces of 16 rows x 64 m, 16-byte chunk c of row r at
   // c ^ (r % 8), and out as runs of 128 bytes of a row.
-  float scales[4];   // DACT8: of rows 16 j + r16, matrix kg % 2, block kg / 2
+  float scales[NJ];   // DACT8: of rows 16 j + r16, matrix kg % 2, block kg / 2
   auto before_tile = [&](const Meta& m) __attribute__((always_inline)) {
     if constexpr (MODE == DACT8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t p = m.start + min(m.n0 + 64 * wn + 16 * j + r16, m.n - 1);
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t p = m.start + min(m.n0 + 16 * NJ * wn + 16 * j + r16, m.n - 1);
         const int b = min((m.m0 + 128 * wm) / 64 + (kg >> 1), a.blocks - 1);
         scales[j] = a.scale[(2 * p + (kg & 1)) * a.blocks + b];
       }
@@ -38,9 +38,9 @@
       const int c0 = m.m0 + 64 * wm, cols = I - c0;
       if (cols <= 0) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         __builtin_amdgcn_sched_barrier(0);
-        const int row0 = m.n0 + 64 * wn + 16 * j, left = m.n - row0;
+        const int row0 = m.n0 + 16 * NJ * wn + 16 * j, left = m.n - row0;
         if (left <= 0) break;
         const int64_t p0 = m.start + row0;
         uint32_t top[2] = {0, 0};
@@ -110,8 +110,8 @@
       bf16* out = MODE == DOWN ? (bf16*)a.y + (int64_t)m.start * H : MODE == DX ? (bf16*)a.dx + (int64_t)m.start * H
                   : (bf16*)a.dw[m.which] + (int64_t)m.e * I * H;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row0 = m.n0 + 64 * wn + 16 * j;
+      for (int j = 0; j < NJ; ++j) {
+        const int row0 = m.n0 + 16 * NJ * wn + 16 * j;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           __builtin_amdgcn_sched_barrier(0);
@@ -131,9 +131,9 @@
     } else {
       const int M = m.which == 2 ? I : H, N = m.which == 2 ? H : I;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         __builtin_amdgcn_sched_barrier(0);
-        const int row = m.n0 + 64 * wn + 16 * j + r16;
+        const int row = m.n0 + 16 * NJ * wn + 16 * j + r16;
         const int64_t at = (int64_t)m.e * I * H + (int64_t)row * M + m.m0 + 128 * wm + 4 * kg;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -160,7 +160,7 @@
   // DACT: stage e of kept rows, lying in this wave's part of a slot
   auto gradients = [&](const Meta& m, int e, uint32_t at_slot) __attribute__((always_inline)) {
     const int j = MODE == DACT ? e >> 1 : e, l = fresh_lane(), r16 = l & 15, kg = l >> 4;
-    const int row0 = m.n0 + 64 * wn + 16 * j, left = m.n - row0;
+    const int row0 = m.n0 + 16 * NJ * wn + 16 * j, left = m.n - row0;
     const uint32_t at = ring0 + at_slot + 4096 * wv + r16 * 128;
 #pragma unroll
     for (int z = 0; z < (MODE == DACT ? 1 : 2); ++z) {

@@ -60,7 +60,6 @@ __device__ __forceinline__ void gated_grad(float g, float u, float da, float& a,
   dg = da * u * (s * (1.0f + (g - gs)));
 }
 
-hipError_t launch_train_gemm(int mode, const TrainArgs& a, int P, hipStream_t s);
 int64_t train_ws_bytes(const moe_dims_t& d, int64_t T);
 hipError_t launch_ffn_train(const TrainArgs& a, int P, bool is_bf16, hipStream_t s);
 hipError_t launch_ffn_backward(const TrainArgs& a, int P, bool is_bf16, hipStream_t s);

@@ -248,20 +248,30 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
   };
   auto col_a = [&](int q) __attribute__((always_inline)) { return slow_col(slow_a + 64 / AL * q, lane % AL, TM); };
   auto col_b = [&](int q) __attribute__((always_inline)) { return slow_col(slow_b + 64 / BL * q, lane % BL, TN); };
-  // DW: x's rows of a stage are looked up through scalar loads a stage ahead
+  // DW: the pairs of a wave's rows of x are looked up through scalar loads a
+  // step before they are loaded; perm_s is a.perm in the constant address space
+  typedef int32_t ints_t __attribute__((ext_vector_type(KW), aligned(4)));
   const __attribute__((address_space(4))) int32_t* perm_s =
       (const __attribute__((address_space(4))) int32_t*)(uintptr_t)a.perm;
   // p / k, p < 2^25: the high word of p ceil(2^32 / k)
   const uint32_t per_k = (uint32_t)(((1ull << 32) + a.k - 1) / a.k);
-  int rows[KW];
+  ints_t pairs_at;
   auto look_up = [&](int stage) __attribute__((always_inline)) {
     if (!DWS) return;
+    const int p = dm.start + BK * stage + KW * wv;
+    if (dm.which == 2 || dm.n == 0) {    // rows of the sorted buffers themselves
 #pragma unroll
-    for (int i = 0; i < KW; ++i) {
-      const int p = max(0, min(dm.start + BK * stage + KW * wv + i, a.pairs - 1));
-      const uint32_t t = dm.which == 2 || dm.n == 0 ? 0u : (uint32_t)perm_s[p];
-      rows[i] = dm.which == 2 ? p : (int)(a.k == 1 ? t : __umulhi(t, per_k));
+      for (int i = 0; i < KW; ++i) pairs_at[i] = p + i;
+    } else if (p + KW <= a.pairs) {
+      pairs_at = *(const __attribute__((address_space(4))) ints_t*)(perm_s + p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < KW; ++i) pairs_at[i] = perm_s[min(p + i, a.pairs - 1)];
     }
+  };
+  auto row_at = [&](int i) __attribute__((always_inline)) {
+    const uint32_t p = (uint32_t)pairs_at[i];
+    return (int)(dm.which == 2 || a.k == 1 ? p : __umulhi(p, per_k));
   };
   auto set_tile = [&]() __attribute__((always_inline)) {
     const int64_t we = (int64_t)dm.e * I * H;
@@ -314,9 +324,9 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
       const char* p = pa[q];
       if constexpr (DWS) {
         constexpr int R = 64 / AL;                        // rows of an instruction
-        int row = rows[R * q];
+        int row = row_at(R * q);
 #pragma unroll
-        for (int i = 1; i < R; ++i) row = lane >= i * AL ? rows[R * q + i] : row;
+        for (int i = 1; i < R; ++i) row = lane >= i * AL ? row_at(R * q + i) : row;
         p += (int64_t)row * step_a;
       } else {
         pa[q] += step_a;
@@ -424,19 +434,22 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
 #define STEP(P, ODD)                                                                           \
   {                                                                                            \
     const uint32_t from = after(slot);                                                         \
-    _Pragma("unroll") for (int i = 0; i < MI; ++i) {                                            \
+    const bool loading = more, keeping = EXTRA > 0 && dpair >= dpairs;                         \
+    _Pragma("unroll") for (int i = 0; i < MI; ++i) {                                           \
       _Pragma("unroll") for (int j = 0; j < NJ; ++j) mac<T>(fa[i], fb[P][j], acc[i][j]);       \
       fa[i] = read_a(i, from);                                                                 \
       if (i < NJ) fb[1 - (P)][i] = read_b(i, from);                                            \
-      if (i == 1 && more) load_stage(slot, ODD);                                               \
+      if (i == 1 && loading) {                                                                 \
+        load_stage(slot, ODD);                                                                 \
+        if (ODD) next_pair(); else look_up(2 * dpair + 1);                                     \
+      }                                                                                        \
       __builtin_amdgcn_sched_barrier(0);                                                       \
     }                                                                                          \
     wait_lds();                                                                                \
-    if (!more) wait_loads<0>();                                                                \
+    if (!loading) wait_loads<0>();                                                             \
     else if (settled > 0) --settled;                                                           \
-    else if (EXTRA > 0 && dpair >= dpairs) wait_loads<(RING - 2) * FEWEST>();                  \
+    else if (keeping) wait_loads<(RING - 2) * FEWEST>();                                       \
     else wait_loads<(RING - 2) * LOADS>();                                                     \
-    if (ODD) { if (more) next_pair(); } else look_up(2 * dpair + 1);                           \
     __builtin_amdgcn_s_barrier();                                                              \
     slot = from;                                                                               \
   }

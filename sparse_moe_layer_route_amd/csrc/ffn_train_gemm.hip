@@ -89,8 +89,11 @@ template <> struct frag<float> {
 
 // c += a b.  The accumulators stay in the accumulation half of the register
 // file: left to itself the compiler moves them to the other and back in every
-// step.  Before they are read, and after they are cleared, matrix_done waits
-// for longer than any hazard between these instructions takes.
+// step.  It knows nothing of the hazards between these instructions and others:
+// the accumulators are cleared by a matrix instruction too (0 * 0 + 0), never
+// by moves that the compiler might place next to one, and before they are
+// read, and after they are cleared, matrix_done waits for longer than any of
+// them takes to write its results.
 template <typename T> __device__ __forceinline__ void mac(const u32x4& a, const u32x4& b, f32x4_t& c) {
   if constexpr (sizeof(T) == 2) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
@@ -99,6 +102,9 @@ template <typename T> __device__ __forceinline__ void mac(const u32x4& a, const 
     for (int q = 0; q < 4; ++q)      // k = 4 kg + q of the four lane groups kg
       asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+a"(c) : "v"(a[q]), "v"(b[q]));
   }
+}
+__device__ __forceinline__ void clear_acc(const u32x4& zeros, f32x4_t& c) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %1, 0" : "=a"(c) : "v"(zeros));
 }
 __device__ __forceinline__ void matrix_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 __device__ __forceinline__ float acc_read(float v) {
@@ -246,8 +252,6 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
     const int f = (k & 3) | (width >= 128 ? ((k >> 3) & 1) << 2 : 0);
     return 16 * ((j >> 1) ^ f) + 8 * (j & 1);
   };
-  auto col_a = [&](int q) __attribute__((always_inline)) { return slow_col(slow_a + 64 / AL * q, lane % AL, TM); };
-  auto col_b = [&](int q) __attribute__((always_inline)) { return slow_col(slow_b + 64 / BL * q, lane % BL, TN); };
   // DW: the pairs of a wave's rows of x are looked up through scalar loads a
   // step before they are loaded; perm_s is a.perm in the constant address space
   typedef int32_t ints_t __attribute__((ext_vector_type(KW), aligned(4)));
@@ -275,6 +279,11 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
   };
   auto set_tile = [&]() __attribute__((always_inline)) {
     const int64_t we = (int64_t)dm.e * I * H;
+    // from the lane afresh: held since the last tile these would cost registers
+    const int lane = fresh_lane(), kchunk = (lane & 3) ^ ((lane >> 3) & 3);
+    const int slow_a = KW * wv + lane / AL, slow_b = KW * wv + lane / BL;
+    auto col_a = [&](int q) __attribute__((always_inline)) { return slow_col(slow_a + 64 / AL * q, lane % AL, TM); };
+    auto col_b = [&](int q) __attribute__((always_inline)) { return slow_col(slow_b + 64 / BL * q, lane % BL, TN); };
 #pragma unroll
     for (int q = 0; q < NA; ++q) {
       const int r = 16 * NA * wv + 16 * q + (lane >> 2);  // k fast: row of the tile
@@ -414,10 +423,12 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
     return BT ? frag<T>::template turned<TN * SZ>((base_b ^ (i << TILE_BITS)) + slot) : read16(base_b + slot + 1024 * i);
   };
   auto clear = [&]() __attribute__((always_inline)) {
+    u32x4 zeros = {0u, 0u, 0u, 0u};
+    asm volatile("s_nop 3" : "+v"(zeros));       // written by moves: let them settle
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NJ; ++j) clear_acc(zeros, acc[i][j]);
     matrix_done();
   };
   auto after = [&](uint32_t slot) __attribute__((always_inline)) {
@@ -597,7 +608,7 @@ void launch_any(int which, const TrainArgs& a, int P, bool is_bf16, hipStream_t 
   if (is_bf16) {
     if (which == 3 && (int64_t)a.H * a.I >= (4 << 20) && P >= 256 * a.E)
       go<DX, Shape<bf16, 2, 2, 8, 8>>(a, (P / 256 + e) * mh, s);
-    else if (tiles > CUS / 2 && (!rows || !few || (which == 3 && tiles >= 2 * CUS)))
+    else if (tiles > (which == 0 ? CUS / 2 : 160) && (!rows || !few || (which == 3 && tiles >= 2 * CUS)))
       launch<Shape<bf16, 2, 2, 8, 4>>(which, a, P, s);
     else if (few && (which == 1 || which == 2))
       launch<Shape<bf16, 1, 4, 4, 1>>(which, a, P, s);

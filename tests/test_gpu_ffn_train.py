@@ -61,7 +61,7 @@ def near(got, want, tol, what):
 class Case:
     """Inputs of one batch: pairs sorted by expert, weights, gradients."""
 
-    def __init__(self, T, H, I, E, k, dtype, keep, miss=0.0, seed=0, counts=None):
+    def __init__(self, T, H, I, E, k, dtype, keep, miss=0.0, seed=0, counts=None, pack=True):
         g = gen(1000 * T + H + I + seed)
         self.T, self.H, self.I, self.E, self.k, self.dtype, self.keep = T, H, I, E, k, dtype, keep
         self.P = P = T * k
@@ -88,7 +88,12 @@ class Case:
         kept = randn(g, P, 2, I, dtype=dtype)
         self.blocks = -(-I // 64)
         self.scale = None
-        if keep == "int8":
+        if keep == "int8" and not pack:        # by the library, which test_rows8 checks
+            self.kept = torch.empty(P, 2, I, dtype=torch.int8, device="cuda")
+            self.scale = torch.empty(P, 2, self.blocks, device="cuda")
+            M.moe_rows_pack8(2 * P, I, kept.view(2 * P, I), self.kept.view(2 * P, I), self.scale.view(2 * P, -1))
+            self.scale[self.n:] = float("nan")
+        elif keep == "int8":
             c, s = FO.pack8(f64(kept).reshape(2 * P, I))
             self.kept = torch.from_numpy(c.reshape(P, 2, I)).to(torch.int8).cuda()
             self.scale = torch.from_numpy(s.reshape(P, 2, self.blocks)).float().cuda()

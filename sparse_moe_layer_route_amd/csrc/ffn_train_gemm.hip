@@ -59,6 +59,13 @@ template <int N> __device__ __forceinline__ void wait_loads() {
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// All waves of the block; no LDS access moves to the other side.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 typedef __attribute__((address_space(3))) u32x4 lds16_t;
 typedef __attribute__((address_space(3))) u32x2 lds8_t;
 typedef __attribute__((address_space(3))) uint32_t lds4_t;
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
     else if (settled > 0) --settled;                                                           \
     else if (keeping) wait_loads<(RING - 2) * FEWEST>();                                       \
     else wait_loads<(RING - 2) * LOADS>();                                                     \
-    __builtin_amdgcn_s_barrier();                                                              \
+    meet();                                                                                    \
     slot = from;                                                                               \
   }
 
@@ -480,14 +487,14 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
     }
   if (!more) wait_loads<0>();
   else wait_loads<(RING - 2) * FEWEST>();                // stages 0 and 1
-  __builtin_amdgcn_s_barrier();
+  meet();
   auto first_fragments = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) fa[i] = read_a(i, slot);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) fb[0][j] = read_b(j, slot);
     wait_lds();
-    __builtin_amdgcn_s_barrier();      // the slot may be filled again
+    meet();      // the slot may be filled again
   };
   first_fragments();
   clear();
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
           else wait_loads<FEWEST * (RING - 1)>();
         }
         if (left > 0 && cols > 0) gradients(cm, e, slot);
-        __builtin_amdgcn_s_barrier();
+        meet();
         if (more) {
           load_stage(slot, (e + RING) & 1);
           if ((e + RING) & 1) next_pair(); else look_up(2 * dpair + 1);
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
       if (!more) wait_loads<0>();
       else if (full) wait_loads<(RING - 2) * (FEWEST + ST)>();
       else wait_loads<(RING - 2) * FEWEST>();
-      __builtin_amdgcn_s_barrier();
+      meet();
       first_fragments();
     } else {
       // what is in flight lands before the first store, so that the next steps

@@ -438,6 +438,32 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
       for (int j = 0; j < NJ; ++j) clear_acc(zeros, acc[i][j]);
     matrix_done();
   };
+  // fp32: what the accumulators have reached is put aside every FLUSH pairs of
+  // stages (512 k), so that a long sum's error grows with the root of its parts
+  // rather than of its terms (4128 terms: 1.2e-6 of the result without)
+  constexpr int FLUSH = 16;
+  f32x4_t aside[SZ == 4 ? MI : 1][SZ == 4 ? NJ : 1] = {};
+  auto put_aside = [&]() __attribute__((always_inline)) {
+    if constexpr (SZ == 4) {
+      matrix_done();
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          float v[4];
+          acc_read4(acc[i][j], v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) aside[i][j][q] += v[q];
+        }
+      clear();
+    }
+  };
+  auto sum4 = [&](int i, int j, float (&v)[4]) __attribute__((always_inline)) {
+    acc_read4(acc[i][j], v);
+    if constexpr (SZ == 4)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += aside[i][j][q];
+  };
   auto after = [&](uint32_t slot) __attribute__((always_inline)) {
     return slot == (RING - 1) * SLOT ? 0u : slot + SLOT;
   };
@@ -506,6 +532,7 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
     for (int p = 0; p < pairs; ++p) {
       STEP(0, RING & 1)
       STEP(1, 1 - (RING & 1))
+      if (SZ == 4 && (p + 1) % FLUSH == 0 && p + 1 < pairs) put_aside();
     }
     if constexpr (EXTRA > 0) {
       // The kept rows' stages follow: a wave works on its own part of each and
@@ -546,17 +573,19 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
       if constexpr (GU || DA) first_fragments();   // read again: they are not held across the outputs
     }
     clear();
+    if constexpr (SZ == 4)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) aside[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
   wait_loads<0>();                     // no load outlives the block's LDS
 #undef STEP
 }
 
 template <int MODE, typename S> void go(const TrainArgs& a, int64_t tiles, hipStream_t s) {
-  // Persistent: the CUs' share, a multiple of the XCDs.  The turned W_d in
-  // pieces of 128 bytes streams faster with two blocks a CU than with four
-  // (64 tokens, H 2048, I 1408, 64 experts: 104 against 120 us).
-  const bool da = MODE == DACT || MODE == DACT8;
-  const int64_t g = std::min<int64_t>(tiles, (da ? std::min(2, S::PER_CU) : S::PER_CU) * CUS);
+  // Persistent: the CUs' share, a multiple of the XCDs.
+  const int64_t g = std::min<int64_t>(tiles, S::PER_CU * CUS);
   train_gemm_kernel<MODE, S><<<(unsigned)((g + NXCD - 1) / NXCD * NXCD), 256, 0, s>>>(a);
 }
 
@@ -600,10 +629,11 @@ template <typename S> void launch(int which, TrainArgs a, int P, hipStream_t s) 
 //            (4096 tokens, H 3584, I 2560, 64 experts top-8: 1540 against 1880)
 //   128x64   few tiles: shared down 26, dact 34, dx 46 (256x128: 30, 54, 59);
 //            few gate/up 72 (88)
-//   64x64    fewer: few down 44, dact 104 (128x64: 49, 121); small down 15, dx
-//            33, dact 14 (23, 50, 21)
+//   64x64    fewer: few down 44 (128x64: 49; dact 126 with either); small down
+//            15, dx 31, dact 14, dw 27 (23, 50, 21, 32)
 // fp32 is bound by its matrix instructions, a sixteenth as fast, and takes
-// the smaller shapes for longer (wide: 1691 against 2014 with 256x128).
+// the smaller shapes throughout, whose sums can be put aside (the largest
+// batches lose by it: wide 2014, with 256x128 1691).
 void launch_any(int which, const TrainArgs& a, int P, bool is_bf16, hipStream_t s) {
   const bool rows = which != 4, few = P < 64 * a.E;
   const int64_t e = std::min(a.E, P), mh = (a.H + 255) / 256, mi = (a.I + 255) / 256;
@@ -617,14 +647,12 @@ void launch_any(int which, const TrainArgs& a, int P, bool is_bf16, hipStream_t 
       go<DX, Shape<bf16, 2, 2, 8, 8>>(a, (P / 256 + e) * mh, s);
     else if (tiles > (which == 0 ? CUS / 2 : 160) && (!rows || !few || (which == 3 && tiles >= 2 * CUS)))
       launch<Shape<bf16, 2, 2, 8, 4>>(which, a, P, s);
-    else if (few && (which == 1 || which == 2))
+    else if (few && which == 1)
       launch<Shape<bf16, 1, 4, 4, 1>>(which, a, P, s);
     else
       launch<Shape<bf16, 1, 4, 8, 1>>(which, a, P, s);
   } else {
-    if (tiles >= 4 * CUS)
-      launch<Shape<float, 2, 2, 8, 4>>(which, a, P, s);
-    else if (rows && which != 0 && row_tiles(64, 128) < 2 * CUS)
+    if (which != 0 && (rows ? row_tiles(64, 128) : 2 * tiles) < 2 * CUS)
       launch<Shape<float, 1, 4, 4, 1>>(which, a, P, s);
     else
       launch<Shape<float, 1, 4, 8, 1>>(which, a, P, s);

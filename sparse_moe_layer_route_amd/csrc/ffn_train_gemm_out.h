@@ -94,7 +94,7 @@
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float d[4], h[4], dg[4], du[4];
-      acc_read4(acc[(4 * half + i) % MI][j], d);
+      sum4((4 * half + i) % MI, j, d);
 #pragma unroll
       for (int q = 0; q < 4; ++q) gated_grad(g[i][q], u[i][q], d[q], h[q], dg[q], du[q]);
       take(hv, i, h);
@@ -133,7 +133,7 @@
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float v[4];
-              acc_read4(acc[4 * w + i][j], v);
+              sum4(4 * w + i, j, v);
               if (16 * i < cols)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) top = max(top, __float_as_uint(v[q]) & 0x7FFFFFFFu);
@@ -146,7 +146,7 @@
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float v[4];
-              acc_read4(acc[4 * w + i][j], v);
+              sum4(4 * w + i, j, v);
               code[w][i] = pack8x4(v, inv);
             }
           }
@@ -155,8 +155,8 @@
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float g[4], u[4], h[4];
-          acc_read4(acc[i][j], g);
-          acc_read4(acc[i + 4][j], u);
+          sum4(i, j, g);
+          sum4(i + 4, j, u);
 #pragma unroll
           for (int q = 0; q < 4; ++q) h[q] = silu_f(g[q]) * u[q];
           take(hv, i, h);
@@ -202,7 +202,7 @@
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float v[4];
-            acc_read4(acc[4 * half + i][j], v);
+            sum4(4 * half + i, j, v);
             take(w, i, v);
           }
           store(w, out + (int64_t)row0 * M + c0, M, N - row0, M - c0);
@@ -224,7 +224,7 @@
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
           float v[4], was[4];
-          acc_read4(acc[i][j], v);
+          sum4(i, j, v);
           if (row >= N || m.m0 + 16 * MI * wm + 16 * i >= M) continue;
           if (a.dw_f32) {
             float* to = (float*)a.dw[m.which] + at + 16 * i;

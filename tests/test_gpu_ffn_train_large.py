@@ -92,9 +92,9 @@ LARGE = [  # T, H, I, E, k, dtype, keep, missing
     (8192, 64, 2576, 1, 1, "bf16", "int8", 0.1),
     (600, 2048, 2064, 1, 1, "bf16", "rows", 0.0),        # dx by 256 x 256
     (777, 2112, 2000, 2, 2, "bf16", "int8", 0.1),
-    (8100, 4096, 80, 1, 1, "f32", "rows", 0.0),          # fp32 by 256 x 128: y and dx
-    (8100, 64, 4096, 1, 1, "f32", "int8", 0.0),          # gate and up, their gradients
-    (300, 512, 528, 64, 4, "f32", "rows", 0.2),          # the weights'
+    (8100, 4096, 80, 1, 1, "f32", "rows", 0.0),          # fp32, the large ends of its shapes
+    (8100, 64, 4096, 1, 1, "f32", "int8", 0.0),    
+    (300, 512, 528, 64, 4, "f32", "rows", 0.2),  
 ]
 
 
@@ -126,3 +126,39 @@ def test_large_gradients_added(dtype, dw):
     c.backward(twice, accumulate_dw=True)
     # v + v is exact in either type
     assert all(torch.equal(2 * a, b) for a, b in zip(once[1:], twice[1:]))
+
+
+# Long fp32 sums are put aside every 512 terms.  With partial sums that wander
+# (independent terms of mean zero) n sequential adds, each off by at most 2^-24 of
+# the partial sum, give an error of 2^-24 sqrt(n / 2) of the result in the root of
+# the mean square; by parts of 512 it is sqrt(512 / 2 + n / 1024).  What stands
+# before the sum (64 terms, the activation) adds less than 8 in these units.
+def long_bound(n):
+    return 2.0 ** -24 * ((256 + n / 1024) ** 0.5 + 8)
+
+
+@pytest.mark.parametrize("T,H,I", [(16, 64, 32768), (100, 64, 16400)])
+def test_long_sums_over_channels(T, H, I):
+    c = Case(T, H, I, 1, 1, "f32", "rows", 0.0, pack=False)
+    y, kept, _ = c.train()
+    e, r, x = next(segments(c))
+    wg, wu, wd = (c.w[n][e].double() for n in ("w_gate", "w_up", "w_down"))
+    g, u = x @ wg.T, x @ wu.T
+    want = (torch.nn.functional.silu(g) * u) @ wd.T
+    assert float((y[r].double() - want).norm() / want.norm()) <= long_bound(I)
+    g, u = (v[r] for v in kept_values(c, c.kept, c.scale))
+    da, s = c.dy[r].double() @ wd, torch.sigmoid(g)
+    want = (da * u * s * (1 + g * (1 - s))) @ wg + (da * g * s) @ wu
+    got = c.backward()[0][r].double()
+    assert float((got - want).norm() / want.norm()) <= long_bound(2 * I)
+
+
+def test_long_sums_over_rows():
+    c = Case(20000, 64, 80, 1, 1, "f32", "rows", 0.0, pack=False)
+    got = c.backward()
+    e, r, x = next(segments(c))
+    g, u = (v[r] for v in kept_values(c, c.kept, c.scale))
+    dy, s = c.dy[r].double(), torch.sigmoid(g)
+    da = dy @ c.w["w_down"][e].double()
+    for v, want in zip(got[1:], ((da * u * s * (1 + g * (1 - s))).T @ x, (da * g * s).T @ x, dy.T @ (g * s * u))):
+        assert float((v[e].double() - want).norm() / want.norm()) <= long_bound(c.n)

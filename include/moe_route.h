@@ -546,7 +546,7 @@ moe_status_t moe_distill_topk(int32_t T, int32_t V, int64_t ld, int32_t K, const
  *   src, dst: rows of cols elements of dtype, ld from one to the next (ld >=
  *     cols; what lies between is neither read nor written).
  *   codes [rows][cols] int8, scale [rows][ceil(cols / 64)] fp32.
- * Limits: cols <= 2^24, ld <= 2^31, rows and rows * ceil(cols / 64) < 2^28.
+ * Limits: cols <= 2^24, ld <= 2^31, rows * ceil(cols / 64) <= 2^28 - 16.
  * rows = 0 enqueues nothing. */
 moe_status_t moe_rows_pack8(int64_t rows, int64_t cols, int64_t ld, const void* src,
                             moe_dtype_t dtype, int8_t* codes, float* scale, void* stream);

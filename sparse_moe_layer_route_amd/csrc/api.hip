@@ -833,9 +833,9 @@ moe_status_t check_rows8(int64_t rows, int64_t cols, int64_t ld, moe_dtype_t dty
   if (rows < 0 || cols <= 0 || ld < cols) return MOE_EINVAL;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
   const int64_t blocks = (cols + kKeepBlock - 1) / kKeepBlock;
-  // lanes over all blocks are counted in 32 bits by the launch
+  // a launch has fewer than 2^32 lanes, 16 for each block, in groups of 256
   if (cols > (1 << 24) || ld > (int64_t(1) << 31) || rows >= (int64_t(1) << 28) ||
-      rows * blocks >= (int64_t(1) << 28))
+      rows * blocks > (int64_t(1) << 28) - 16)
     return MOE_EUNSUPPORTED;
   return MOE_OK;
 }

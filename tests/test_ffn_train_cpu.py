@@ -177,7 +177,7 @@ def rows8(fn, rows=4, cols=100, ld=128, src=A, dtype=1, codes=A + STEP, scale=A 
     (dict(rows=-1), 1), (dict(cols=0), 1), (dict(ld=99), 1), (dict(dtype=2), 1), (dict(src=None), 1),
     (dict(codes=None), 1), (dict(scale=None), 1), (dict(src=A + 8), 1), (dict(codes=A + STEP + 4), 1),
     (dict(cols=(1 << 24) + 1, ld=1 << 25), 2), (dict(ld=(1 << 31) + 1), 2), (dict(rows=1 << 28), 2),
-    (dict(rows=1 << 27), 2), (dict(codes=A), 1), (dict(scale=A + 16), 1)])
+    (dict(rows=(1 << 28) - 15, cols=1), 2), (dict(rows=1 << 27), 2), (dict(codes=A), 1), (dict(scale=A + 16), 1)])
 def test_rows8_refused(fn, kw, status):
     assert rows8(fn, **kw) == status
 

@@ -484,6 +484,18 @@ def test_rows8_many_and_other_strides():
     assert bool((dst.view(rows, ld)[:, cols:] == MARK).all())
 
 
+def test_rows8_the_most_blocks():
+    rows = (1 << 28) - 16
+    src = (torch.arange(rows, dtype=torch.int32, device="cuda") % 251 - 125).to(torch.bfloat16).view(rows, 1)
+    codes = torch.zeros(rows, 1, dtype=torch.int8, device="cuda")
+    scale = torch.full((rows, 1), float("nan"), device="cuda")
+    M.moe_rows_pack8(rows, 1, src, codes, scale)
+    assert torch.equal(codes, (127 * torch.sign(src)).to(torch.int8))
+    got = torch.empty_like(src)
+    M.moe_rows_unpack8(rows, 1, codes, scale, got)
+    assert torch.equal(got, src)         # 127 (top / 127) rounds to top in bf16
+
+
 def test_refusals_with_gpu_tensors():
     c = Case(4, 64, 32, 2, 1, "bf16", "rows")
     y, kept, _ = c.outputs()

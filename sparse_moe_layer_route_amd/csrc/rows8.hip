@@ -19,21 +19,37 @@ __device__ __forceinline__ float load1(const bf16* p) { return bf16_to_f(p->b); 
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(bf16* p, float v) { p->b = f_to_bf16(v); }
 
-// Codes of N values.  v * inv is off by up to 2^-16; where that could decide
-// which of two codes is nearer, 64 bits do: the product is exact in them, so a
-// tie is one.
+// Codes of N values, in the low byte of c: the sum with 1.5 * 2^23 rounds
+// v * inv to an integer and leaves it there.  inv is rounded, so the product is
+// off by up to 2^-16; where that could decide which of two codes is nearer, the
+// middle between them does: 254 |v| and (2 m + 1) top are exact in 64 bits, so
+// a tie is one.
 template <int N>
-__device__ __forceinline__ void codes_of(const float (&v)[N], float top, float inv, int (&c)[N]) {
-  bool close = false;
+__device__ __forceinline__ void codes_of(const float (&v)[N], float top, float inv, uint32_t (&c)[N]) {
+  constexpr float SHIFT = 0x1.8p23f, CLOSE = 0.5f - 0x1p-14f;
+  float far = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float f = v[i] * inv, q = rintf(f);
-    c[i] = inv > 0.0f ? (int)q : 0;
-    close |= fabsf(f - q) > 0.5f - 0x1p-14f;
+    const float b = fmaf(v[i], inv, SHIFT);
+    c[i] = __float_as_uint(b);
+    far = fmaxf(far, fabsf(fmaf(v[i], inv, SHIFT - b)));
   }
-  if (close && inv > 0.0f) {
-    for (int i = 0; i < N; ++i) c[i] = (int)rint((double)v[i] * 127.0 / (double)top);
+  if (far > CLOSE && inv > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float f = fabsf(v[i]) * inv, m = floorf(f);
+      if (fabsf(f - m - 0.5f) < 0x1p-13f) {
+        const double past = 254.0 * (double)fabsf(v[i]) - (double)(2.0f * m + 1.0f) * (double)top;
+        const int n = (int)m, near = past > 0.0 || (past == 0.0 && (n & 1)) ? n + 1 : n;
+        c[i] = (uint32_t)(v[i] < 0.0f ? -near : near);
+      }
+    }
   }
+}
+
+// The low bytes of four.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(b, a, 0x0C0C0400u) | __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
 }
 
 // blocks: of a row; total: of all rows.  VEC: four lanes a block, else 16.
@@ -76,7 +92,7 @@ rows_pack8_kernel(const T* __restrict__ src, int64_t ld, int cols, uint32_t bloc
   }
   float s;
   const float inv = pack8_inverse(__uint_as_float(top), s);
-  int c[N];
+  uint32_t c[N];
   codes_of(v, __uint_as_float(top), inv, c);
   if (!on) return;
   if (sub == 0) scale[blk] = s;
@@ -86,13 +102,12 @@ rows_pack8_kernel(const T* __restrict__ src, int64_t ld, int cols, uint32_t bloc
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = (c[4 * i] & 0xFF) | (c[4 * i + 1] & 0xFF) << 8 | (c[4 * i + 2] & 0xFF) << 16 |
-             (uint32_t)c[4 * i + 3] << 24;
+      w[i] = inv > 0.0f ? low_bytes(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]) : 0u;
     *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (col + 16 * i < cols) to[16 * i] = (int8_t)c[i];
+      if (col + 16 * i < cols) to[16 * i] = inv > 0.0f ? (int8_t)c[i] : 0;
   }
 }
 

@@ -58,7 +58,7 @@ def hazards(code):
     return bad
 
 
-def test_checker_sees_both_kinds():
+def test_the_reading_sees_both_kinds():
     assert hazards(["v_accvgpr_write_b32 a7, v4", "v_mfma_f32_16x16x32_bf16 a[4:7], v[8:11], v[0:3], a[4:7]"])
     assert hazards(["v_mfma_f32_16x16x32_bf16 a[4:7], v[8:11], v[0:3], a[4:7]", "s_nop 15",
                     "v_accvgpr_read_b32 v1, a5"])

@@ -421,6 +421,61 @@ ROWS8 = [  # rows, cols, ld, dtype
 ]
 
 
+@pytest.mark.parametrize("T,H,I,E,k,dtype,keep", [(70, 128, 96, 4, 2, "bf16", "int8"), (70, 128, 96, 4, 2, "f32", "rows"),
+                                                   (1500, 512, 1024, 4, 2, "bf16", "rows")])
+def test_values_that_are_not_finite_stay_where_they_belong(T, H, I, E, k, dtype, keep):
+    """A token whose pairs are not computed reaches nothing; an infinity in one
+    pair's row reaches that row's outputs and its expert's weights alone."""
+    c = Case(T, H, I, E, k, dtype, keep, 0.3, pack=False)
+    clean, grads = c.train(), c.backward()
+    used = torch.zeros(T, dtype=torch.bool)
+    used[torch.div(c.perm[:c.n].cpu().long(), k, rounding_mode="floor")] = True
+    assert not bool(used.all())
+    c.x[~used.cuda()] = float("nan")
+    for a, b in zip(clean, c.train()):
+        assert a is b or torch.equal(a, b)
+    assert all(torch.equal(a, b) for a, b in zip(grads, c.backward()))
+    off = c.offsets.tolist()
+    p, e = off[2] - 1, 1                  # the last row of expert 1
+    token = int(c.perm[p]) // k
+    row = c.dy[p, 5].clone()
+    c.dy[p, 5] = float("inf")
+    got = c.backward()
+    keep_rows = torch.arange(c.P, device="cuda") != p
+    assert torch.equal(got[0][keep_rows], grads[0][keep_rows]) and not bool(got[0][p].isfinite().any())
+    for a, b in zip(got[1:], grads[1:]):
+        others = [i for i in range(E) if i != e]
+        assert torch.equal(a[others], b[others]) and not bool(a[e].isfinite().all())
+    c.dy[p, 5] = row
+    c.x[token, 3] = float("inf")
+    mine = (torch.div(c.perm[:c.n].long(), k, rounding_mode="floor") == token).nonzero().flatten()
+    y, kept, scale = c.train()
+    others = torch.ones(c.P, dtype=torch.bool, device="cuda")
+    others[mine] = False
+    assert torch.equal(y[others], clean[0][others]) and torch.equal(kept[others], clean[1][others])
+    assert not bool(y[mine].isfinite().any())
+    if scale is not None:                 # comes back as NaN
+        assert torch.equal(scale[others], clean[2][others]) and bool(scale[mine].isnan().all())
+        assert bool((kept[mine] == 0).all())
+
+
+@pytest.mark.parametrize("dtype,keep", [("bf16", "int8"), ("f32", "rows")])
+def test_two_streams_at_once(dtype, keep):
+    cases = [Case(T, 256, 160, 6, 2, dtype, keep, 0.1, seed=s, pack=False) for s, T in enumerate((700, 333))]
+    want = [(c.train(), c.backward()) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [(c.outputs(), c.grads()) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, s, (out, grads) in zip(cases, streams, outs):
+            c.train(out, stream=s)
+            c.backward(grads, stream=s)
+    torch.cuda.synchronize()
+    for (w, wg), (o, og) in zip(want, outs):
+        assert all(a is b or torch.equal(a, b) for a, b in zip((*w, *wg), (*o, *og)))
+
+
 @pytest.mark.parametrize("rows,cols,ld,dtype", ROWS8)
 def test_rows8(rows, cols, ld, dtype):
     say(f"[rows8] {rows}x{cols} ld={ld} {dtype}")

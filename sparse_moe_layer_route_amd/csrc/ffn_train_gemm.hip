@@ -26,6 +26,7 @@
 
 #include "common.h"
 #include "ffn_train.h"
+#include "ffn_train_shapes.h"
 
 namespace moe {
 namespace {
@@ -615,44 +616,19 @@ template <typename S> void launch(int which, TrainArgs a, int P, hipStream_t s) 
   }
 }
 
-// The shapes and when they are taken; times in us of the launch at
-//   few:    64 tokens, H 2048, I 1408, 64 experts top-6 (6 rows an expert; forward: 8 tokens)
-//   batch:  4096 tokens, H 1536, I 512, 40 experts top-8 (819 rows)
-//   shared: 2048 tokens, H 2048, I 1408, one expert
-//   small:  1000 tokens, H 256, I 512, 8 experts top-2, fp32 (forward: 333)
-//   wide:   4096 tokens, H 2048, I 512, 32 experts top-4, fp32: all launches
-//   256x128  two blocks a CU, one's outputs beside the other's products: where
-//            its tiles fill the CUs.  batch: gate/up 149, down 78, dact 120, dx
-//            135 (256x256: 188, 92, 157, 157)
-//   256x256  one block a CU, half of the weights' traffic: dx of matrices that
-//            outgrow an XCD's L2, which are fetched again for every 128 rows
-//            (4096 tokens, H 3584, I 2560, 64 experts top-8: 1540 against 1880)
-//   128x64   few tiles: shared down 26, dact 34, dx 46 (256x128: 30, 54, 59);
-//            few gate/up 72 (88)
-//   64x64    fewer: few down 44 (128x64: 49; dact 126 with either); small down
-//            15, dx 31, dact 14, dw 27 (23, 50, 21, 32)
-// fp32 is bound by its matrix instructions, a sixteenth as fast, and takes
-// the smaller shapes throughout, whose sums can be put aside (the largest
-// batches lose by it: wide 2014, with 256x128 1691).
 void launch_any(int which, const TrainArgs& a, int P, bool is_bf16, hipStream_t s) {
-  const bool rows = which != 4, few = P < 64 * a.E;
-  const int64_t e = std::min(a.E, P), mh = (a.H + 255) / 256, mi = (a.I + 255) / 256;
-  auto row_tiles = [&](int n, int m) {   // tiles of m outputs by n rows
-    return (P / n + e) * ((which == 0 ? 2 * a.I : which == 2 ? a.I : a.H) + m - 1) / m;
-  };
-  const int64_t tiles = rows ? row_tiles(128, 256)
-                             : a.E * (2 * mh * ((a.I + 127) / 128) + mi * ((a.H + 127) / 128));
+  const train_shape shape = train_shape_of((train_launch)which, is_bf16, P, a.E, a.H, a.I);
   if (is_bf16) {
-    if (which == 3 && (int64_t)a.H * a.I >= (4 << 20) && P >= 256 * a.E)
-      go<DX, Shape<bf16, 2, 2, 8, 8>>(a, (P / 256 + e) * mh, s);
-    else if (tiles > (which == 0 ? CUS / 2 : 160) && (!rows || !few || (which == 3 && tiles >= 2 * CUS)))
+    if (shape == SHAPE_256x256)
+      go<DX, Shape<bf16, 2, 2, 8, 8>>(a, train_row_tiles(P, a.E, a.H, 256, 256), s);
+    else if (shape == SHAPE_256x128)
       launch<Shape<bf16, 2, 2, 8, 4>>(which, a, P, s);
-    else if (few && which == 1)
+    else if (shape == SHAPE_64x64)
       launch<Shape<bf16, 1, 4, 4, 1>>(which, a, P, s);
     else
       launch<Shape<bf16, 1, 4, 8, 1>>(which, a, P, s);
   } else {
-    if (which != 0 && (rows ? row_tiles(64, 128) : 2 * tiles) < 2 * CUS)
+    if (shape == SHAPE_64x64)
       launch<Shape<float, 1, 4, 4, 1>>(which, a, P, s);
     else
       launch<Shape<float, 1, 4, 8, 1>>(which, a, P, s);

@@ -43,7 +43,6 @@ enum { GATE_UP, GATE_UP8, DOWN, DACT, DACT8, DX, DW, DW_ANY };
 
 constexpr int STAGING = 2048;       // LDS of a wave's outputs: 16 rows x 64 bf16
 constexpr int NXCD = 8;
-constexpr int CUS = 256;
 
 __device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 
@@ -586,52 +585,49 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
 
 template <int MODE, typename S> void go(const TrainArgs& a, int64_t tiles, hipStream_t s) {
   // Persistent: the CUs' share, a multiple of the XCDs.
-  const int64_t g = std::min<int64_t>(tiles, S::PER_CU * CUS);
+  const int64_t g = std::min<int64_t>(tiles, S::PER_CU * kTrainCus);
   train_gemm_kernel<MODE, S><<<(unsigned)((g + NXCD - 1) / NXCD * NXCD), 256, 0, s>>>(a);
 }
 
-template <typename S> void launch(int which, TrainArgs a, int P, hipStream_t s) {
+// A launch is known when this is compiled, so that only the shapes its rule
+// can choose are.
+template <train_launch W, typename S> void launch(TrainArgs a, int P, hipStream_t s) {
   constexpr int TM = S::TM, TN = S::TN;
-  const int64_t row_tiles = P / TN + std::min(a.E, P);       // an upper bound
-  const int64_t mh = (a.H + TM - 1) / TM, mi = (a.I + TM - 1) / TM;
-  if (which == 0) {
-    if constexpr (S::MI == 8) {
-      const int64_t tiles = row_tiles * ((a.I + TM / 2 - 1) / (TM / 2));
-      if (a.keep8) go<GATE_UP8, S>(a, tiles, s);
-      else go<GATE_UP, S>(a, tiles, s);
-    }
-  } else if (which == 1) {
-    go<DOWN, S>(a, row_tiles * mh, s);
-  } else if (which == 2) {
-    if (a.keep8) go<DACT8, S>(a, row_tiles * mi, s);
-    else go<DACT, S>(a, row_tiles * mi, s);
-  } else if (which == 3) {
-    go<DX, S>(a, row_tiles * mh, s);
+  auto row_tiles = [&](int width, int m) { return train_row_tiles(P, a.E, width, TN, m); };
+  if constexpr (W == TRAIN_GATE_UP) {
+    static_assert(S::MI == 8, "a wave has 64 channels of either matrix");
+    if (a.keep8) go<GATE_UP8, S>(a, row_tiles(a.I, TM / 2), s);
+    else go<GATE_UP, S>(a, row_tiles(a.I, TM / 2), s);
+  } else if constexpr (W == TRAIN_DOWN) {
+    go<DOWN, S>(a, row_tiles(a.H, TM), s);
+  } else if constexpr (W == TRAIN_DACT) {
+    if (a.keep8) go<DACT8, S>(a, row_tiles(a.I, TM), s);
+    else go<DACT, S>(a, row_tiles(a.I, TM), s);
+  } else if constexpr (W == TRAIN_DX) {
+    go<DX, S>(a, row_tiles(a.H, TM), s);
   } else {
     a.n_dw = (a.dw[0] != nullptr) + (a.dw[1] != nullptr) + (a.dw[2] != nullptr);
     if (!a.n_dw) return;
+    const int64_t mh = (a.H + TM - 1) / TM, mi = (a.I + TM - 1) / TM;
     const int64_t tiles = a.E * a.n_dw * std::max(mh * ((a.I + TN - 1) / TN), mi * ((a.H + TN - 1) / TN));
     if (a.dw_f32 || a.accumulate) go<DW_ANY, S>(a, tiles, s);
     else if constexpr (S::SZ == 2) go<DW, S>(a, tiles, s);
   }
 }
 
-void launch_any(int which, const TrainArgs& a, int P, bool is_bf16, hipStream_t s) {
-  const train_shape shape = train_shape_of((train_launch)which, is_bf16, P, a.E, a.H, a.I);
+template <train_launch W> void launch_any(const TrainArgs& a, int P, bool is_bf16, hipStream_t s) {
+  const train_shape shape = train_shape_of(W, is_bf16, P, a.E, a.H, a.I);
   if (is_bf16) {
-    if (shape == SHAPE_256x256)
-      go<DX, Shape<bf16, 2, 2, 8, 8>>(a, train_row_tiles(P, a.E, a.H, 256, 256), s);
-    else if (shape == SHAPE_256x128)
-      launch<Shape<bf16, 2, 2, 8, 4>>(which, a, P, s);
-    else if (shape == SHAPE_64x64)
-      launch<Shape<bf16, 1, 4, 4, 1>>(which, a, P, s);
-    else
-      launch<Shape<bf16, 1, 4, 8, 1>>(which, a, P, s);
+    if constexpr (W == TRAIN_DX)
+      if (shape == SHAPE_256x256) return launch<W, Shape<bf16, 2, 2, 8, 8>>(a, P, s);
+    if constexpr (W == TRAIN_DOWN)
+      if (shape == SHAPE_64x64) return launch<W, Shape<bf16, 1, 4, 4, 1>>(a, P, s);
+    if (shape == SHAPE_256x128) return launch<W, Shape<bf16, 2, 2, 8, 4>>(a, P, s);
+    launch<W, Shape<bf16, 1, 4, 8, 1>>(a, P, s);
   } else {
-    if (shape == SHAPE_64x64)
-      launch<Shape<float, 1, 4, 4, 1>>(which, a, P, s);
-    else
-      launch<Shape<float, 1, 4, 8, 1>>(which, a, P, s);
+    if constexpr (W != TRAIN_GATE_UP)
+      if (shape == SHAPE_64x64) return launch<W, Shape<float, 1, 4, 4, 1>>(a, P, s);
+    launch<W, Shape<float, 1, 4, 8, 1>>(a, P, s);
   }
 }
 
@@ -642,17 +638,17 @@ int64_t train_ws_bytes(const moe_dims_t& d, int64_t T) {
 }
 
 hipError_t launch_ffn_train(const TrainArgs& a, int P, bool is_bf16, hipStream_t s) {
-  launch_any(0, a, P, is_bf16, s);
-  launch_any(1, a, P, is_bf16, s);
+  launch_any<TRAIN_GATE_UP>(a, P, is_bf16, s);
+  launch_any<TRAIN_DOWN>(a, P, is_bf16, s);
   return hipGetLastError();
 }
 
 hipError_t launch_ffn_backward(const TrainArgs& a, int P, bool is_bf16, hipStream_t s) {
   if (P > 0) {
-    launch_any(2, a, P, is_bf16, s);
-    if (a.dx) launch_any(3, a, P, is_bf16, s);
+    launch_any<TRAIN_DACT>(a, P, is_bf16, s);
+    if (a.dx) launch_any<TRAIN_DX>(a, P, is_bf16, s);
   }
-  launch_any(4, a, P, is_bf16, s);
+  launch_any<TRAIN_DW>(a, P, is_bf16, s);
   return hipGetLastError();
 }
 

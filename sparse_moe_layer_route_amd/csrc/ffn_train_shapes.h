@@ -31,7 +31,8 @@ inline int64_t train_row_tiles(int P, int E, int width, int n, int m) {
 //            every launch had it, gate/up 188, down 92, dact 157 (149, 78, 120)
 //   256x256  one block a CU, half of the weights' traffic: dx of matrices that
 //            outgrow an XCD's L2, which are fetched again for every 128 rows
-//            (4096 tokens, H 3584, I 2560, 64 experts top-8: 1535 against 1908)
+//            (4096 tokens, H 3584, I 2560, 64 experts top-8: 1535 against 1908).
+//            Four rounds of its tiles, or CUs stand idle: below
 //   128x64   few tiles: shared down 25, dact 32, dx 44 (256x128: 30, 53, 60);
 //            few rows: few gate/up 212, dact 66 (215, 83), with 8 tokens
 //            gate/up 131 (143)
@@ -44,6 +45,8 @@ inline int64_t train_row_tiles(int P, int E, int width, int n, int m) {
 //   dact     72-102 1.7-2.1; 128-164 1.3-1.7; 192-240 1.15-1.4; 258-294 0.9-1.2; 386-528 0.7-1.0
 //   dx       72-98 1.4-1.6; 128-164 1.1-1.4; 192-196 0.9-1.15; 258-288 0.7-1.0
 //   dw       96 1.2; 192 1.1-1.2; 272 0.6-0.7; 384 0.7-0.8
+//   dx of H I >= 2^22, 256x256 over the better of both, by its own tiles: 8-48 2.3-2.4; 64-144 1.25-2.0;
+//            160-272 0.9-1.05; 288-384 1.05-1.5; 462-910 0.8-1.2; 1008-1280 0.8-1.05; 2688 0.8
 //   dx of few rows  268-320 1.2; 416 1.1; 520-536 0.9; 832-1312 0.9-1.0
 // and fp32's 128x64 over 64x64 by the tiles of the former:
 //   down, dact, dx  130-320 1.0-1.5; 514-576 0.95-1.2; 1028-1152 0.9-1.15
@@ -63,7 +66,9 @@ inline train_shape train_shape_of(train_launch which, bool is_bf16, int P, int E
     const bool fills = rows ? train_row_tiles(P, E, width, 64, 128) >= 3 * kTrainCus : 2 * tiles >= 2 * kTrainCus;
     return fills ? SHAPE_128x64 : SHAPE_64x64;
   }
-  if (which == TRAIN_DX && (int64_t)H * I >= (4 << 20) && P >= 256 * E) return SHAPE_256x256;
+  if (which == TRAIN_DX && (int64_t)H * I >= (4 << 20) && P >= 256 * E &&
+      train_row_tiles(P, E, H, 256, 256) >= 4 * kTrainCus)
+    return SHAPE_256x256;
   if (rows && few) {
     if (which == TRAIN_DX && tiles >= 2 * kTrainCus) return SHAPE_256x128;
     return which == TRAIN_DOWN ? SHAPE_64x64 : SHAPE_128x64;

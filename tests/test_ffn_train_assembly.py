@@ -47,6 +47,7 @@ def test_every_kernel_is_one_that_a_call_reaches(kernels, ask):  # noqa: F811
     size = lambda most: int(2 ** rng.uniform(0, most))  # noqa: E731
     for _ in range(4000):
         queries.append(("shape", rng.randrange(5), rng.randrange(2), size(17), size(6.02), 64 * size(6), 16 * size(8)))
+    queries.append(("shape", DX, 1, 32768, 64, 3584, 2560))
     reached = set()
     for (_, which, bf16, *_sizes), s in zip(queries, ask(queries)):
         ty = "bf16" if bf16 else "f32"

@@ -84,6 +84,13 @@ def test_narrow_outputs_are_not_counted_twice(ask):
     assert shape(ask, DOWN, "bf16", 128 * 170, 1, 64, 512) == "128x64"
 
 
+def test_few_tiles_take_no_blocks_that_fill_a_cu(ask):
+    """A shared expert's dx, 256 to 4096 rows: 16 to 136 tiles of 256x256 for 256 CUs."""
+    for rows in (256, 1024):
+        assert shape(ask, DX, "bf16", rows, 1, 2048, 2048) == "128x64"
+    assert shape(ask, DX, "bf16", 4096, 1, 2048, 2048) == "256x128"
+
+
 def test_both_sides_of_each_crossing(ask):
     # tiles of 256x128: rows / 128 + 1 for one expert, times the tiles across
     for which, H, I, last in ((DOWN, 256, 512, 192), (DX, 256, 512, 192), (DACT, 512, 256, 192),
@@ -92,10 +99,12 @@ def test_both_sides_of_each_crossing(ask):
         assert shape(ask, which, "bf16", last * 128, 1, H, I) == "256x128"
     for E, want in ((16, "128x64"), (17, "256x128")):              # 12 tiles of dW an expert
         assert shape(ask, DW, "bf16", 4096, E, 256, 512) == want
-    # dx of matrices past an XCD's L2, 256 rows an expert and more
-    assert shape(ask, DX, "bf16", 256 * 4, 4, 2048, 2048) == "256x256"
-    assert shape(ask, DX, "bf16", 256 * 4 - 1, 4, 2048, 2048) != "256x256"
-    assert shape(ask, DX, "bf16", 256 * 4, 4, 2048, 2032) != "256x256"
+    # dx of matrices past an XCD's L2: 256 rows an expert and four rounds of tiles
+    assert shape(ask, DX, "bf16", 256 * 124, 4, 2048, 2048) == "256x256"          # 128 by 8
+    assert shape(ask, DX, "bf16", 256 * 124 - 1, 4, 2048, 2048) == "256x128"
+    assert shape(ask, DX, "bf16", 256 * 124, 4, 2048, 2032) == "256x128"
+    assert shape(ask, DX, "bf16", 256 * 64, 64, 4096, 2048) == "256x256"
+    assert shape(ask, DX, "bf16", 256 * 64 - 1, 64, 4096, 2048) == "256x128"
     # few rows an expert
     assert shape(ask, DOWN, "bf16", 64 * 8 - 1, 8, 2048, 512) == "64x64"
     assert shape(ask, DOWN, "bf16", 64 * 8, 8, 2048, 512) == "128x64"

@@ -18,6 +18,8 @@ CASES = [  # T, H, I, E, k, dtype, keep, missing
     (24576, 256, 272, 1, 1, "bf16", "int8", 0.0),      # 193: down and dx by 256 x 128
     (64, 2048, 48, 64, 6, "bf16", "rows", 0.1),        # dx of few rows by 256 x 128
     (63, 2048, 48, 64, 4, "bf16", "int8", 0.1),        # and by 128 x 64
+    (4000, 8192, 528, 2, 2, "bf16", "rows", 0.1),      # dx by 256 x 256
+    (9001, 8256, 512, 1, 1, "bf16", "int8", 0.0),      # the same with ragged ends
     (1500, 128, 2064, 6, 2, "f32", "rows", 0.1),       # fp32 dact and dw by 128 x 64
     (1500, 2112, 144, 6, 2, "f32", "int8", 0.1),       # fp32 down and dx
 ]
